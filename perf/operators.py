@@ -187,7 +187,7 @@ def _pack8(x, group):
     m, k = x.shape
     v = x.float().view(m, k // group, group)
     top = v.abs().amax(-1, keepdim=True)
-    step = (((top / 127.0).view(torch.int32) + 0xFFFF) & -0x10000).view(torch.float32)
+    step = (((top.double() / 127.0).float().view(torch.int32) + 0xFFFF) & -0x10000).view(torch.float32)
     step = torch.where(torch.isfinite(top), step, float("nan"))
     codes = torch.where(step > 0, torch.round(v / step), 0.0).clamp(-127, 127).to(torch.int8)
     return codes.view(m, k), step.to(torch.bfloat16).view(m, k // group)
