@@ -321,6 +321,94 @@ ANY4_API int any4_pack_format(int format, const uint8_t* idx_nib, const uint16_t
                               const uint16_t* beta, int n, int k, int group, void* packed,
                               size_t packed_bytes, any4_stream_t stream);
 
+/*
+ * Low-rank adapters beside a shared any4 weight. The source pages have no
+ * counterpart; a user serves many fine-tunes of one model from one quantized
+ * weight this way, and trains them on top of it.
+ *
+ * L adapters of rank R belong to one projection:
+ *   a      [L][R][K] bf16,  b  [L][N][R] bf16,  scale [L] fp32, on the device;
+ *   ids    [M] int32, the adapter of each token, in any order. A token whose
+ *          id is outside [0, L) has no adapter. NULL: adapter 0 for all.
+ * 1 <= L <= 65536; R a multiple of 8, 8 <= R <= 128 (adapters of a lower rank
+ * are padded with zero rows of A and zero columns of B); everything else as
+ * for any4_linear_bits (bits 2, 3 or 4).
+ *
+ * any4_linear_lora - y[t] = x[t] . W_hat^T + u[t] . B_l^T with
+ * u[t] = s_l (x[t] . A_l^T) and l = ids[t]; u[t] = 0 without an adapter.
+ *
+ *   x, packed, y   as for any4_linear_bits; a and b 16-byte aligned.
+ *   u          [M][R] bf16 output, 16-byte aligned, or NULL: what a training
+ *              step keeps for any4_linear_lora_grad.
+ *   workspace  >= any4_lora_workspace_bytes(...) bytes, 16-byte aligned, with
+ *              any4_linear's contract: its first any4_lora_header_bytes()
+ *              bytes zero before the first use, left zero by every call that
+ *              completes; calls that may overlap need separate ones. It may be
+ *              the workspace of any call of this header, if large enough. The
+ *              32-bit status word is any4_linear's (byte offset 65536*4).
+ *
+ * u is held in more than bf16 on its way into y (fp32, or a bf16 pair of its
+ * leading and trailing part) and y is rounded once from its fp32 sum.
+ * Results do not depend on how ids order the tokens, and repeat bit for bit.
+ */
+ANY4_API size_t any4_lora_header_bytes(void);
+ANY4_API size_t any4_lora_workspace_bytes(int bits, int m, int n, int k, int group, int adapters, int rank);
+ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, int m, int n, int k, int group,
+                              const uint16_t* a, const uint16_t* b, const float* scale, const int32_t* ids,
+                              int adapters, int rank, uint16_t* y, uint16_t* u, void* workspace,
+                              size_t workspace_bytes, any4_stream_t stream);
+
+/*
+ * any4_linear_lora_grad - the gradients of any4_linear_lora for a frozen
+ * weight. With v[t] = s_l (dy[t] . B_l), zero for tokens without an adapter:
+ *
+ *   dx     [M][K] bf16:     dx[t] = dy[t] . W_hat + v[t] . A_l
+ *   da     [L][R][K] bf16:  dA_l = sum over the tokens of l of v[t]^T x[t]
+ *   db     [L][N][R] bf16:  dB_l = sum over the tokens of l of dy[t]^T u[t]
+ *
+ * Each output may be NULL (at least one is not), 16-byte aligned. da and db
+ * are overwritten, with zeros for adapters without tokens.
+ *
+ *   dy         [M][N] bf16, 16-byte aligned.
+ *   x          the forward's input (needed for da), one of two forms: bf16
+ *              [M][K] (x_codes and x_steps NULL), or x NULL and an 8-bit
+ *              checkpoint of any4_act_pack with groups of x_group columns.
+ *              With a checkpoint, da is that of its any4_act_unpack values.
+ *   u          [M][R] bf16 as any4_linear_lora wrote it (needed for db).
+ *   packed, a  needed for dx; b for dx and da.
+ *   workspace  >= any4_lora_grad_workspace_bytes(...), as for any4_linear_lora.
+ *              It holds W_hat in bf16 (N*K*2 bytes) while dx is computed.
+ * Sums are fp32 in a fixed order: repeated calls give the same bits.
+ */
+ANY4_API size_t any4_lora_grad_workspace_bytes(int bits, int m, int n, int k, int group, int adapters, int rank);
+ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t* x, const int8_t* x_codes,
+                                   const uint16_t* x_steps, int x_group, const uint16_t* u, const void* packed, int m,
+                                   int n, int k, int group, const uint16_t* a, const uint16_t* b, const float* scale,
+                                   const int32_t* ids, int adapters, int rank, uint16_t* dx, uint16_t* da,
+                                   uint16_t* db, void* workspace, size_t workspace_bytes, any4_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits: a layer's input kept from its forward to
+ * its backward pass as one signed byte per value and one bf16 step per token
+ * and group of G columns (G in {64, 128, 256, 512, 1024}, K % G == 0,
+ * 1 <= M <= 2^20, K <= 2^20):
+ *
+ *   step = max |x| of the group / 127, rounded up to bf16
+ *   code = x / step rounded half to even, -127 .. 127
+ *   value = code * step, rounded once to bf16
+ *
+ * |value - x| <= step / 2 before that rounding. A group of zeros has step 0
+ * and zero codes; a group with an infinity or a NaN has step NaN and zero
+ * codes, and reads back as NaN.
+ *
+ *   x      [M][K] bf16; codes [M][K]; both 16-byte aligned.
+ *   steps  [M][K/G] bf16.
+ */
+ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* codes, uint16_t* steps,
+                           any4_stream_t stream);
+ANY4_API int any4_act_unpack(const int8_t* codes, const uint16_t* steps, int m, int k, int group, uint16_t* x,
+                             any4_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 ANY4_API const char* any4_strerror(int status);
 

@@ -59,6 +59,22 @@ lib.any4_dequant_bits.argtypes = [_c_int, _p, _c_int, _c_int, _c_int, _p, _p]
 lib.any4_dequant_bits.restype = _c_int
 lib.any4_linear_bits.argtypes = [_c_int, _p, _p, _c_int, _c_int, _c_int, _c_int, _p, _p, _c_size, _p]
 lib.any4_linear_bits.restype = _c_int
+lib.any4_lora_header_bytes.argtypes = []
+lib.any4_lora_header_bytes.restype = _c_size
+lib.any4_lora_workspace_bytes.argtypes = [_c_int] * 7
+lib.any4_lora_workspace_bytes.restype = _c_size
+lib.any4_linear_lora.argtypes = [_c_int, _p, _p, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p, _c_int, _c_int,
+                                 _p, _p, _p, _c_size, _p]
+lib.any4_linear_lora.restype = _c_int
+lib.any4_lora_grad_workspace_bytes.argtypes = [_c_int] * 7
+lib.any4_lora_grad_workspace_bytes.restype = _c_size
+lib.any4_linear_lora_grad.argtypes = [_c_int, _p, _p, _p, _p, _c_int, _p, _p, _c_int, _c_int, _c_int, _c_int,
+                                      _p, _p, _p, _p, _c_int, _c_int, _p, _p, _p, _p, _c_size, _p]
+lib.any4_linear_lora_grad.restype = _c_int
+lib.any4_act_pack.argtypes = [_p, _c_int, _c_int, _c_int, _p, _p, _p]
+lib.any4_act_pack.restype = _c_int
+lib.any4_act_unpack.argtypes = [_p, _p, _c_int, _c_int, _c_int, _p, _p]
+lib.any4_act_unpack.restype = _c_int
 lib.any4_strerror.argtypes = [_c_int]
 lib.any4_strerror.restype = ctypes.c_char_p
 lib.any4_last_cuda_error.argtypes = []
@@ -68,7 +84,9 @@ EXPORTED = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_linear_works
             "any4_linear_workspace_bytes_bits", "any4_linear_grid", "any4_linear_kernel",
             "any4_linear", "any4_linear_noalloc", "any4_noalloc_status_word", "any4_quantize", "any4_format_lut",
             "any4_pack_format", "any4_packed_bytes_bits", "any4_pack_bits", "any4_dequant_bits",
-            "any4_linear_bits", "any4_strerror", "any4_last_cuda_error")
+            "any4_linear_bits", "any4_lora_header_bytes", "any4_lora_workspace_bytes", "any4_linear_lora",
+            "any4_lora_grad_workspace_bytes", "any4_linear_lora_grad", "any4_act_pack", "any4_act_unpack",
+            "any4_strerror", "any4_last_cuda_error")
 
 ANY4_FORMAT_INT4, ANY4_FORMAT_NF4, ANY4_FORMAT_FP4 = 1, 2, 3
 FORMATS = {"int4": ANY4_FORMAT_INT4, "nf4": ANY4_FORMAT_NF4, "fp4": ANY4_FORMAT_FP4}
@@ -337,6 +355,203 @@ def any4_pack_format(fmt, idx_nib: torch.Tensor, alpha: torch.Tensor, beta: torc
                                 _dev(beta, "beta", 2, (n, k // group)), n, k, group,
                                 _dev(packed, "packed", 1), packed.numel(), _stream(dev)))
     return packed
+
+
+# ---- low-rank adapters and 8-bit activation checkpoints
+
+def _typed(t: torch.Tensor, name: str, dtypes, device: torch.device, shape) -> int:
+    """Pointer of a contiguous CUDA tensor of one of ``dtypes`` on ``device``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values, or their bit patterns
+_BYTES = (torch.uint8,)
+_LORA_WORKSPACES: dict = {}
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-dimensional CUDA tensor")
+    return t.shape[0]
+
+
+def _adapter_workspace(need: int, device: torch.device) -> torch.Tensor:
+    """A workspace with a zeroed header: kept per stream and grown on demand,
+    or, while a CUDA graph is captured, one of the graph's own."""
+    header = lib.any4_lora_header_bytes()
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws[:header].zero_()
+        return ws
+    key = (device.index, _stream(device))
+    ws = _LORA_WORKSPACES.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws[:header].zero_()
+        _LORA_WORKSPACES[key] = ws
+    return ws
+
+
+def _adapters(a, b, scale, ids, m: int, n: int, k: int, device: torch.device):
+    """Checked adapter arguments: pointers of a, b, scale, ids, then L and R."""
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError("a must be a tensor of shape (adapters, rank, K)")
+    count, rank = a.shape[0], a.shape[1]
+    return (_typed(a, "a", _BF16, device, (count, rank, k)), _typed(b, "b", _BF16, device, (count, n, rank)),
+            _typed(scale, "scale", (torch.float32,), device, (count,)),
+            None if ids is None else _typed(ids, "ids", (torch.int32,), device, (m,)), count, rank)
+
+
+def _weight(packed, n: int, k: int, group: int, bits: int, device: torch.device) -> int:
+    """Pointer of a packed weight that is large enough for its shape."""
+    if not isinstance(packed, torch.Tensor):
+        raise ValueError("packed must be a CUDA tensor")
+    need = lib.any4_packed_bytes_bits(bits, n, k, group)
+    if need == 0:
+        raise Any4Error(ANY4_ESHAPE)
+    if packed.numel() < need:
+        raise Any4Error(ANY4_EWORKSPACE)
+    return _typed(packed, "packed", _BYTES, device, packed.shape)
+
+
+def any4_lora_workspace_bytes(m: int, n: int, k: int, group: int, adapters: int, rank: int, bits: int = 4) -> int:
+    return lib.any4_lora_workspace_bytes(bits, m, n, k, group, adapters, rank)
+
+
+def any4_lora_grad_workspace_bytes(m: int, n: int, k: int, group: int, adapters: int, rank: int,
+                                   bits: int = 4) -> int:
+    return lib.any4_lora_grad_workspace_bytes(bits, m, n, k, group, adapters, rank)
+
+
+def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, group: int, a: torch.Tensor,
+                     b: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor | None = None, bits: int = 4,
+                     out: torch.Tensor | None = None, u: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = x[t] . W_hat^T + u[t] . B_l^T with u[t] = scale[l] (x[t] . A_l^T)
+    and l = ids[t]: the any4 linear layer with one of L low-rank adapters per
+    token (a: L x R x K, b: L x N x R bf16, scale: L fp32, ids: M int32; ids
+    outside [0, L) have no adapter, None is adapter 0 for every token).
+    ``u`` (M x R bf16) is written where given, for any4_linear_lora_grad."""
+    m = _rows(x, "x")
+    dev = x.device
+    with torch.cuda.device(dev):
+        ad = _adapters(a, b, scale, ids, m, n, k, dev)
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            need = lib.any4_lora_workspace_bytes(bits, m, n, k, group, ad[4], ad[5])
+            if need == 0:
+                raise Any4Error(ANY4_ESHAPE)
+            workspace = _adapter_workspace(need, dev)
+        _check(lib.any4_linear_lora(
+            bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k,
+            group, *ad, _typed(out, "out", _BF16, dev, (m, n)),
+            None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5])),
+            _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), _stream(dev)))
+    return out
+
+
+def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: torch.Tensor | None, n: int, k: int,
+                          group: int, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
+                          ids: torch.Tensor | None = None, bits: int = 4,
+                          outputs: tuple = ("dx", "da", "db"), dx: torch.Tensor | None = None,
+                          da: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None) -> tuple:
+    """(dx, da, db) of any4_linear_lora for dy (M x N bf16); None for those
+    not named in ``outputs``. ``x`` is the forward's bf16 input or the
+    (codes, steps) pair any4_act_pack made of it (needed for da), ``u`` what
+    the forward wrote (needed for db), ``packed`` the weight (for dx)."""
+    m = _rows(dy, "dy")
+    dev = dy.device
+    unknown = set(outputs) - {"dx", "da", "db"}
+    if unknown or not outputs:
+        raise ValueError(f"outputs must name some of dx, da and db, got {tuple(outputs)}")
+    with torch.cuda.device(dev):
+        ad = _adapters(a, b, scale, ids, m, n, k, dev)
+        count, rank = ad[4], ad[5]
+
+        def made(name, t, shape):
+            if name not in outputs:
+                if t is not None:
+                    raise ValueError(f"{name} was given but is not among the outputs")
+                return None, None
+            if t is None:
+                t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            return t, _typed(t, name, _BF16, dev, shape)
+
+        dx, dx_p = made("dx", dx, (m, k))
+        da, da_p = made("da", da, (count, rank, k))
+        db, db_p = made("db", db, (count, n, rank))
+        x_p = codes_p = steps_p = None
+        x_group = 0
+        if da is not None:
+            if isinstance(x, (tuple, list)):
+                codes, steps = x
+                groups = steps.shape[1] if isinstance(steps, torch.Tensor) and steps.dim() == 2 else 0
+                if groups < 1 or k % groups:
+                    raise ValueError("steps must be a tensor of shape (M, K / group)")
+                x_group = k // groups
+                codes_p = _typed(codes, "codes", (torch.int8,), dev, (m, k))
+                steps_p = _typed(steps, "steps", _BF16, dev, (m, groups))
+            else:
+                x_p = _typed(x, "x", _BF16, dev, (m, k))
+        u_p = _typed(u, "u", _BF16, dev, (m, rank)) if db is not None else None
+        w_p = _weight(packed, n, k, group, bits, dev) if dx is not None else None
+        if workspace is None:
+            need = lib.any4_lora_grad_workspace_bytes(bits, m, n, k, group, count, rank)
+            if need == 0:
+                raise Any4Error(ANY4_ESHAPE)
+            workspace = _adapter_workspace(need, dev)
+        _check(lib.any4_linear_lora_grad(
+            bits, _typed(dy, "dy", _BF16, dev, (m, n)), x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad,
+            dx_p, da_p, db_p, _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
+            _stream(dev)))
+    return dx, da, db
+
+
+def any4_act_pack(x: torch.Tensor, group: int, codes: torch.Tensor | None = None,
+                  steps: torch.Tensor | None = None) -> tuple:
+    """8-bit checkpoint of an activation x (M x K bf16): (codes, steps), one
+    int8 per value and one bf16 step per token and ``group`` columns."""
+    m = _rows(x, "x")
+    k, dev = x.shape[1], x.device
+    if group < 1 or k % group:
+        raise Any4Error(ANY4_ESHAPE)
+    with torch.cuda.device(dev):
+        if codes is None:
+            codes = torch.empty((m, k), dtype=torch.int8, device=dev)
+        if steps is None:
+            steps = torch.empty((m, k // group), dtype=torch.bfloat16, device=dev)
+        _check(lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group,
+                                 _typed(codes, "codes", (torch.int8,), dev, (m, k)),
+                                 _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev)))
+    return codes, steps
+
+
+def any4_act_unpack(codes: torch.Tensor, steps: torch.Tensor, group: int,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bf16 values (M x K) an 8-bit checkpoint stands for."""
+    m = _rows(codes, "codes")
+    k, dev = codes.shape[1], codes.device
+    if group < 1 or k % group:
+        raise Any4Error(ANY4_ESHAPE)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+        _check(lib.any4_act_unpack(_typed(codes, "codes", (torch.int8,), dev, (m, k)),
+                                   _typed(steps, "steps", _BF16, dev, (m, k // group)), m, k, group,
+                                   _typed(out, "out", _BF16, dev, (m, k)), _stream(dev)))
+    return out
 
 
 def any4_strerror(status: int) -> str:

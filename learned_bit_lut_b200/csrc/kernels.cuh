@@ -75,17 +75,19 @@ LinearPlan plan_linear(int m, const Layout& L, int num_sms);
 int regt_warps(int m);
 int regt_max_cluster();
 cudaError_t launch_linear_regt(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                               void* workspace, int cluster, cudaStream_t stream);
+                               void* workspace, int cluster, cudaStream_t stream, const float* delta);
 
 // M <= 16, any4, few chunks per thread block: the row-pair tables in shared
 // memory, one cluster of `cluster` blocks per panel (linear_small.cu).
 int small_warps(int m);
 int small_max_cluster();
 cudaError_t launch_linear_small(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                                void* workspace, int cluster, cudaStream_t stream);
+                                void* workspace, int cluster, cudaStream_t stream, const float* delta);
 
+// delta (M <= 16): an fp32 [M][N] term added to each sum before its one
+// rounding to bf16, or null.
 cudaError_t launch_linear(const uint16_t* x, const uint8_t* packed, const Layout& L, int m,
                           uint16_t* y, void* workspace, const LinearPlan& plan,
-                          cudaStream_t stream);
+                          cudaStream_t stream, const float* delta = nullptr);
 
 }  // namespace any4

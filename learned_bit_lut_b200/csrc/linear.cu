@@ -114,6 +114,7 @@ struct Params {
   const uint16_t* x;
   const uint8_t* packed;
   uint16_t* y;
+  const float* delta;                       // [M][N] added to the sums before their rounding, or null
   float* partials;
   unsigned* counters;
   unsigned* status;
@@ -242,6 +243,7 @@ __device__ __forceinline__ void store_out(const Params& p, int P, int o, float v
   out_pos<MODE>(o / NF, o % NF, token, row);
   const int n = P * kPanelRows + row;
   if (token < p.m && n < p.n) {
+    if (p.delta != nullptr) v += __ldcg(p.delta + (size_t)token * p.n + n);
     const __nv_bfloat16 hv = __float2bfloat16_rn(v);
     p.y[(size_t)token * p.n + n] = *reinterpret_cast<const uint16_t*>(&hv);
   }
@@ -944,16 +946,17 @@ LinearPlan plan_linear(int m, const Layout& L, int num_sms) {
 
 cudaError_t launch_linear(const uint16_t* x, const uint8_t* packed, const Layout& L, int m,
                           uint16_t* y, void* workspace, const LinearPlan& plan,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, const float* delta) {
   if (plan.mode == 3) return launch_prefill(x, packed, L, m, y, workspace, plan.ctas, stream);
-  if (plan.regt) return launch_linear_regt(x, packed, L, m, y, workspace, plan.cluster, stream);
-  if (plan.small) return launch_linear_small(x, packed, L, m, y, workspace, plan.cluster, stream);
+  if (plan.regt) return launch_linear_regt(x, packed, L, m, y, workspace, plan.cluster, stream, delta);
+  if (plan.small) return launch_linear_small(x, packed, L, m, y, workspace, plan.cluster, stream, delta);
   cudaError_t e = allow_large_smem();
   if (e != cudaSuccess) return e;
   Params p{};
   p.x = x;
   p.packed = packed;
   p.y = y;
+  p.delta = delta;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   p.counters = reinterpret_cast<unsigned*>(ws);
   p.status = reinterpret_cast<unsigned*>(ws + kCountersBytes);

@@ -51,6 +51,7 @@ struct RegtParams {
   const uint16_t* x;
   const uint8_t* packed;
   uint16_t* y;
+  const float* delta;   // [M][N] added to the sums before their rounding, or null
   unsigned* status;
   int m, n, k;
   int kc, groups, g_shift;
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(
         const int row = P * kPanelRows + 16 * u + g + 8 * (q >> 1);
         const int tok = 8 * h + 2 * t + (q & 1);
         if (row < p.n && tok < p.m) {
+          if (p.delta != nullptr) v[u][h][q] += __ldcg(p.delta + (size_t)tok * p.n + row);
           const __nv_bfloat16 hv = __float2bfloat16_rn(v[u][h][q]);
           p.y[(size_t)tok * p.n + row] = *reinterpret_cast<const uint16_t*>(&hv);
         }
@@ -256,7 +258,8 @@ int regt_warps(int m) { return m <= 8 ? RegtCfg<1>::kWarps : RegtCfg<2>::kWarps;
 int regt_max_cluster() { return kRegtMaxCluster; }
 
 cudaError_t launch_linear_regt(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                               void* workspace, int cluster, cudaStream_t stream) {
+                               void* workspace, int cluster, cudaStream_t stream,
+                                const float* delta) {
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -272,6 +275,7 @@ cudaError_t launch_linear_regt(const uint16_t* x, const uint8_t* packed, const L
   p.x = x;
   p.packed = packed;
   p.y = y;
+  p.delta = delta;
   p.status = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(workspace) + kCountersBytes);
   p.m = m; p.n = L.n; p.k = L.k;
   p.kc = L.kchunks; p.groups = L.groups;

@@ -52,6 +52,7 @@ struct SmallParams {
   const uint16_t* x;
   const uint8_t* packed;
   uint16_t* y;
+  const float* delta;   // [M][N] added to the sums before their rounding, or null
   unsigned* status;
   int m, n, k;
   int kc, groups, g_shift;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kern
     }
     const int nrow = P * kPanelRows + row;
     if (token < p.m && nrow < p.n) {
+      if (p.delta != nullptr) v[i] += __ldcg(p.delta + (size_t)token * p.n + nrow);
       const __nv_bfloat16 hv = __float2bfloat16_rn(v[i]);
       p.y[(size_t)token * p.n + nrow] = *reinterpret_cast<const uint16_t*>(&hv);
     }
@@ -335,7 +337,8 @@ int small_warps(int m) { return m <= 4 ? SmallCfg<0>::kNW : m <= 8 ? SmallCfg<1>
 int small_max_cluster() { return kSmallMaxCluster; }
 
 cudaError_t launch_linear_small(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                                void* workspace, int cluster, cudaStream_t stream) {
+                                void* workspace, int cluster, cudaStream_t stream,
+                                const float* delta) {
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -352,6 +355,7 @@ cudaError_t launch_linear_small(const uint16_t* x, const uint8_t* packed, const 
   p.x = x;
   p.packed = packed;
   p.y = y;
+  p.delta = delta;
   p.status = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(workspace) + kCountersBytes);
   p.m = m; p.n = L.n; p.k = L.k;
   p.kc = L.kchunks; p.groups = L.groups;
