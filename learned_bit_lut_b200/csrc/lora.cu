@@ -16,7 +16,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <initializer_list>
 
 #include "../../include/any4.h"
 #include "kernels.cuh"
@@ -117,24 +116,29 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, cudaStream_
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Tokens go through the decode kernels 16 at a time.
-constexpr int kSlice = 16;
-
-// The workspace: any4_linear's own for a slice, then u in fp32, then the fp32 term.
+// The workspace: any4_linear's own, then for M <= 16 the inner values u in
+// fp32 and the fp32 term, else u as a bf16 pair, the adapters of each token
+// tile and the partial sums of u.
 struct LoraSpace {
-  size_t u32, delta, total;
+  size_t u32, delta, pairs, lists, partials, total;
 };
-LoraSpace lora_space(const Layout& L, int m, int rank, int sms) {
-  LoraSpace s;
-  size_t lin = 0;
-  for (int t : {1, 4, 5, 8, 9, kSlice}) {   // a last slice may be of any size
-    const size_t w = plan_linear(t, L, sms).workspace_bytes;
-    if (w > lin) lin = w;
+LoraSpace lora_space(const LinearPlan& plan, int m, int n, int k, int rank, int sms) {
+  LoraSpace s{};
+  size_t at = align_up(plan.workspace_bytes, kAlign);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, kAlign);
+    return here;
+  };
+  if (plan.mode != 3) {
+    s.u32 = take((size_t)m * rank * sizeof(float));
+    s.delta = take((size_t)m * n * sizeof(float));
+  } else {
+    s.pairs = take(pairs_bytes(m, rank));
+    s.lists = take(slot_lists_bytes(m));
+    s.partials = take(down_partials_bytes(m, k, rank, sms));
   }
-  const int slice = m < kSlice ? m : kSlice;
-  s.u32 = align_up(lin, kAlign);
-  s.delta = s.u32 + align_up((size_t)slice * rank * sizeof(float), kAlign);
-  s.total = s.delta + align_up((size_t)slice * L.n * sizeof(float), kAlign);
+  s.total = at;
   return s;
 }
 
@@ -158,7 +162,7 @@ ANY4_API size_t any4_lora_workspace_bytes(int bits, int m, int n, int k, int gro
     any4::record_cuda_error(e);
     return 0;
   }
-  return any4::lora_space(any4::make_layout(n, k, group, bits), m, rank, sms).total;
+  return any4::lora_space(any4::plan_linear(m, any4::make_layout(n, k, group, bits), sms), m, n, k, rank, sms).total;
 }
 
 ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, int m, int n, int k, int group,
@@ -171,27 +175,38 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
   if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) ||
       !aligned(ids, 4) || !aligned(y, 4) || !aligned(u, 16) || !aligned(workspace, 16))
     return ANY4_EALIGN;
+  if (workspace_bytes < kHeaderBytes) return ANY4_EWORKSPACE;
   int sms = 0;
   cudaError_t e = cached_sm_count(&sms);
   if (e != cudaSuccess) return record_cuda_error(e);
   const Layout L = make_layout(n, k, group, bits);
-  const LoraSpace space = lora_space(L, m, rank, sms);
+  const LinearPlan plan = plan_linear(m, L, sms);
+  const LoraSpace space = lora_space(plan, m, n, k, rank, sms);
   if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
+  const Adapters ad = {a, b, scale, ids, adapters, rank};
+  const uint8_t* w = static_cast<const uint8_t*>(packed);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  float* u32 = reinterpret_cast<float*>(ws + space.u32);
-  float* delta = reinterpret_cast<float*>(ws + space.delta);
   const cudaStream_t st = (cudaStream_t)stream;
-  for (int t0 = 0; e == cudaSuccess && t0 < m; t0 += kSlice) {
-    const int ms = m - t0 < kSlice ? m - t0 : kSlice;
-    const uint16_t* xs = x + (size_t)t0 * k;
-    uint16_t* us = u == nullptr ? nullptr : u + (size_t)t0 * rank;
-    const Adapters ad = {a, b, scale, ids == nullptr ? nullptr : ids + t0, adapters, rank};
-    const dim3 up((unsigned)ms, (unsigned)((n + kUpThreads - 1) / kUpThreads));
-    e = launch_pdl(adapter_down_kernel, dim3((unsigned)ms, (unsigned)rank), kDownThreads, st, xs, ad, k, u32, us);
+  if (plan.mode != 3) {
+    float* u32 = reinterpret_cast<float*>(ws + space.u32);
+    float* delta = reinterpret_cast<float*>(ws + space.delta);
+    const dim3 up((unsigned)m, (unsigned)((n + kUpThreads - 1) / kUpThreads));
+    e = launch_pdl(adapter_down_kernel, dim3((unsigned)m, (unsigned)rank), kDownThreads, st, x, ad, k, u32, u);
     if (e == cudaSuccess) e = launch_pdl(adapter_up_kernel, up, kUpThreads, st, ad, n, (const float*)u32, delta);
+    if (e == cudaSuccess) e = launch_linear(x, w, L, m, y, workspace, plan, st, delta);
+  } else {
+    AdapterTerm term{};
+    term.ad = ad;
+    uint16_t* pairs = reinterpret_cast<uint16_t*>(ws + space.pairs);
+    term.pairs = pairs;
+    if (ids != nullptr) {
+      for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
+      e = launch_slot_lists(ad, m, ws + space.lists, st);
+    }
     if (e == cudaSuccess)
-      e = launch_linear(xs, static_cast<const uint8_t*>(packed), L, ms, y + (size_t)t0 * n, workspace,
-                        plan_linear(ms, L, sms), st, delta);
+      e = launch_down(false, x, ad, term.lists[1], m, n, k, pairs, u, reinterpret_cast<float*>(ws + space.partials),
+                      reinterpret_cast<unsigned*>(ws), reinterpret_cast<unsigned*>(ws + kCountersBytes), sms, st);
+    if (e == cudaSuccess) e = launch_prefill_lora(x, w, L, m, y, workspace, sms, term, st);
   }
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);
 }

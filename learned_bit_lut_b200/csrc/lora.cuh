@@ -32,4 +32,63 @@ __device__ __forceinline__ int adapter_of(const Adapters& ad, int token) {
   return l >= 0 && l < ad.count ? l : -1;
 }
 
+// The adapters present in each tile of 64, 128 or 256 tokens, in order of
+// their first token: slots[tile * tokens + j], j < counts[tile] & kSlotCount,
+// with kSlotMixed set where the tile's tokens do not all have the same
+// adapter. Without lists (no ids) every tile has adapter 0 alone.
+constexpr int kSlotCount = 0xFFFF;
+constexpr int kSlotMixed = 1 << 30;
+struct SlotLists {
+  const int* slots;
+  const int* counts;
+  int tokens;
+};
+__device__ __forceinline__ int slot_count(const SlotLists& s, int tile, bool& mixed) {
+  if (s.slots == nullptr) {
+    mixed = false;
+    return 1;
+  }
+  const int c = __ldcg(s.counts + tile);
+  mixed = (c & kSlotMixed) != 0;
+  return c & kSlotCount;
+}
+__device__ __forceinline__ int slot_at(const SlotLists& s, int tile, int j) {
+  return s.slots == nullptr ? 0 : __ldcg(s.slots + (size_t)tile * s.tokens + j);
+}
+
+constexpr int kListTile = 256;   // the lists are built 256 tokens at a time
+size_t slot_lists_bytes(int m);
+SlotLists slot_lists(void* space, int m, int tokens);   // tokens: 64, 128 or 256
+cudaError_t launch_slot_lists(const Adapters& ad, int m, void* space, cudaStream_t stream);
+
+// The adapters' inner values of every token, z[t] = s_l in[t] . M_l with
+// M_l = A_l^T (forward: in = x, u) or B_l (backward: in = dy, v), zeros
+// without an adapter, as a bf16 pair: row t of `pairs` is [leading part, R16
+// values][trailing part, R16 values], R16 = R rounded up to 16, whose sum is z
+// to 2^-16; `rounded` (or null) gets z in bf16, R values a row.
+inline int rank16(int rank) { return (rank + 15) / 16 * 16; }
+inline size_t pairs_bytes(int m, int rank) { return (size_t)m * rank16(rank) * 4; }
+size_t down_partials_bytes(int m, int cols, int rank, int num_sms);
+cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, const SlotLists& lists, int m, int n, int k,
+                        uint16_t* pairs, uint16_t* rounded, float* partials, unsigned* counters, unsigned* status,
+                        int num_sms, cudaStream_t stream);
+
+// What a GEMM adds to its sums: z[t] . M_l for z as above, M_l = B_l^T
+// (forward) or A_l (backward), in the accumulators of the main product.
+struct AdapterTerm {
+  Adapters ad;
+  SlotLists lists[3];      // 64, 128, 256 tokens per tile
+  const uint16_t* pairs;
+};
+
+// y = x . W_hat^T + u . B_l^T for M > 16 (prefill.cu); the workspace is
+// any4_linear's.
+cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
+                                void* workspace, int num_sms, const AdapterTerm& term, cudaStream_t stream);
+
+// dx = dy . W_hat + v . A_l for W_hat (N x K) dequantized to bf16.
+size_t dx_partials_bytes(const Layout& L, int m, int num_sms);
+cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
+                      unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream);
+
 }  // namespace any4

@@ -40,56 +40,21 @@ __device__ __forceinline__ float kept_value(const Kept& kp, int k, int t, int co
   return bf16_bits_to_float(bf16_of((float)kp.codes[at] * bf16_bits_to_float(kp.steps[at / kp.group])));
 }
 
-__global__ void __launch_bounds__(128) grad_v_kernel(const uint16_t* __restrict__ dy, const Adapters ad, int n,
-                                                     float* __restrict__ v) {
-  const int t = blockIdx.x, r = threadIdx.x;
-  if (r >= ad.rank) return;
-  const int l = adapter_of(ad, t);
-  float acc = 0.0f;
-  if (l >= 0) {
-    for (int i = 0; i < n; ++i)
-      acc = fmaf(bf16_bits_to_float(dy[(size_t)t * n + i]), bf16_bits_to_float(ad.b[((size_t)l * n + i) * ad.rank + r]), acc);
-    acc *= ad.scale[l];
-  }
-  v[(size_t)t * ad.rank + r] = acc;
+__device__ __forceinline__ float pair_value(const uint16_t* pairs, int r16, int t, int r) {
+  const uint16_t* z = pairs + (size_t)t * 2 * r16 + r;
+  return bf16_bits_to_float(z[0]) + bf16_bits_to_float(z[r16]);
 }
 
-// 16 x 16 outputs per block of 256 threads.
-__global__ void __launch_bounds__(256) grad_dx_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ w,
-                                                      const Adapters ad, const float* __restrict__ v, int m, int n, int k,
-                                                      uint16_t* __restrict__ dx) {
-  __shared__ float sd[16][65], sw[64][17];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int t = blockIdx.x * 16 + ty, col = blockIdx.y * 16 + tx;   // K is a multiple of 64
-  float acc = 0.0f;
-  for (int n0 = 0; n0 < n; n0 += 64) {
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int tt = blockIdx.x * 16 + e / 64, nn = n0 + e % 64;
-      sd[e / 64][e % 64] = tt < m && nn < n ? bf16_bits_to_float(dy[(size_t)tt * n + nn]) : 0.0f;
-      const int wn = n0 + e / 16;
-      sw[e / 16][e % 16] = wn < n ? bf16_bits_to_float(w[(size_t)wn * k + blockIdx.y * 16 + e % 16]) : 0.0f;
-    }
-    __syncthreads();
-    for (int i = 0; i < 64; ++i) acc = fmaf(sd[ty][i], sw[i][tx], acc);
-    __syncthreads();
-  }
-  if (t >= m) return;
-  const int l = adapter_of(ad, t);
-  if (l >= 0)
-    for (int r = 0; r < ad.rank; ++r)
-      acc = fmaf(v[(size_t)t * ad.rank + r], bf16_bits_to_float(ad.a[((size_t)l * ad.rank + r) * k + col]), acc);
-  dx[(size_t)t * k + col] = bf16_of(acc);
-}
-
-__global__ void __launch_bounds__(128) grad_da_kernel(const Kept kp, const Adapters ad, const float* __restrict__ v, int m,
-                                                      int k, uint16_t* __restrict__ da) {
+__global__ void __launch_bounds__(128) grad_da_kernel(const Kept kp, const Adapters ad,
+                                                      const uint16_t* __restrict__ pairs, int r16, int m, int k,
+                                                      uint16_t* __restrict__ da) {
   const int l = blockIdx.x, r0 = blockIdx.y * 8, col = blockIdx.z * 128 + threadIdx.x;
   if (col >= k) return;
   float acc[8] = {};
   for (int t = 0; t < m; ++t) {
     if (adapter_of(ad, t) != l) continue;
     const float xv = kept_value(kp, k, t, col);
-    for (int j = 0; j < 8; ++j) acc[j] = fmaf(v[(size_t)t * ad.rank + r0 + j], xv, acc[j]);
+    for (int j = 0; j < 8; ++j) acc[j] = fmaf(pair_value(pairs, r16, t, r0 + j), xv, acc[j]);
   }
   for (int j = 0; j < 8; ++j) da[((size_t)l * ad.rank + r0 + j) * k + col] = bf16_of(acc[j]);
 }
@@ -109,15 +74,26 @@ __global__ void __launch_bounds__(128) grad_db_kernel(const uint16_t* __restrict
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// The workspace: any4_linear's header, v in fp32, then W_hat in bf16.
+// The workspace: any4_linear's header, W_hat in bf16, v as a bf16 pair, the
+// adapters of each token tile, then the partial sums of v and of dx (which
+// follow each other).
 struct GradSpace {
-  size_t v32, what, total;
+  size_t what, pairs, lists, partials, total;
 };
-GradSpace grad_space(int m, int n, int k, int rank) {
-  GradSpace s;
-  s.v32 = align_up(kHeaderBytes, kAlign);
-  s.what = s.v32 + align_up((size_t)m * rank * sizeof(float), kAlign);
-  s.total = s.what + align_up((size_t)n * k * 2, kAlign);
+GradSpace grad_space(const Layout& L, int m, int rank, int sms) {
+  GradSpace s{};
+  size_t at = align_up(kHeaderBytes, kAlign);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, kAlign);
+    return here;
+  };
+  s.what = take((size_t)L.n * L.k * 2);
+  s.pairs = take(pairs_bytes(m, rank));
+  s.lists = take(slot_lists_bytes(m));
+  const size_t down = down_partials_bytes(m, L.n, rank, sms), dx = dx_partials_bytes(L, m, sms);
+  s.partials = take(down > dx ? down : dx);
+  s.total = at;
   return s;
 }
 
@@ -133,7 +109,13 @@ extern "C" {
 
 ANY4_API size_t any4_lora_grad_workspace_bytes(int bits, int m, int n, int k, int group, int adapters, int rank) {
   if (!any4::grad_shape_ok(bits, m, n, k, group, adapters, rank)) return 0;
-  return any4::grad_space(m, n, k, rank).total;
+  int sms = 0;
+  const cudaError_t e = any4::cached_sm_count(&sms);
+  if (e != cudaSuccess) {
+    any4::record_cuda_error(e);
+    return 0;
+  }
+  return any4::grad_space(any4::make_layout(n, k, group, bits), m, rank, sms).total;
 }
 
 ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t* x, const int8_t* x_codes,
@@ -153,21 +135,35 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
       !aligned(packed, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) || !aligned(ids, 4) ||
       !aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16) || !aligned(workspace, 16))
     return ANY4_EALIGN;
-  const GradSpace space = grad_space(m, n, k, rank);
+  if (workspace_bytes < kHeaderBytes) return ANY4_EWORKSPACE;
+  int sms = 0;
+  cudaError_t e = cached_sm_count(&sms);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  const Layout L = make_layout(n, k, group, bits);
+  const GradSpace space = grad_space(L, m, rank, sms);
   if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
   const Adapters ad = {a, b, scale, ids, adapters, rank};
   const Kept kp = {kept8 ? nullptr : x, x_codes, x_steps, x_group};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  float* v32 = reinterpret_cast<float*>(ws + space.v32);
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + space.what);
+  uint16_t* pairs = reinterpret_cast<uint16_t*>(ws + space.pairs);
+  float* partials = reinterpret_cast<float*>(ws + space.partials);
+  unsigned* counters = reinterpret_cast<unsigned*>(ws);
+  unsigned* status = reinterpret_cast<unsigned*>(ws + kCountersBytes);
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
-  if (dx || da) grad_v_kernel<<<m, 128, 0, st>>>(dy, ad, n, v32);
-  if (dx) {
-    e = launch_dequant(static_cast<const uint8_t*>(packed), make_layout(n, k, group, bits), what, st);
-    if (e == cudaSuccess) grad_dx_kernel<<<dim3((m + 15) / 16, k / 16), 256, 0, st>>>(dy, what, ad, v32, m, n, k, dx);
+  AdapterTerm term{};
+  term.ad = ad;
+  term.pairs = pairs;
+  if (dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st);
+  if (e == cudaSuccess && ids != nullptr) {
+    for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
+    e = launch_slot_lists(ad, m, ws + space.lists, st);
   }
-  if (e == cudaSuccess && da) grad_da_kernel<<<dim3(adapters, rank / 8, (k + 127) / 128), 128, 0, st>>>(kp, ad, v32, m, k, da);
+  if (e == cudaSuccess && (dx || da))
+    e = launch_down(true, dy, ad, term.lists[1], m, n, k, pairs, nullptr, partials, counters, status, sms, st);
+  if (e == cudaSuccess && dx) e = launch_dx(dy, what, L, m, dx, partials, counters, status, sms, term, st);
+  if (e == cudaSuccess && da)
+    grad_da_kernel<<<dim3(adapters, rank / 8, (k + 127) / 128), 128, 0, st>>>(kp, ad, pairs, rank16(rank), m, k, da);
   if (e == cudaSuccess && db) grad_db_kernel<<<dim3(adapters, rank / 8, (n + 127) / 128), 128, 0, st>>>(dy, u, ad, m, n, db);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);

@@ -29,13 +29,15 @@
 // 32*(w%4) .. +31). Every mbarrier wait is bounded (~2 s); a timeout sets the
 // workspace status word and the block winds down.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.cuh"
+#include "lora.cuh"
 #include "regdecode.cuh"
+#include "tcgen05.cuh"
 
 namespace any4 {
 
@@ -49,24 +51,22 @@ constexpr int kAStageBytes = kBM * kBK * 2;    // 16 KB
 constexpr int kBStageBytes = kBN * kBK * 2;    // 32 KB
 constexpr int kStageBytes = kAStageBytes + kBStageBytes;
 constexpr int kGemmThreads = 192;
+constexpr int kPatchThreads = 128;             // with adapters: 4 warps more
 constexpr uint32_t kAccCols = kBN;             // fp32 columns per accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;   // two accumulators
 constexpr int kGemmSmem = kStages * kStageBytes + 1024 + 1024;   // stages, control, alignment
-constexpr long long kGemmWaitCycles = 4000000000ll;
-
-// tcgen05 instruction descriptor, kind::f16: D fp32, A and B bf16, both
-// K-major, N = 256, M = 128.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBN >> 3) << 17) |
-                            ((uint32_t)(kBM >> 4) << 24);
 
 struct GemmCtl {
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t raw[kStages];       // TMA bytes of a stage to be patched
+  uint64_t patched[kStages];
   uint32_t tmem_base;
   int abort_flag;
   int last_split;   // epilogue: this block finishes the tile's split-K sum
+  int spoilt[4];    // tile tcount & 3: an adapter's infinities or NaN were taken out
 };
 
 constexpr int kEpilogueBar = 1;                 // named barrier of the 4 epilogue warps
@@ -78,106 +78,91 @@ __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync %0, 128;" ::"n"(kEpilogueBar) : "memory");
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
+// ------------------------------------------------- the adapters' extra stages
+//
+// z . M^T (z = u or v of lora.cuh, M the adapter's N x R matrix B or, for dx,
+// A^T) is R more columns of the contraction, so its products go into the same
+// accumulators: behind a tile's main loop come extra stages that hold M's
+// tile where W's goes and z's where x's goes. z is a bf16 pair, leading and
+// trailing part; for R <= 32 both lie in one 64-column row and share a stage,
+// beyond that each 64 rank columns take one stage per part. Only the last of
+// a tile's K splits takes them.
+//
+// A tile whose tokens do not all have one adapter runs the stages of each of
+// its adapters, with z zeroed in the rows of the other tokens. So that an
+// infinity or NaN in an adapter reaches none of those (0 times it is NaN), it
+// is taken out of M's tile as well, and the epilogue, told by `spoilt`, adds
+// its products for the adapter's own tokens in fp32. This patching runs on
+// warps that idle otherwise; tiles of one adapter go straight from TMA to the
+// tensor core.
+struct NoLora {};
+struct LoraArgs {
+  CUtensorMap mmap;   // M: B [L][N][R], or A [L][R][K]
+  CUtensorMap zmap;   // pairs [tokens][2 R16]
+  Adapters ad;
+  SlotLists lists;
+  const uint16_t* pairs;
+  int r16;
+};
+
+struct Extra {
+  int rank0, zcol, steps;   // first rank column, column of the pairs, 16-deep steps
+  bool both;                // leading and trailing part in one stage
+};
+__device__ __forceinline__ int extra_stages(int r16) { return r16 <= 32 ? 1 : (r16 + 63) / 64 * 2; }   // per adapter
+__device__ __forceinline__ Extra extra_stage(int r16, int h) {
+  if (r16 <= 32) return {0, 0, r16 / 16, true};
+  const int rank0 = 64 * (h >> 1);
+  return {rank0, (h & 1) * r16 + rank0, min(4, (r16 - rank0) / 16), false};
 }
 
-__device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in each half that is finite
+  const uint32_t bad = ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;   // magnitude >= 0x7F80
+  return ~((bad >> 15) * 0xFFFFu);
 }
 
-// Bounded wait; false when the block is aborting or the wait timed out.
-__device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kGemmWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
+// Takes the infinities and NaN out of `bytes` of shared memory; true if this
+// thread found any.
+__device__ __forceinline__ bool patch_finite(uint32_t addr, int bytes, int thread, int threads) {
+  bool found = false;
+  for (int e = thread * 16; e < bytes; e += threads * 16) {
+    const uint4 v = lds128(addr + e);
+    const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
+    if ((a & b & c & d) != 0xFFFFFFFFu) {
+      sts128(addr + e, v.x & a, v.y & b, v.z & c, v.w & d);
+      found = true;
     }
   }
+  return found;
 }
 
-// gemm_wait for warps that wait long (a whole tile) and must not take issue
-// slots from the warps doing the work meanwhile: sleeps between polls.
-__device__ __forceinline__ bool gemm_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                               unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    __nanosleep(200);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kGemmWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
-    }
+// What patch_finite took out of the products of token t and output row: the
+// non-finite entries of its adapter's row times z.
+template <bool TRANS>
+__device__ __noinline__ float spoilt_term(const LoraArgs& la, int t, int row, int rows) {
+  const int l = adapter_of(la.ad, t);
+  float sum = 0.0f;
+  if (l < 0) return sum;
+  for (int r = 0; r < la.ad.rank; ++r) {
+    const uint32_t w = TRANS ? la.ad.a[((size_t)l * la.ad.rank + r) * rows + row]
+                             : la.ad.b[((size_t)l * rows + row) * la.ad.rank + r];
+    if ((w & 0x7F80u) != 0x7F80u) continue;
+    const uint16_t* z = la.pairs + (size_t)t * 2 * la.r16 + r;
+    sum += (bf16_bits_to_float(__ldcg(z)) + bf16_bits_to_float(__ldcg(z + la.r16))) * bf16_bits_to_float(w);
   }
+  return sum;
 }
 
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// arrives once on `bar` when every tcgen05.mma this thread issued so far is complete
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(accumulate), "r"(kIdesc)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_ld_x32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-
-// Shared-memory matrix descriptor of a K-major tile written by TMA with the
-// 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__global__ void __launch_bounds__(kGemmThreads, 1)
+// y[t][row] = sum over K of in[t][.] W[row][.] for `n` rows and a contraction
+// of `k`: W K-major (N x K), or with TRANS the K axis down W's rows (dx: row =
+// input column, contraction over the N outputs; a last chunk past `k` reads
+// zeros). X: NoLora, or LoraArgs for the adapters' term.
+template <bool TRANS, typename X>
+__global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0), 1)
     prefill_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         uint16_t* __restrict__ y, int m, int n, int k, int splits, float* __restrict__ partials,
-                        unsigned* counters, unsigned* status) {
+                        unsigned* counters, unsigned* status, const __grid_constant__ X lora) {
+  constexpr bool LORA = std::is_same<X, LoraArgs>::value;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
@@ -188,7 +173,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   volatile int* abort_flag = &ctl->abort_flag;
 
   const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + kBN - 1) / kBN;
-  const int tiles = n_tiles * m_tiles, kch = k / kBK;
+  const int tiles = n_tiles * m_tiles, kch = (k + kBK - 1) / kBK;
   const int units = tiles * splits;   // unit u: tile u / splits, K split u % splits
   auto k_range = [&](int u, int& kc0, int& kc1) {
     const int sp = u % splits;
@@ -196,6 +181,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     kc1 = (int)((long long)(sp + 1) * kch / splits);
   };
 
+  constexpr uint32_t idesc = tc_idesc(kBN, TRANS);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);    // TMA expect_tx arrival + bytes
@@ -204,6 +190,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);    // tcgen05.commit
       mbar_init(smem_addr(&ctl->acc_empty[b]), 4);   // one arrival per epilogue warp
+    }
+    if (LORA) {
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(smem_addr(&ctl->raw[s]), 1);
+        mbar_init(smem_addr(&ctl->patched[s]), kPatchThreads / 32);
+      }
+      for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -238,8 +231,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           const uint32_t fb = smem_addr(&ctl->full[s]);
           mbar_arrive_expect_tx(fb, kStageBytes);
-          tma_load_2d(sa(s), &wmap, kc * kBK, nt * kBM, fb);
+          if (TRANS) {
+            tma_load_2d(sa(s), &wmap, nt * kBM, kc * kBK, fb);
+            tma_load_2d(sa(s) + kAStageBytes / 2, &wmap, nt * kBM + 64, kc * kBK, fb);
+          } else {
+            tma_load_2d(sa(s), &wmap, kc * kBK, nt * kBM, fb);
+          }
           tma_load_2d(sb(s), &xmap, kc * kBK, mt * kBN, fb);
+        }
+        if constexpr (LORA) {
+          if (u % splits != splits - 1) continue;
+          bool mixed;
+          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          for (int e = 0; e < count; ++e, ++it) {
+            const int s = it % kStages;
+            const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+            if (it >= kStages && !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
+            const Extra ex = extra_stage(lora.r16, e % per);
+            const int l = slot_at(lora.lists, mt, e / per);
+            // a stage to be patched lands on a barrier of its own: the patching
+            // warps see only those stages, so they cannot count the others
+            const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
+            mbar_arrive_expect_tx(fb, kStageBytes);
+            if (mixed) mbar_arrive_one(smem_addr(&ctl->full[s]));
+            if (TRANS) {
+              tma_load_3d(sa(s), &lora.mmap, nt * kBM, ex.rank0, l, fb);
+              tma_load_3d(sa(s) + kAStageBytes / 2, &lora.mmap, nt * kBM + 64, ex.rank0, l, fb);
+            } else {
+              tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, fb);
+            }
+            tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * kBN, fb);
+          }
         }
       }
     }
@@ -247,7 +269,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       int it = 0, tcount = 0;
+      [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
+        [[maybe_unused]] bool mixed = false;
+        [[maybe_unused]] int slots = 0;
+        if constexpr (LORA)
+          if (u % splits == splits - 1) slots = slot_count(lora.lists, (u / splits) % m_tiles, mixed);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
@@ -261,13 +288,78 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t ph = (uint32_t)(it / kStages) & 1u;
           if (!gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status)) break;
           tc_fence_after();
-          const uint64_t ad = sw128_desc(sa(s)), bd = sw128_desc(sb(s));
+          const uint64_t ad = TRANS ? sw128_desc_mn(sa(s), kAStageBytes / 2) : sw128_desc(sa(s)), bd = sw128_desc(sb(s));
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)   // 16 columns = 32 bytes = 2 descriptor units
-            tc_mma(d, ad + 2u * (uint64_t)kk, bd + 2u * (uint64_t)kk, (kc > kc0 || kk > 0) ? 1u : 0u);
+            tc_mma(d, ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bd + 2u * (uint64_t)kk, idesc, (kc > kc0 || kk > 0) ? 1u : 0u);
           tc_commit(smem_addr(&ctl->empty[s]));   // the stage is free once these MMAs are done
         }
+        if constexpr (LORA) {
+          const int per = extra_stages(lora.r16);
+          for (int e = 0; e < slots * per; ++e, ++it) {
+            const int s = it % kStages;
+            if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kStages) & 1u, abort_flag, status)) break;
+            if (mixed) {
+              if (!gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)) break;
+              patch_phase ^= 1u << s;
+            }
+            tc_fence_after();
+            const Extra ex = extra_stage(lora.r16, e % per);
+            const uint64_t ad = TRANS ? sw128_desc_mn(sa(s), kAStageBytes / 2) : sw128_desc(sa(s)), bd = sw128_desc(sb(s));
+            for (int kk = 0; kk < ex.steps; ++kk) {
+              const uint64_t ak = ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bk = bd + 2u * (uint64_t)kk;
+              tc_mma(d, ak, bk, idesc, 1u);
+              if (ex.both) tc_mma(d, ak, bk + (uint64_t)(lora.r16 / 8), idesc, 1u);   // R16 columns on
+            }
+            tc_commit(smem_addr(&ctl->empty[s]));
+          }
+        }
         tc_commit(smem_addr(&ctl->acc_full[b]));
+      }
+    }
+  } else if (LORA && warp >= 6) {
+    // ---------------------------------------------------------- patching
+    if constexpr (LORA) {
+      const int thread = threadIdx.x - kGemmThreads;
+      int it = 0, tcount = 0;
+      uint32_t raw_phase = 0;
+      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
+        const int mt = (u / splits) % m_tiles;
+        int kc0, kc1;
+        k_range(u, kc0, kc1);
+        it += kc1 - kc0;
+        if (u % splits != splits - 1) continue;
+        bool mixed;
+        const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+        if (mixed) {
+          int id[kBN / kPatchThreads];
+#pragma unroll
+          for (int i = 0; i < kBN / kPatchThreads; ++i) {
+            const int t = mt * kBN + thread + i * kPatchThreads;
+            id[i] = t < m ? adapter_of(lora.ad, t) : -1;
+          }
+          bool ok = true;
+          for (int e = 0; e < count && ok; ++e) {
+            const int s = (it + e) % kStages;
+            const int l = slot_at(lora.lists, mt, e / per);
+            ok = __all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->raw[s]), (raw_phase >> s) & 1u, abort_flag, status));
+            if (!ok) break;   // the whole warp leaves
+            raw_phase ^= 1u << s;
+            if (patch_finite(sa(s), kAStageBytes, thread, kPatchThreads)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+#pragma unroll
+            for (int i = 0; i < kBN / kPatchThreads; ++i)
+              if (id[i] != l) {
+                const uint32_t zrow = sb(s) + (uint32_t)(thread + i * kPatchThreads) * 128u;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sts128(zrow + 16u * c, 0u, 0u, 0u, 0u);
+              }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
+          }
+          if (!ok) break;
+        }
+        it += count;
       }
     }
   } else {
@@ -283,6 +375,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       epilogue_sync();          // all four warps leave together if any wait gave up
       if (*abort_flag) break;
       tc_fence_after();
+      [[maybe_unused]] int spoilt = 0;
+      if constexpr (LORA) spoilt = *(volatile int*)&ctl->spoilt[tcount & 3];
       const int r = 32 * q + lane, row = nt * kBM + r;
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * kAccCols;
       float* part = partials + (size_t)u * kPartialFloats;   // [token][row] of this split
@@ -292,6 +386,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_ld_x32(tbase + 32u * (uint32_t)j, v);
         tc_wait_ld();
         const int m0 = mt * kBN + 32 * j;
+        if constexpr (LORA)
+          if (spoilt && row < n) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (m0 + i < m) v[i] = __float_as_uint(__uint_as_float(v[i]) + spoilt_term<TRANS>(lora, m0 + i, row, n));
+          }
         if (splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) __stcg(part + (32 * j + i) * kBM + r, __uint_as_float(v[i]));
@@ -305,6 +405,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
       }
+      if constexpr (LORA)
+        if (spoilt) {   // all four warps have read it
+          epilogue_sync();
+          if (q == 0 && lane == 0) *(volatile int*)&ctl->spoilt[tcount & 3] = 0;
+        }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
@@ -382,8 +487,7 @@ struct FusedCfg {
   static constexpr int kStage = kAStageBytes + kBStage;
   static constexpr uint32_t kTmem = 2 * BN;   // two accumulators (a power of two >= 32)
   static constexpr int kSmem = kFusedStages * kStage + 1024 + 1024;
-  static constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
-                                      ((uint32_t)(kBM >> 4) << 24);
+  static constexpr uint32_t kIdescN = tc_idesc(BN);
 };
 
 struct FusedCtl {
@@ -391,9 +495,11 @@ struct FusedCtl {
   uint64_t empty[kFusedStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t patched[kFusedStages];
   uint32_t tmem_base;
   int abort_flag;
   int last_split;
+  int spoilt[4];
 };
 
 struct FusedParams {
@@ -402,25 +508,12 @@ struct FusedParams {
   int panels, kchunks, groups, g_shift;
 };
 
-template <int BN>
-__device__ __forceinline__ void tc_mma_n(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(accumulate), "r"(FusedCfg<BN>::kIdescN)
-      : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-template <int BN>
+template <int BN, typename X>
 __global__ void __launch_bounds__(kFusedThreads, 1)
     prefill_fused_kernel(const __grid_constant__ CUtensorMap xmap, const FusedParams fp, uint16_t* __restrict__ y,
                          int m, int n, int k, int splits, float* __restrict__ partials, unsigned* counters,
-                         unsigned* status) {
+                         unsigned* status, const __grid_constant__ X lora) {
+  constexpr bool LORA = std::is_same<X, LoraArgs>::value;
   using C = FusedCfg<BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -449,6 +542,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);
       mbar_init(smem_addr(&ctl->acc_empty[b]), 4);
     }
+    if (LORA) {
+      for (int s = 0; s < kFusedStages; ++s) mbar_init(smem_addr(&ctl->patched[s]), kFusedDecoders);
+      for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
+    }
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -476,7 +573,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     // [half][lane][4 words] layout), columns 16t + 8h .. +7
     const int woff = 32 * half + lane;
     int it = 0;
-    for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
+    [[maybe_unused]] int tcount = 0;
+    for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
       const int nt = (u / splits) / m_tiles;
       const int P = nt * (kBM / kPanelRows) + p;
       const bool live = P < fp.panels;   // the last tile may end before this panel
@@ -550,6 +648,40 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           ok = stage(kc + 1, wb, rb);
         }
       }
+      if constexpr (LORA) {
+        // the adapters' stages come whole by TMA; the decoders count them in
+        // and patch those of tiles with several adapters
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok && u % splits == splits - 1) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");   // lists, ids and pairs are ready
+          const int mt = (u / splits) % m_tiles, thread = threadIdx.x - 6 * 32;
+          bool mixed;
+          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          const int t = mt * BN + thread;
+          const int id = mixed && thread < BN && t < m ? adapter_of(lora.ad, t) : -1;
+          for (int e = 0; e < count && ok; ++e) {
+            const int s = it % kFusedStages;
+            const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
+            ++it;
+            ok = __all_sync(0xFFFFFFFFu, it <= kFusedStages ||
+                                             gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status));
+            if (!ok) break;   // the whole warp leaves
+            if (lane == 0) mbar_arrive_one(smem_addr(&ctl->full[s]));
+            if (!mixed) continue;
+            const int l = slot_at(lora.lists, mt, e / per);
+            ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
+            if (!ok) break;
+            if (patch_finite(sa(s), kAStageBytes, thread, 32 * kFusedDecoders)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (thread < BN && id != l) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) sts128(sb(s) + (uint32_t)thread * 128u + 16u * c, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
+          }
+        }
+      }
       if (!ok) break;
     }
   } else if (warp == 0) {
@@ -569,13 +701,35 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           mbar_arrive_expect_tx(fb, C::kBStage);
           tma_load_2d(sb(s), &xmap, kc * kBK, mt * BN, fb);
         }
+        if constexpr (LORA) {
+          if (u % splits != splits - 1) continue;
+          const int nt = (u / splits) / m_tiles;
+          bool mixed;
+          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          for (int e = 0; e < count; ++e, ++it) {
+            const int s = it % kFusedStages;
+            const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
+            if (it >= kFusedStages && !gemm_wait_idle(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
+            const Extra ex = extra_stage(lora.r16, e % per);
+            const uint32_t fb = smem_addr(&ctl->full[s]);
+            mbar_arrive_expect_tx(fb, C::kStage);
+            tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, slot_at(lora.lists, mt, e / per), fb);
+            tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * BN, fb);
+          }
+        }
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       int it = 0, tcount = 0;
+      [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
+      if (LORA) asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists are ready
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
+        [[maybe_unused]] bool mixed = false;
+        [[maybe_unused]] int slots = 0;
+        if constexpr (LORA)
+          if (u % splits == splits - 1) slots = slot_count(lora.lists, (u / splits) % m_tiles, mixed);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status)) break;
@@ -591,8 +745,28 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           const uint64_t ad = sw128_desc(sa(s)), bd = sw128_desc(sb(s));
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            tc_mma_n<BN>(d, ad + 2u * (uint64_t)kk, bd + 2u * (uint64_t)kk, (kc > kc0 || kk > 0) ? 1u : 0u);
+            tc_mma(d, ad + 2u * (uint64_t)kk, bd + 2u * (uint64_t)kk, C::kIdescN, (kc > kc0 || kk > 0) ? 1u : 0u);
           tc_commit(smem_addr(&ctl->empty[s]));
+        }
+        if constexpr (LORA) {
+          const int per = extra_stages(lora.r16);
+          for (int e = 0; e < slots * per; ++e, ++it) {
+            const int s = it % kFusedStages;
+            if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kFusedStages) & 1u, abort_flag, status)) break;
+            if (mixed) {
+              if (!gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)) break;
+              patch_phase ^= 1u << s;
+            }
+            tc_fence_after();
+            const Extra ex = extra_stage(lora.r16, e % per);
+            const uint64_t ad = sw128_desc(sa(s)), bd = sw128_desc(sb(s));
+            for (int kk = 0; kk < ex.steps; ++kk) {
+              const uint64_t ak = ad + 2u * (uint64_t)kk, bk = bd + 2u * (uint64_t)kk;
+              tc_mma(d, ak, bk, C::kIdescN, 1u);
+              if (ex.both) tc_mma(d, ak, bk + (uint64_t)(lora.r16 / 8), C::kIdescN, 1u);
+            }
+            tc_commit(smem_addr(&ctl->empty[s]));
+          }
         }
         tc_commit(smem_addr(&ctl->acc_full[b]));
       }
@@ -611,6 +785,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       epilogue_sync();
       if (*abort_flag) break;
       tc_fence_after();
+      [[maybe_unused]] int spoilt = 0;
+      if constexpr (LORA) spoilt = *(volatile int*)&ctl->spoilt[tcount & 3];
       const int r = 32 * q + lane, row = nt * kBM + r;
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * BN;
       float* part = partials + (size_t)u * kPartialFloats;
@@ -620,6 +796,12 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         tc_ld_x32(tbase + 32u * (uint32_t)j, v);
         tc_wait_ld();
         const int m0 = mt * BN + 32 * j;
+        if constexpr (LORA)
+          if (spoilt && row < n) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (m0 + i < m) v[i] = __float_as_uint(__uint_as_float(v[i]) + spoilt_term<false>(lora, m0 + i, row, n));
+          }
         if (splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) __stcg(part + (32 * j + i) * kBM + r, __uint_as_float(v[i]));
@@ -633,6 +815,11 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           }
         }
       }
+      if constexpr (LORA)
+        if (spoilt) {   // all four warps have read it
+          epilogue_sync();
+          if (q == 0 && lane == 0) *(volatile int*)&ctl->spoilt[tcount & 3] = 0;
+        }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
@@ -679,56 +866,31 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
-// rows x cols bf16 matrix (row-major), boxes of box_rows x 64 columns, 128-byte swizzle
-bool encode_bf16_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaError_t allow_gemm_smem() {
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
   static std::atomic<unsigned long long> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (done_mask.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(prefill_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done_mask.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 
-template <int BN>
-cudaError_t allow_fused_smem() {
-  static std::atomic<unsigned long long> done_mask{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (done_mask.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(prefill_fused_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, FusedCfg<BN>::kSmem);
-  if (e == cudaSuccess) done_mask.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+// The adapter arguments of a kernel with `tokens` per tile and `rows` output
+// rows; false if a tensor map cannot be encoded.
+bool fill_lora(NoLora*, const AdapterTerm*, const Layout&, int, int, bool) { return true; }
+bool fill_lora(LoraArgs* la, const AdapterTerm* term, const Layout& L, int m, int tokens, bool trans) {
+  const Adapters& ad = term->ad;
+  la->ad = ad;
+  la->lists = term->lists[tokens == 64 ? 0 : tokens == 128 ? 1 : 2];
+  la->pairs = term->pairs;
+  la->r16 = rank16(ad.rank);
+  return encode_bf16_map(&la->zmap, term->pairs, m, 2 * la->r16, tokens) &&
+         (trans ? encode_bf16_map3(&la->mmap, ad.a, ad.count, ad.rank, L.k, 64)
+                : encode_bf16_map3(&la->mmap, ad.b, ad.count, L.n, ad.rank, kBM));
 }
 
 // Token tile of the fused path: the smallest of 64, 128, 256 that holds M
@@ -755,13 +917,14 @@ int splits_for(const Layout& L, int tiles, int num_sms) {
 constexpr int kFusedMaxTokens = 512;
 bool fused_path(const Layout& L, int m) { return L.bits == 4 && m <= kFusedMaxTokens; }
 
-template <int BN>
+template <int BN, typename X>
 cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                         void* workspace, int num_sms, cudaStream_t stream) {
-  cudaError_t e = allow_fused_smem<BN>();
+                         void* workspace, int num_sms, const AdapterTerm* term, cudaStream_t stream) {
+  cudaError_t e = allow_smem<prefill_fused_kernel<BN, X>>(FusedCfg<BN>::kSmem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap;
-  if (!encode_bf16_map(&xmap, x, m, L.k, BN)) return cudaErrorInvalidValue;
+  X lora;
+  if (!encode_bf16_map(&xmap, x, m, L.k, BN) || !fill_lora(&lora, term, L, m, BN, false)) return cudaErrorInvalidValue;
   const int tiles = tiles_for(L, m, BN);
   const int splits = splits_for(L, tiles, num_sms);
   const int units = tiles * splits;
@@ -783,9 +946,39 @@ cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_fused_kernel<BN>, xmap, fp, y, m, L.n, L.k, splits,
+  return cudaLaunchKernelEx(&cfg, prefill_fused_kernel<BN, X>, xmap, fp, y, m, L.n, L.k, splits,
                             reinterpret_cast<float*>(ws + kHeaderBytes), reinterpret_cast<unsigned*>(ws),
-                            reinterpret_cast<unsigned*>(ws + kCountersBytes));
+                            reinterpret_cast<unsigned*>(ws + kCountersBytes), lora);
+}
+
+// The GEMM over `rows` output rows and a contraction of `cols`, from W_hat in
+// bf16 (N x K; TRANS: rows = K, cols = N).
+template <bool TRANS, typename X>
+cudaError_t launch_gemm(const uint16_t* in, const uint16_t* what, const Layout& L, int m, uint16_t* out, int splits,
+                        float* partials, unsigned* counters, unsigned* status, int num_sms, const AdapterTerm* term,
+                        cudaStream_t stream) {
+  cudaError_t e = allow_smem<prefill_gemm_kernel<TRANS, X>>(kGemmSmem);
+  if (e != cudaSuccess) return e;
+  const int rows = TRANS ? L.k : L.n, cols = TRANS ? L.n : L.k;
+  CUtensorMap wmap, xmap;
+  X lora;
+  if (!encode_bf16_map(&wmap, what, L.n, L.k, TRANS ? kBK : kBM) || !encode_bf16_map(&xmap, in, m, cols, kBN) ||
+      !fill_lora(&lora, term, L, m, kBN, TRANS))
+    return cudaErrorInvalidValue;
+  const int tiles = ((rows + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+  const int units = tiles * splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units < num_sms ? units : num_sms);
+  cfg.blockDim = dim3(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0));
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel<TRANS, X>, wmap, xmap, out, m, rows, cols, splits, partials,
+                            counters, status, lora);
 }
 
 }  // namespace
@@ -794,15 +987,18 @@ size_t prefill_scratch_offset() { return kHeaderBytes; }
 
 bool prefill_fused(const Layout& L, int m) { return fused_path(L, m); }
 
-int prefill_splits(const Layout& L, int m, int num_sms) {
-  const int tiles = ((L.n + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
-  const int kch = L.k / kBK;
+// K splits of a GEMM with `rows` output rows and a contraction of `cols`.
+static int gemm_splits(int rows, int cols, int m, int num_sms) {
+  const int tiles = ((rows + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+  const int kch = cols / kBK;
   int s = tiles < num_sms ? num_sms / tiles : 1;
   const int smax = kch / kMinSplitChunks > 0 ? kch / kMinSplitChunks : 1;
   if (s > smax) s = smax;
   if (s > kMaxSplits) s = kMaxSplits;
   return s < 1 ? 1 : s;
 }
+
+int prefill_splits(const Layout& L, int m, int num_sms) { return gemm_splits(L.n, L.k, m, num_sms); }
 
 size_t prefill_partials_offset(const Layout& L) {
   return kHeaderBytes + align_up((size_t)L.n * L.k * 2, kAlign);
@@ -820,43 +1016,45 @@ size_t prefill_workspace_bytes(const Layout& L, int m, int num_sms) {
   return prefill_partials_offset(L) + partials;
 }
 
-cudaError_t launch_prefill(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
-                           void* workspace, int num_sms, cudaStream_t stream) {
+template <typename X>
+static cudaError_t launch_prefill_any(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
+                                      void* workspace, int num_sms, const AdapterTerm* term, cudaStream_t stream) {
   if (fused_path(L, m)) {
     switch (fused_bn(m)) {
-      case 64: return launch_fused<64>(x, packed, L, m, y, workspace, num_sms, stream);
-      case 128: return launch_fused<128>(x, packed, L, m, y, workspace, num_sms, stream);
-      default: return launch_fused<256>(x, packed, L, m, y, workspace, num_sms, stream);
+      case 64: return launch_fused<64, X>(x, packed, L, m, y, workspace, num_sms, term, stream);
+      case 128: return launch_fused<128, X>(x, packed, L, m, y, workspace, num_sms, term, stream);
+      default: return launch_fused<256, X>(x, packed, L, m, y, workspace, num_sms, term, stream);
     }
   }
-  cudaError_t e = allow_gemm_smem();
-  if (e != cudaSuccess) return e;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + prefill_scratch_offset());
-  e = launch_dequant(packed, L, what, stream);   // bf16 W_hat, N x K
+  const cudaError_t e = launch_dequant(packed, L, what, stream);   // bf16 W_hat, N x K
   if (e != cudaSuccess) return e;
-  CUtensorMap wmap, xmap;
-  if (!encode_bf16_map(&wmap, what, L.n, L.k, kBM) || !encode_bf16_map(&xmap, x, m, L.k, kBN))
-    return cudaErrorInvalidValue;
-  const int tiles = ((L.n + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
-  const int splits = prefill_splits(L, m, num_sms);
-  const int units = tiles * splits;
-  const int grid = units < num_sms ? units : num_sms;
-  unsigned* status = reinterpret_cast<unsigned*>(ws + kCountersBytes);
-  unsigned* counters = reinterpret_cast<unsigned*>(ws);
-  float* partials = reinterpret_cast<float*>(ws + prefill_partials_offset(L));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel, wmap, xmap, y, m, L.n, L.k, splits, partials, counters,
-                            status);
+  return launch_gemm<false, X>(x, what, L, m, y, prefill_splits(L, m, num_sms),
+                               reinterpret_cast<float*>(ws + prefill_partials_offset(L)), reinterpret_cast<unsigned*>(ws),
+                               reinterpret_cast<unsigned*>(ws + kCountersBytes), num_sms, term, stream);
+}
+
+cudaError_t launch_prefill(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
+                           void* workspace, int num_sms, cudaStream_t stream) {
+  return launch_prefill_any<NoLora>(x, packed, L, m, y, workspace, num_sms, nullptr, stream);
+}
+
+cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
+                                void* workspace, int num_sms, const AdapterTerm& term, cudaStream_t stream) {
+  return launch_prefill_any<LoraArgs>(x, packed, L, m, y, workspace, num_sms, &term, stream);
+}
+
+size_t dx_partials_bytes(const Layout& L, int m, int num_sms) {
+  const int splits = gemm_splits(L.k, L.n, m, num_sms);
+  const int tiles = ((L.k + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+  return splits > 1 ? align_up((size_t)tiles * splits * kPartialFloats * sizeof(float), kAlign) : 0;
+}
+
+cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
+                      unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream) {
+  return launch_gemm<true, LoraArgs>(dy, what, L, m, dx, gemm_splits(L.k, L.n, m, num_sms), partials, counters, status,
+                                     num_sms, &term, stream);
 }
 
 }  // namespace any4

@@ -210,6 +210,15 @@ def test_zero_adapters_leave_the_projection():
         assert bool((y == base).all())
 
 
+@pytest.mark.parametrize("m", [40, 100, 200, 700])
+def test_zero_adapters_leave_the_prefill(m):
+    """With B = 0 the prefill layer is any4_linear bit for bit too."""
+    c = Case(m, 1024, 1024, 128, 4, 3, 16, "mixed", seed=7)
+    c.b.zero_()
+    base = a4.any4_linear(c.x, c.packed(), *c.shape())
+    assert bool((forward(c) == base).all())
+
+
 @pytest.mark.parametrize("m", [1, 16, 60, 600])
 def test_streams_graphs_and_two_calls_at_once(m):
     c = Case(m, 528, 1024, 128, 4, 5, 16, "mixed", seed=8)
