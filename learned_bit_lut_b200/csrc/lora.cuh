@@ -33,27 +33,28 @@ __device__ __forceinline__ int adapter_of(const Adapters& ad, int token) {
 }
 
 // The adapters present in each tile of 64, 128 or 256 tokens, in order of
-// their first token: slots[tile * tokens + j], j < counts[tile] & kSlotCount,
-// with kSlotMixed set where the tile's tokens do not all have the same
-// adapter. Without lists (no ids) every tile has adapter 0 alone.
+// their first token: heads[tile] = {count, with kSlotMixed set where the
+// tile's tokens do not all have the same adapter; the first adapter},
+// slots[tile * tokens + j] for j < count. Without lists (no ids) every tile
+// has adapter 0 alone.
 constexpr int kSlotCount = 0xFFFF;
 constexpr int kSlotMixed = 1 << 30;
 struct SlotLists {
   const int* slots;
-  const int* counts;
+  const int2* heads;
   int tokens;
 };
-__device__ __forceinline__ int slot_count(const SlotLists& s, int tile, bool& mixed) {
-  if (s.slots == nullptr) {
-    mixed = false;
-    return 1;
-  }
-  const int c = __ldcg(s.counts + tile);
-  mixed = (c & kSlotMixed) != 0;
-  return c & kSlotCount;
+struct SlotHead {
+  int count, first;
+  bool mixed;
+};
+__device__ __forceinline__ SlotHead slot_head(const SlotLists& s, int tile) {
+  if (s.slots == nullptr) return {1, 0, false};
+  const int2 h = __ldcg(s.heads + tile);
+  return {h.x & kSlotCount, h.y, (h.x & kSlotMixed) != 0};
 }
-__device__ __forceinline__ int slot_at(const SlotLists& s, int tile, int j) {
-  return s.slots == nullptr ? 0 : __ldcg(s.slots + (size_t)tile * s.tokens + j);
+__device__ __forceinline__ int slot_at(const SlotLists& s, int tile, const SlotHead& h, int j) {
+  return j == 0 ? h.first : __ldcg(s.slots + (size_t)tile * s.tokens + j);
 }
 
 constexpr int kListTile = 256;   // the lists are built 256 tokens at a time
@@ -80,6 +81,16 @@ struct AdapterTerm {
   SlotLists lists[3];      // 64, 128, 256 tokens per tile
   const uint16_t* pairs;
 };
+
+// dA (of the kept input: bf16 x, or codes and steps with groups of x_group) and
+// dB, from v as pairs and the kept u (lora_wgrad.cu). `space` holds
+// wgrad_partials_bytes of partial sums.
+size_t wgrad_partials_bytes(int m, int cols, int adapters, int width, int num_sms);
+cudaError_t launch_da(const uint16_t* x, const int8_t* codes, const uint16_t* steps, int x_group, const uint16_t* pairs,
+                      const Adapters& ad, const SlotLists& lists, int m, int k, uint16_t* da, void* space,
+                      unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
+cudaError_t launch_db(const uint16_t* dy, const uint16_t* u, const Adapters& ad, const SlotLists& lists, int m, int n,
+                      uint16_t* db, void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
 
 // y = x . W_hat^T + u . B_l^T for M > 16 (prefill.cu); the workspace is
 // any4_linear's.

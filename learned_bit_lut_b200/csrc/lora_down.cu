@@ -33,7 +33,7 @@ namespace {
 
 struct ListSpace {
   int* slots[3];    // 64, 128, 256 tokens per tile
-  int* counts[3];
+  int2* heads[3];
 };
 
 __host__ __device__ inline int list_tokens(int i) { return 64 << i; }
@@ -44,8 +44,8 @@ ListSpace list_space(void* space, int m) {
   int* p = static_cast<int*>(space);
   for (int i = 0; i < 3; ++i, p += padded) s.slots[i] = p;
   for (int i = 0; i < 3; ++i) {
-    s.counts[i] = p;
-    p += padded / list_tokens(i);
+    s.heads[i] = reinterpret_cast<int2*>(p);
+    p += 2 * padded / list_tokens(i);
   }
   return s;
 }
@@ -61,10 +61,24 @@ __global__ void __launch_bounds__(kListTile) slot_lists_kernel(const Adapters ad
   const int mine = t < m ? adapter_of(ad, t) : -1;
   id[i] = mine;
   __syncthreads();
-  int before = -1;   // the nearest earlier token of the same adapter
-  if (mine >= 0)
-    for (int s = i - 1; s >= 0 && before < 0; --s)
-      if (id[s] == mine) before = s;
+  // the nearest earlier token of the same adapter: within the warp, or the
+  // first token of the nearest earlier warp that has one (tiles start at warps)
+  int before = -1;
+  const unsigned same = __match_any_sync(0xFFFFFFFFu, mine) & ((1u << lane) - 1u);
+  if (same != 0) {
+    before = (i & ~31) + 31 - __clz(same);
+  } else if (mine >= 0) {
+    for (int w = warp - 1; w >= 0 && before < 0; --w) {
+      const int4* ids = reinterpret_cast<const int4*>(id + 32 * w);
+      bool found = false;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int4 q = ids[c];
+        found |= q.x == mine || q.y == mine || q.z == mine || q.w == mine;
+      }
+      if (found) before = 32 * w;
+    }
+  }
   const unsigned none = __ballot_sync(0xFFFFFFFFu, t < m && mine < 0);
   if (lane == 0) warp_none[warp] = none != 0;
   unsigned first[3];
@@ -82,13 +96,15 @@ __global__ void __launch_bounds__(kListTile) slot_lists_kernel(const Adapters ad
     for (int w = base >> 5; w < warp; ++w) rank += warp_first[g][w];
     const size_t tile0 = (size_t)blockIdx.x * kListTile + base;
     if (first[g] >> lane & 1u) out.slots[g][tile0 + rank] = mine;
+    // the head: count, and the tile's first adapter (its first token has rank 0)
+    if (first[g] >> lane & 1u && rank == 0) out.heads[g][tile0 / tokens].y = mine;
     if (i == base) {
       int count = 0, gap = 0;
       for (int w = base >> 5; w < (base + tokens) >> 5; ++w) {
         count += warp_first[g][w];
         gap |= warp_none[w];
       }
-      out.counts[g][tile0 / tokens] = count | (count > 1 || gap ? kSlotMixed : 0);
+      out.heads[g][tile0 / tokens].x = count | (count > 1 || gap ? kSlotMixed : 0);
     }
   }
 }
@@ -143,8 +159,8 @@ __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, 
   for (int i = 0; i < 8; ++i) {
     hi[i] = bf16x2_of(z[2 * i], z[2 * i + 1]);
     const float h0 = bf16_bits_to_float(hi[i] & 0xFFFFu), h1 = __uint_as_float(hi[i] & 0xFFFF0000u);
-    // an infinite or NaN leading part is the whole value
-    lo[i] = bf16x2_of(isfinite(h0) ? z[2 * i] - h0 : 0.0f, isfinite(h1) ? z[2 * i + 1] - h1 : 0.0f);
+    // an infinity or NaN goes into both parts: the sum of their products is that of the one
+    lo[i] = bf16x2_of(isfinite(h0) ? z[2 * i] - h0 : h0, isfinite(h1) ? z[2 * i + 1] - h1 : h1);
   }
   uint4* row = reinterpret_cast<uint4*>(p.pairs + (size_t)t * 2 * p.r16 + r0);
   row[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -192,9 +208,9 @@ __global__ void __launch_bounds__(kDownTcThreads, 1)
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists and `in` are ready, the outputs are free
-  bool mixed;
-  const int count = slot_count(p.lists, tile, mixed);
-  for (int j = threadIdx.x; j < count; j += kDownTcThreads) ctl->slots[j] = slot_at(p.lists, tile, j);
+  const SlotHead head = slot_head(p.lists, tile);
+  const int count = head.count;
+  for (int j = threadIdx.x; j < count; j += kDownTcThreads) ctl->slots[j] = slot_at(p.lists, tile, head, j);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -374,13 +390,13 @@ int down_splits(int m, int cols, int num_sms) {
 
 size_t slot_lists_bytes(int m) {
   const size_t padded = align_up((size_t)m, kListTile);
-  return align_up((3 * padded + padded / 64 + padded / 128 + padded / 256) * sizeof(int), kAlign);
+  return align_up((3 * padded + 2 * (padded / 64 + padded / 128 + padded / 256)) * sizeof(int), kAlign);
 }
 
 SlotLists slot_lists(void* space, int m, int tokens) {
   const ListSpace s = list_space(space, m);
   const int i = tokens == 64 ? 0 : tokens == 128 ? 1 : 2;
-  return {s.slots[i], s.counts[i], tokens};
+  return {s.slots[i], s.heads[i], tokens};
 }
 
 cudaError_t launch_slot_lists(const Adapters& ad, int m, void* space, cudaStream_t stream) {

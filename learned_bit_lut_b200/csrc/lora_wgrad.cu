@@ -1,0 +1,626 @@
+// The adapters' gradients (lora.cuh): sums over tokens of outer products,
+//
+//   dA_l = sum over the tokens of l of v[t]^T x[t]      (R x K)
+//   dB_l = sum over the tokens of l of dy[t]^T u[t]     (N x R)
+//
+// Both are a tall skinny product src^T z with the tokens as the contraction:
+// src is x or dy (128 of its columns per block), z the R inner values. A
+// 64-token chunk of src is a tile with the contraction down its rows, an
+// MN-major operand as TMA brings it in, and so is z's. Against one chunk of
+// src go the z tiles of every adapter that has a token in it, each into its
+// own tensor-memory columns; v is a bf16 pair whose two parts are 2 R16
+// columns of one instruction and are added in the epilogue.
+//
+// src is read once and bounds the work (R <= 64; the rest is small and comes
+// from L2), so x kept in 8 bits halves it: 8 warps turn the codes into the
+// bf16 values they stand for (act8.cuh) on their way into the operand tile.
+//
+// A chunk whose tokens do not all have one adapter is patched by the same
+// warps: the rows of other tokens are zeroed in z, and infinities and NaN are
+// taken out of src, where 0 times them would be NaN; for the columns and
+// adapters they belong to the epilogue then sums anew in fp32. So a padding token's or
+// another request's values reach no sum but their own.
+//
+// Blocks: 128 columns of src x a share of the chunks x as many adapters as
+// tensor memory holds (512 columns). Shares of the chunks are added by the
+// last block to arrive, in order.
+//
+// Warps: 0 = TMA, 1 = MMA, 2-5 = epilogue, 6-13 = codes and patches.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "act8.cuh"
+#include "lora.cuh"
+#include "tcgen05.cuh"
+
+namespace any4 {
+
+namespace {
+
+constexpr int kCols = 128;                       // src columns per block (MMA M)
+constexpr int kTokens = 64;                      // contraction per chunk
+constexpr int kABytes = kTokens * kCols * 2;     // a chunk of src in bf16: two halves of 64 columns
+constexpr int kRawBytes = kTokens * kCols;       // the same in codes
+constexpr int kWorkers = 8;
+constexpr int kWorkThreads = kWorkers * 32;
+constexpr int kWgradThreads = 192 + kWorkThreads;
+constexpr int kZBudget = 100 * 1024;
+constexpr int kMaxZStages = 8;
+constexpr int kWgradBar = 1;
+constexpr int kMaxGroups = 16;                   // adapters per block: 512 columns / 32
+
+template <bool CODES>
+struct WgradCfg {
+  static constexpr int kAStages = CODES ? 3 : 6;
+  static constexpr int kRawStages = CODES ? 6 : 0;
+  static constexpr int kSrcBytes = kAStages * kABytes + kRawStages * kRawBytes;   // 96 KB both
+};
+constexpr int kMaxAStages = 6, kMaxRawStages = 6;
+constexpr int kMaxSplits = 16;
+constexpr int kWgradFixed = 1024 + 1024;         // control, alignment
+constexpr int kWgradSmem = WgradCfg<false>::kSrcBytes + kZBudget + kWgradFixed;
+// a block's chunk masks share the z stages' budget: all of 2^20 tokens leave one stage of the widest
+static_assert(kMaxTokens / kTokens * 4 + 4 * 8192 <= kZBudget, "masks and a z stage");
+
+constexpr unsigned kMixed = 1u << 31;
+
+struct alignas(1024) WgradCtl {
+  uint64_t a_full[kMaxAStages], a_empty[kMaxAStages];
+  uint64_t a_raw[kMaxAStages], a_ready[kMaxAStages];     // bytes of a chunk to be patched; patched or converted
+  uint64_t code_full[kMaxRawStages], code_empty[kMaxRawStages];
+  uint64_t z_full[kMaxZStages], z_empty[kMaxZStages];
+  uint64_t z_raw[kMaxZStages], z_ready[kMaxZStages];
+  uint64_t acc_full;
+  uint32_t tmem_base;
+  int abort_flag;
+  int leave, last;
+  int spoilt;
+  unsigned touched;                   // bit g: adapter group g has a product
+};
+static_assert(sizeof(WgradCtl) == 1024, "control block");
+
+struct WgradParams {
+  Adapters ad;
+  SlotLists lists;            // 64 tokens per tile
+  int m, cols, chunks;
+  int splits, passes;
+  int width;                  // z columns of one instruction: 2 R16 (pairs) or R16
+  int r16;
+  int group_cols, per_pass;   // tensor-memory columns per adapter, adapters per block
+  int z_bytes, z_stages;
+  uint32_t idesc, tmem_cols;
+  const uint16_t* src;        // bf16 src, or
+  const uint8_t* codes;
+  const uint16_t* steps;
+  int step_shift, step_cols;  // log2 of the group, groups per row
+  const uint16_t* z;          // pairs, or the kept u
+  int z_stride;
+  uint16_t* out;
+  float* partials;            // [unit][adapter of the pass][R16][128]
+  unsigned* masks;            // [unit]: adapters with a product
+  unsigned* counters;
+  unsigned* status;
+};
+
+__device__ __forceinline__ void wgrad_epilogue_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kWgradBar) : "memory"); }
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xFFFFFFFFu, gemm_wait(bar, parity, abort_flag, status));   // the whole warp goes on or leaves
+}
+
+// src[t][col] as the product sees it.
+__device__ __forceinline__ float src_value(const WgradParams& p, int t, int col) {
+  const size_t at = (size_t)t * p.cols + col;
+  if (p.codes == nullptr) return bf16_bits_to_float(__ldcg(p.src + at));
+  const float step = bf16_bits_to_float(__ldcg(p.steps + (size_t)t * p.step_cols + (col >> p.step_shift)));
+  return __bfloat162float(__float2bfloat16_rn((float)(int8_t)__ldcg(p.codes + at) * step));
+}
+
+// Column col of adapter l, ranks r0 .. r0 + 15, where infinities or NaN of the
+// adapter's own tokens were taken out of src: the sum over its tokens anew.
+template <bool PAIRS>
+__device__ __noinline__ void spoilt_sums(const WgradParams& p, int c0, int c1, int l, int col, int r0, float (&sum)[16]) {
+  const int t0 = c0 * kTokens, t1 = min(p.m, c1 * kTokens);
+  bool own = false;
+  for (int t = t0; t < t1 && !own; ++t) own = adapter_of(p.ad, t) == l && !isfinite(src_value(p, t, col));
+  if (!own) return;
+  for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+  for (int t = t0; t < t1; ++t) {
+    if (adapter_of(p.ad, t) != l) continue;
+    const float s = src_value(p, t, col);
+    const uint16_t* z = p.z + (size_t)t * p.z_stride + r0;
+    for (int i = 0; i < 16 && r0 + i < p.ad.rank; ++i) {
+      float v = bf16_bits_to_float(__ldcg(z + i));
+      if (PAIRS) v += bf16_bits_to_float(__ldcg(z + p.r16 + i));
+      sum[i] += v * s;
+    }
+  }
+}
+
+// 16 rank values of one src column to the output: dA [L][R][cols] (PAIRS) or
+// dB [L][cols][R].
+template <bool PAIRS>
+__device__ __forceinline__ void store_grad(const WgradParams& p, int l, int col, int r0, const float (&v)[16]) {
+  if (PAIRS) {
+    uint16_t* out = p.out + ((size_t)l * p.ad.rank + r0) * p.cols + col;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (r0 + i < p.ad.rank) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+        out[(size_t)i * p.cols] = *reinterpret_cast<const uint16_t*>(&h);
+      }
+    }
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    uint4* out = reinterpret_cast<uint4*>(p.out + ((size_t)l * p.cols + col) * p.ad.rank + r0);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (r0 + 8 < p.ad.rank) out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// PAIRS: z is a bf16 pair and the result dA; else z is u and the result dB.
+// CODES: src is an 8-bit checkpoint.
+template <bool PAIRS, bool CODES>
+__global__ void __launch_bounds__(kWgradThreads, 1)
+    adapter_wgrad_kernel(const __grid_constant__ CUtensorMap smap, const __grid_constant__ CUtensorMap zmap,
+                         const __grid_constant__ WgradParams p) {
+  using C = WgradCfg<CODES>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  const uint32_t rbase = sbase + C::kAStages * kABytes, zbase = sbase + C::kSrcBytes;
+  WgradCtl* ctl = reinterpret_cast<WgradCtl*>(smem_raw + (zbase - raw) + (size_t)p.z_stages * p.z_bytes);
+  // chunk c0 + i: bit g is adapter l_lo + g, kMixed: its tokens do not all have one adapter
+  unsigned* info = reinterpret_cast<unsigned*>(ctl + 1);
+  volatile int* abort_flag = &ctl->abort_flag;
+  // unit: column tile, then pass, then share of the chunks
+  const int unit = blockIdx.x, split = unit % p.splits, tp = unit / p.splits;
+  const int pass = tp % p.passes, ct = tp / p.passes;
+  const int c0 = (int)((long long)split * p.chunks / p.splits), c1 = (int)((long long)(split + 1) * p.chunks / p.splits);
+  const int l_lo = pass * p.per_pass, l_hi = min(p.ad.count, l_lo + p.per_pass);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kAStages; ++s) {
+      mbar_init(smem_addr(&ctl->a_full[s]), 1);
+      mbar_init(smem_addr(&ctl->a_empty[s]), 1);
+      mbar_init(smem_addr(&ctl->a_raw[s]), 1);
+      mbar_init(smem_addr(&ctl->a_ready[s]), kWorkers);
+    }
+    for (int s = 0; s < C::kRawStages; ++s) {
+      mbar_init(smem_addr(&ctl->code_full[s]), 1);
+      mbar_init(smem_addr(&ctl->code_empty[s]), kWorkers);
+    }
+    for (int s = 0; s < p.z_stages; ++s) {
+      mbar_init(smem_addr(&ctl->z_full[s]), 1);
+      mbar_init(smem_addr(&ctl->z_empty[s]), 1);
+      mbar_init(smem_addr(&ctl->z_raw[s]), 1);
+      mbar_init(smem_addr(&ctl->z_ready[s]), kWorkers);
+    }
+    mbar_init(smem_addr(&ctl->acc_full), 2);   // the last products, and `touched`
+    ctl->abort_flag = 0;
+    ctl->spoilt = 0;
+    ctl->touched = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int c = c0 + threadIdx.x; c < c1; c += kWgradThreads) {
+    const SlotHead h = slot_head(p.lists, c);
+    unsigned mask = 0;
+#pragma unroll 4
+    for (int j = 0; j < h.count; ++j) {
+      const int l = slot_at(p.lists, c, h, j);
+      if (l >= l_lo && l < l_hi) mask |= 1u << (l - l_lo);
+    }
+    info[c - c0] = mask != 0 && h.mixed ? mask | kMixed : mask;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  // Every role walks the chunks, and a chunk's adapters (the bits of its mask
+  // in ascending order), alike.
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      int ai = 0, zi = 0;
+      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+        const unsigned in = info[c - c0];
+        if (in == 0) continue;
+        const bool mixed = in & kMixed;
+        if (CODES) {
+          const int s = ai % (C::kRawStages > 0 ? C::kRawStages : 1);
+          const uint32_t ph = (uint32_t)(ai / (C::kRawStages > 0 ? C::kRawStages : 1)) & 1u;
+          if (ai >= C::kRawStages && !gemm_wait(smem_addr(&ctl->code_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
+          const uint32_t fb = smem_addr(&ctl->code_full[s]);
+          mbar_arrive_expect_tx(fb, kRawBytes);
+          tma_load_2d(rbase + (uint32_t)s * kRawBytes, &smap, ct * kCols, c * kTokens, fb);
+        } else {
+          const int s = ai % C::kAStages;
+          const uint32_t ph = (uint32_t)(ai / C::kAStages) & 1u;
+          if (ai >= C::kAStages && !gemm_wait(smem_addr(&ctl->a_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
+          const uint32_t fb = smem_addr(mixed ? &ctl->a_raw[s] : &ctl->a_full[s]);
+          mbar_arrive_expect_tx(fb, kABytes);
+          if (mixed) mbar_arrive_one(smem_addr(&ctl->a_full[s]));
+          tma_load_2d(sbase + (uint32_t)s * kABytes, &smap, ct * kCols, c * kTokens, fb);
+          tma_load_2d(sbase + (uint32_t)s * kABytes + kABytes / 2, &smap, ct * kCols + 64, c * kTokens, fb);
+        }
+        ++ai;
+        for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
+          const int s = zi % p.z_stages;
+          const uint32_t ph = (uint32_t)(zi / p.z_stages) & 1u;
+          if (zi >= p.z_stages && !gemm_wait(smem_addr(&ctl->z_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
+          ++zi;
+          const uint32_t fb = smem_addr(mixed ? &ctl->z_raw[s] : &ctl->z_full[s]);
+          mbar_arrive_expect_tx(fb, p.z_bytes);
+          if (mixed) mbar_arrive_one(smem_addr(&ctl->z_full[s]));
+          for (int b = 0; b * 64 < p.width; ++b)
+            tma_load_2d(zbase + (uint32_t)(s * p.z_bytes + b * 8192), &zmap, 64 * b, c * kTokens, fb);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      int ai = 0, zi = 0;
+      uint32_t a_phase = 0, z_phase = 0;   // bit s: parity of stage s's next patch
+      unsigned touched = 0;
+      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+        const unsigned in = info[c - c0];
+        if (in == 0) continue;
+        const bool mixed = in & kMixed;
+        const int s = ai % C::kAStages;
+        const uint32_t ph = (uint32_t)(ai / C::kAStages) & 1u;
+        ++ai;
+        if (CODES) {
+          if (!gemm_wait(smem_addr(&ctl->a_ready[s]), ph, abort_flag, p.status)) break;
+        } else {
+          if (!gemm_wait(smem_addr(&ctl->a_full[s]), ph, abort_flag, p.status)) break;
+          if (mixed) {
+            if (!gemm_wait(smem_addr(&ctl->a_ready[s]), (a_phase >> s) & 1u, abort_flag, p.status)) break;
+            a_phase ^= 1u << s;
+          }
+        }
+        const uint64_t ad = sw128_desc_mn(sbase + (uint32_t)s * kABytes, kABytes / 2);
+        for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
+          const int g = __ffs(left) - 1, zs = zi % p.z_stages;
+          const uint32_t zph = (uint32_t)(zi / p.z_stages) & 1u;
+          ++zi;
+          if (!gemm_wait(smem_addr(&ctl->z_full[zs]), zph, abort_flag, p.status)) break;
+          if (mixed) {
+            if (!gemm_wait(smem_addr(&ctl->z_ready[zs]), (z_phase >> zs) & 1u, abort_flag, p.status)) break;
+            z_phase ^= 1u << zs;
+          }
+          tc_fence_after();
+          const uint64_t bd = sw128_desc_mn(zbase + (uint32_t)(zs * p.z_bytes), 8192);
+#pragma unroll
+          for (int kk = 0; kk < kTokens / 16; ++kk)
+            tc_mma(tmem + (uint32_t)(g * p.group_cols), ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, p.idesc,
+                   kk > 0 || (touched >> g & 1u) ? 1u : 0u);
+          touched |= 1u << g;
+          tc_commit(smem_addr(&ctl->z_empty[zs]));
+        }
+        tc_commit(smem_addr(&ctl->a_empty[s]));
+      }
+      *(volatile unsigned*)&ctl->touched = touched;
+      mbar_arrive_one(smem_addr(&ctl->acc_full));
+      tc_commit(smem_addr(&ctl->acc_full));
+    }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------ codes and patches
+    const int thread = threadIdx.x - 192;
+    int ai = 0, zi = 0;
+    uint32_t a_phase = 0, z_phase = 0;
+    bool ok = true;
+    // codes: this thread's two runs of 16 columns (run, run + 4) of one token
+    const int token = thread & 63, run = thread >> 6;
+    auto steps_of = [&](int c) {
+      uint32_t two = 0;
+      const int t = c * kTokens + token;
+      if (CODES && c < c1 && t < p.m) {
+        const uint16_t* row = p.steps + (size_t)t * p.step_cols;
+        const int col = ct * kCols + 16 * run;
+        if (col < p.cols) two = ld_nc_u16(row + (col >> p.step_shift));
+        if (col + 64 < p.cols) two |= ld_nc_u16(row + ((col + 64) >> p.step_shift)) << 16;
+      }
+      return two;
+    };
+    uint32_t step_next = steps_of(c0);
+    for (int c = c0; c < c1 && ok && !*abort_flag; ++c) {
+      const unsigned in = info[c - c0];
+      const bool mixed = in & kMixed;
+      const uint32_t step = step_next;
+      step_next = steps_of(c + 1);
+      if (in == 0) continue;
+      const int s = ai % C::kAStages;
+      const uint32_t abase = sbase + (uint32_t)s * kABytes;
+      if (CODES) {
+        constexpr int kR = C::kRawStages > 0 ? C::kRawStages : 1;
+        const int rs = ai % kR;
+        ok = warp_wait(smem_addr(&ctl->code_full[rs]), (uint32_t)(ai / kR) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        if (ai >= C::kAStages) {
+          ok = warp_wait(smem_addr(&ctl->a_empty[s]), ((uint32_t)(ai / C::kAStages) & 1u) ^ 1u, abort_flag, p.status);
+          if (!ok) break;
+        }
+        bool bad = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t st = half ? step >> 16 : step & 0xFFFFu;
+          if (mixed && (st & 0x7F80u) == 0x7F80u) {   // a group that reads back as NaN
+            st = 0;
+            bad = true;
+          }
+          const uint32_t step2 = st | (st << 16);
+          const uint4 q = lds128(rbase + (uint32_t)(rs * kRawBytes + token * 128 + (((run + 4 * half) ^ (token & 7)) << 4)));
+          uint4 lo, hi;
+          act8_values4(q.x, step2, lo.x, lo.y);
+          act8_values4(q.y, step2, lo.z, lo.w);
+          act8_values4(q.z, step2, hi.x, hi.y);
+          act8_values4(q.w, step2, hi.z, hi.w);
+          const uint32_t row = abase + (uint32_t)(half * (kABytes / 2) + token * 128);
+          sts128(row + (uint32_t)(((2 * run) ^ (token & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
+          sts128(row + (uint32_t)(((2 * run + 1) ^ (token & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
+        }
+        if (bad) *(volatile int*)&ctl->spoilt = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
+          mbar_arrive_one(smem_addr(&ctl->code_empty[rs]));
+        }
+      } else if (mixed) {
+        ok = warp_wait(smem_addr(&ctl->a_raw[s]), (a_phase >> s) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        a_phase ^= 1u << s;
+        if (patch_finite(abase, kABytes, thread, kWorkThreads)) *(volatile int*)&ctl->spoilt = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
+      }
+      ++ai;
+      if (!mixed) {
+        ++zi;   // its one adapter
+        continue;
+      }
+      // four threads a token: its 16-byte pieces of each 64-column block
+      const int zt = thread >> 2, zq = thread & 3, t = c * kTokens + zt;
+      const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
+      for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
+        const int l = l_lo + __ffs(left) - 1;
+        const int zs = zi % p.z_stages;
+        ++zi;
+        ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        z_phase ^= 1u << zs;
+        if (mine != l) {
+          for (int b = 0; b * 64 < p.width; ++b) {
+            const uint32_t zrow = zbase + (uint32_t)(zs * p.z_bytes + b * 8192 + zt * 128);
+            sts128(zrow + 16u * zq, 0u, 0u, 0u, 0u);
+            sts128(zrow + 16u * (zq + 4), 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_one(smem_addr(&ctl->z_ready[zs]));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, row = 32 * q + lane, col = ct * kCols + row;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
+    gemm_wait(smem_addr(&ctl->acc_full), 0u, abort_flag, p.status);
+    wgrad_epilogue_sync();
+    if (row == 0) ctl->leave = *abort_flag;
+    wgrad_epilogue_sync();
+    if (!ctl->leave) {
+      tc_fence_after();
+      const unsigned touched = *(volatile unsigned*)&ctl->touched;
+      const int spoilt = *(volatile int*)&ctl->spoilt;
+      const size_t unit_floats = (size_t)p.per_pass * p.r16 * kCols;
+      float* part = p.partials + (size_t)unit * unit_floats + row;
+      for (int l = l_lo; l < l_hi; ++l) {
+        const int g = l - l_lo;
+        const bool has = touched >> g & 1u;
+        if (!has && p.splits > 1) continue;
+        for (int r0 = 0; r0 < p.r16; r0 += 16) {
+          float v[16] = {};
+          if (has) {
+            uint32_t a[16];
+            tc_ld_x16(tlane + (uint32_t)(g * p.group_cols + r0), a);
+            if (PAIRS) {
+              uint32_t b[16];
+              tc_ld_x16(tlane + (uint32_t)(g * p.group_cols + p.r16 + r0), b);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+            } else {
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
+            }
+            if (spoilt && col < p.cols) spoilt_sums<PAIRS>(p, c0, c1, l, col, r0, v);
+            __syncwarp();
+          }
+          if (p.splits > 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(part + ((size_t)g * p.r16 + r0 + i) * kCols, v[i]);
+          } else if (col < p.cols) {
+            store_grad<PAIRS>(p, l, col, r0, v);
+          }
+        }
+      }
+      if (p.splits > 1) {
+        if (row == 0) __stcg(p.masks + unit, touched);
+        __threadfence();
+        wgrad_epilogue_sync();
+        if (row == 0) ctl->last = atomicAdd(p.counters + tp, 1u) == (unsigned)(p.splits - 1);
+        wgrad_epilogue_sync();
+        if (ctl->last) {
+          __threadfence();
+          const unsigned* masks = p.masks + (size_t)tp * p.splits;
+          const float* base = p.partials + (size_t)tp * p.splits * unit_floats + row;
+          for (int l = l_lo; l < l_hi; ++l) {
+            const int g = l - l_lo;
+            for (int r0 = 0; r0 < p.r16; r0 += 16) {
+              float v[16] = {};
+              for (int sp = 0; sp < p.splits; ++sp) {
+                if (!(__ldcg(masks + sp) >> g & 1u)) continue;
+                const float* src = base + (size_t)sp * unit_floats + (size_t)(g * p.r16 + r0) * kCols;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += __ldcg(src + i * kCols);
+              }
+              if (col < p.cols) store_grad<PAIRS>(p, l, col, r0, v);
+            }
+          }
+          if (row == 0) p.counters[tp] = 0u;   // ready for the next call
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tc_free(tmem, p.tmem_cols);
+}
+
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done_mask.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done_mask.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// How m tokens, src columns and adapters with z columns `width` wide are cut up.
+struct WgradPlan {
+  int tiles, chunks, splits, passes, group_cols, per_pass;
+};
+WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
+  WgradPlan w;
+  w.tiles = (cols + kCols - 1) / kCols;
+  w.chunks = (m + kTokens - 1) / kTokens;
+  w.group_cols = (width + 31) / 32 * 32;
+  w.per_pass = 512 / w.group_cols;
+  if (w.per_pass > kMaxGroups) w.per_pass = kMaxGroups;
+  if (w.per_pass > adapters) w.per_pass = adapters;
+  w.passes = (adapters + w.per_pass - 1) / w.per_pass;
+  // shares of the chunks: one block per SM, two chunks each at least, and no
+  // more than the last block can add up quickly
+  const int units = w.tiles * w.passes;
+  int s = units < num_sms ? num_sms / units : 1;
+  if (s > w.chunks / 2) s = w.chunks / 2;
+  if (s > kMaxSplits) s = kMaxSplits;
+  w.splits = s < 1 ? 1 : s;
+  return w;
+}
+
+template <bool PAIRS, bool CODES>
+cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensorMap& zmap, void* space, int num_sms,
+                         cudaStream_t stream) {
+  const WgradPlan w = wgrad_plan(p.m, p.cols, p.ad.count, p.width, num_sms);
+  p.chunks = w.chunks;
+  p.splits = w.splits;
+  p.passes = w.passes;
+  p.group_cols = w.group_cols;
+  p.per_pass = w.per_pass;
+  p.r16 = rank16(p.ad.rank);
+  p.z_bytes = (p.width + 63) / 64 * 8192;
+  const int info_bytes = (int)align_up((size_t)(w.chunks + w.splits - 1) / w.splits * sizeof(unsigned), 16);
+  const int stages = (kZBudget - info_bytes) / p.z_bytes;
+  p.z_stages = stages < kMaxZStages ? stages : kMaxZStages;
+  p.idesc = tc_idesc(p.width, true, true);
+  p.tmem_cols = 32;
+  while ((int)p.tmem_cols < w.per_pass * w.group_cols) p.tmem_cols *= 2;
+  const size_t units = (size_t)w.tiles * w.passes * w.splits;
+  p.masks = static_cast<unsigned*>(space);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + align_up(units * sizeof(unsigned), kAlign));
+  cudaError_t e = allow_smem<adapter_wgrad_kernel<PAIRS, CODES>>(kWgradSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3(kWgradThreads);
+  cfg.dynamicSmemBytes = (size_t)WgradCfg<CODES>::kSrcBytes + (size_t)p.z_stages * p.z_bytes + info_bytes + kWgradFixed;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<PAIRS, CODES>, smap, zmap, p);
+}
+
+}  // namespace
+
+size_t wgrad_partials_bytes(int m, int cols, int adapters, int width, int num_sms) {
+  const WgradPlan w = wgrad_plan(m, cols, adapters, width, num_sms);
+  if (w.splits == 1) return 0;
+  const size_t units = (size_t)w.tiles * w.passes * w.splits;
+  const int r16 = width;   // at least the rows of a partial sum
+  return align_up(units * sizeof(unsigned), kAlign) + align_up(units * w.per_pass * r16 * kCols * sizeof(float), kAlign);
+}
+
+cudaError_t launch_da(const uint16_t* x, const int8_t* codes, const uint16_t* steps, int x_group, const uint16_t* pairs,
+                      const Adapters& ad, const SlotLists& lists, int m, int k, uint16_t* da, void* space,
+                      unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
+  WgradParams p{};
+  p.ad = ad;
+  p.lists = lists;
+  p.m = m;
+  p.cols = k;
+  p.width = 2 * rank16(ad.rank);
+  p.src = x;
+  p.codes = reinterpret_cast<const uint8_t*>(codes);
+  p.steps = steps;
+  p.z = pairs;
+  p.z_stride = p.width;
+  p.out = da;
+  p.counters = counters;
+  p.status = status;
+  CUtensorMap smap, zmap;
+  if (!encode_bf16_map(&zmap, pairs, m, p.width, kTokens)) return cudaErrorInvalidValue;
+  if (codes == nullptr) {
+    if (!encode_bf16_map(&smap, x, m, k, kTokens)) return cudaErrorInvalidValue;
+    return launch_wgrad<true, false>(p, smap, zmap, space, num_sms, stream);
+  }
+  while ((1 << p.step_shift) < x_group) ++p.step_shift;
+  p.step_cols = k >> p.step_shift;
+  if (!encode_u8_map(&smap, codes, m, k, kTokens)) return cudaErrorInvalidValue;
+  return launch_wgrad<true, true>(p, smap, zmap, space, num_sms, stream);
+}
+
+cudaError_t launch_db(const uint16_t* dy, const uint16_t* u, const Adapters& ad, const SlotLists& lists, int m, int n,
+                      uint16_t* db, void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
+  WgradParams p{};
+  p.ad = ad;
+  p.lists = lists;
+  p.m = m;
+  p.cols = n;
+  p.width = rank16(ad.rank);
+  p.src = dy;
+  p.z = u;
+  p.z_stride = ad.rank;
+  p.out = db;
+  p.counters = counters;
+  p.status = status;
+  CUtensorMap smap, zmap;
+  if (!encode_bf16_map(&smap, dy, m, n, kTokens) || !encode_bf16_map(&zmap, u, m, ad.rank, kTokens))
+    return cudaErrorInvalidValue;
+  return launch_wgrad<false, false>(p, smap, zmap, space, num_sms, stream);
+}
+
+}  // namespace any4

@@ -92,7 +92,8 @@ __device__ __forceinline__ void epilogue_sync() {
 // its adapters, with z zeroed in the rows of the other tokens. So that an
 // infinity or NaN in an adapter reaches none of those (0 times it is NaN), it
 // is taken out of M's tile as well, and the epilogue, told by `spoilt`, adds
-// its products for the adapter's own tokens in fp32. This patching runs on
+// its products for the adapter's own tokens in fp32 (where z is not finite
+// either, the result is NaN). This patching runs on
 // warps that idle otherwise; tiles of one adapter go straight from TMA to the
 // tensor core.
 struct NoLora {};
@@ -114,26 +115,6 @@ __device__ __forceinline__ Extra extra_stage(int r16, int h) {
   if (r16 <= 32) return {0, 0, r16 / 16, true};
   const int rank0 = 64 * (h >> 1);
   return {rank0, (h & 1) * r16 + rank0, min(4, (r16 - rank0) / 16), false};
-}
-
-__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in each half that is finite
-  const uint32_t bad = ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;   // magnitude >= 0x7F80
-  return ~((bad >> 15) * 0xFFFFu);
-}
-
-// Takes the infinities and NaN out of `bytes` of shared memory; true if this
-// thread found any.
-__device__ __forceinline__ bool patch_finite(uint32_t addr, int bytes, int thread, int threads) {
-  bool found = false;
-  for (int e = thread * 16; e < bytes; e += threads * 16) {
-    const uint4 v = lds128(addr + e);
-    const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
-    if ((a & b & c & d) != 0xFFFFFFFFu) {
-      sts128(addr + e, v.x & a, v.y & b, v.z & c, v.w & d);
-      found = true;
-    }
-  }
-  return found;
 }
 
 // What patch_finite took out of the products of token t and output row: the
@@ -241,14 +222,15 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         }
         if constexpr (LORA) {
           if (u % splits != splits - 1) continue;
-          bool mixed;
-          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          const SlotHead head = slot_head(lora.lists, mt);
+          const bool mixed = head.mixed;
+          const int per = extra_stages(lora.r16), count = head.count * per;
           for (int e = 0; e < count; ++e, ++it) {
             const int s = it % kStages;
             const uint32_t ph = (uint32_t)(it / kStages) & 1u;
             if (it >= kStages && !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
             const Extra ex = extra_stage(lora.r16, e % per);
-            const int l = slot_at(lora.lists, mt, e / per);
+            const int l = slot_at(lora.lists, mt, head, e / per);
             // a stage to be patched lands on a barrier of its own: the patching
             // warps see only those stages, so they cannot count the others
             const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
@@ -271,10 +253,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       int it = 0, tcount = 0;
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
-        [[maybe_unused]] bool mixed = false;
-        [[maybe_unused]] int slots = 0;
+        [[maybe_unused]] SlotHead head{0, 0, false};
         if constexpr (LORA)
-          if (u % splits == splits - 1) slots = slot_count(lora.lists, (u / splits) % m_tiles, mixed);
+          if (u % splits == splits - 1) head = slot_head(lora.lists, (u / splits) % m_tiles);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
@@ -296,10 +277,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         }
         if constexpr (LORA) {
           const int per = extra_stages(lora.r16);
-          for (int e = 0; e < slots * per; ++e, ++it) {
+          for (int e = 0; e < head.count * per; ++e, ++it) {
             const int s = it % kStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kStages) & 1u, abort_flag, status)) break;
-            if (mixed) {
+            if (head.mixed) {
               if (!gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)) break;
               patch_phase ^= 1u << s;
             }
@@ -329,8 +310,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         k_range(u, kc0, kc1);
         it += kc1 - kc0;
         if (u % splits != splits - 1) continue;
-        bool mixed;
-        const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+        const SlotHead head = slot_head(lora.lists, mt);
+        const bool mixed = head.mixed;
+        const int per = extra_stages(lora.r16), count = head.count * per;
         if (mixed) {
           int id[kBN / kPatchThreads];
 #pragma unroll
@@ -341,7 +323,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           bool ok = true;
           for (int e = 0; e < count && ok; ++e) {
             const int s = (it + e) % kStages;
-            const int l = slot_at(lora.lists, mt, e / per);
+            const int l = slot_at(lora.lists, mt, head, e / per);
             ok = __all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->raw[s]), (raw_phase >> s) & 1u, abort_flag, status));
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
@@ -655,8 +637,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (ok && u % splits == splits - 1) {
           asm volatile("griddepcontrol.wait;" ::: "memory");   // lists, ids and pairs are ready
           const int mt = (u / splits) % m_tiles, thread = threadIdx.x - 6 * 32;
-          bool mixed;
-          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          const SlotHead head = slot_head(lora.lists, mt);
+          const bool mixed = head.mixed;
+          const int per = extra_stages(lora.r16), count = head.count * per;
           const int t = mt * BN + thread;
           const int id = mixed && thread < BN && t < m ? adapter_of(lora.ad, t) : -1;
           for (int e = 0; e < count && ok; ++e) {
@@ -668,7 +651,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             if (!ok) break;   // the whole warp leaves
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->full[s]));
             if (!mixed) continue;
-            const int l = slot_at(lora.lists, mt, e / per);
+            const int l = slot_at(lora.lists, mt, head, e / per);
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
             if (patch_finite(sa(s), kAStageBytes, thread, 32 * kFusedDecoders)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
@@ -704,8 +687,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if constexpr (LORA) {
           if (u % splits != splits - 1) continue;
           const int nt = (u / splits) / m_tiles;
-          bool mixed;
-          const int per = extra_stages(lora.r16), count = slot_count(lora.lists, mt, mixed) * per;
+          const SlotHead head = slot_head(lora.lists, mt);
+          const int per = extra_stages(lora.r16), count = head.count * per;
           for (int e = 0; e < count; ++e, ++it) {
             const int s = it % kFusedStages;
             const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
@@ -713,7 +696,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             const Extra ex = extra_stage(lora.r16, e % per);
             const uint32_t fb = smem_addr(&ctl->full[s]);
             mbar_arrive_expect_tx(fb, C::kStage);
-            tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, slot_at(lora.lists, mt, e / per), fb);
+            tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, slot_at(lora.lists, mt, head, e / per), fb);
             tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * BN, fb);
           }
         }
@@ -726,10 +709,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       if (LORA) asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists are ready
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
-        [[maybe_unused]] bool mixed = false;
-        [[maybe_unused]] int slots = 0;
+        [[maybe_unused]] SlotHead head{0, 0, false};
         if constexpr (LORA)
-          if (u % splits == splits - 1) slots = slot_count(lora.lists, (u / splits) % m_tiles, mixed);
+          if (u % splits == splits - 1) head = slot_head(lora.lists, (u / splits) % m_tiles);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status)) break;
@@ -750,10 +732,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         }
         if constexpr (LORA) {
           const int per = extra_stages(lora.r16);
-          for (int e = 0; e < slots * per; ++e, ++it) {
+          for (int e = 0; e < head.count * per; ++e, ++it) {
             const int s = it % kFusedStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kFusedStages) & 1u, abort_flag, status)) break;
-            if (mixed) {
+            if (head.mixed) {
               if (!gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)) break;
               patch_phase ^= 1u << s;
             }

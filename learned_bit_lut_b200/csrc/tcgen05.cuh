@@ -164,10 +164,30 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t next_
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in each half that is finite
+  const uint32_t bad = ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;   // magnitude >= 0x7F80
+  return ~((bad >> 15) * 0xFFFFu);
+}
+
+// Takes the infinities and NaN out of `bytes` of shared memory; true if this
+// thread found any.
+__device__ __forceinline__ bool patch_finite(uint32_t addr, int bytes, int thread, int threads) {
+  bool found = false;
+  for (int e = thread * 16; e < bytes; e += threads * 16) {
+    const uint4 v = lds128(addr + e);
+    const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
+    if ((a & b & c & d) != 0xFFFFFFFFu) {
+      sts128(addr + e, v.x & a, v.y & b, v.z & c, v.w & d);
+      found = true;
+    }
+  }
+  return found;
+}
+
 // bf16 matrix of rows x cols (row-major) as 2-D boxes of box_rows x 64
 // columns, or a stack of depth such matrices as 3-D boxes of one each, with
 // the 128-byte swizzle; columns and rows past the end read as zero.
-// encode_u8_map: bytes, boxes of box_rows x 128 columns, no swizzle.
+// encode_u8_map: bytes, boxes of box_rows x 128 columns, 128-byte swizzle.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
 bool encode_bf16_map3(CUtensorMap* map, const void* base, int depth, int rows, int cols, int box_rows);
 bool encode_u8_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
