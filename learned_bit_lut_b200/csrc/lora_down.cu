@@ -17,7 +17,7 @@
 // contraction is split and the last block of a tile to arrive adds the
 // others' fp32 partials in order (deterministic).
 //
-// Warps: 0 = TMA, 1 = MMA, 2-5 = epilogue.
+// Warps: 0 = TMA of `in`, 1 = MMA, 2-5 = epilogue, 6 = TMA of the adapters.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -116,8 +116,8 @@ constexpr int kChunk = 64;                          // contraction columns per s
 constexpr int kXStages = 4;
 constexpr int kXBytes = kTileTokens * kChunk * 2;   // 16 KB
 constexpr int kMaxWStages = 16;
-constexpr int kWBudget = 128 * 1024;                // adapter stages
-constexpr int kDownTcThreads = 192;
+constexpr int kWBudget = 44 * 1024;                 // adapter stages: two blocks per SM
+constexpr int kDownTcThreads = 224;
 constexpr int kMaxTmemCols = 512;
 constexpr int kDownBar = 1;
 
@@ -176,7 +176,7 @@ __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, 
 }
 
 template <bool BACK>
-__global__ void __launch_bounds__(kDownTcThreads, 1)
+__global__ void __launch_bounds__(kDownTcThreads, 2)
     adapter_down_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                            const DownParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -220,54 +220,64 @@ __global__ void __launch_bounds__(kDownTcThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int xi = 0, wi = 0;
+      Ring r;
+      for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass) {
+        for (int kc = kc0; kc < kc1; ++kc) {
+          if (r.wrapped && !gemm_wait(smem_addr(&ctl->xempty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
+          const uint32_t xb = smem_addr(&ctl->xfull[r.s]);
+          mbar_arrive_expect_tx(xb, kXBytes);
+          tma_load_2d(sbase + (uint32_t)r.s * kXBytes, &xmap, kc * kChunk, tile * kTileTokens, xb);
+          r.next(kXStages);
+        }
+      }
+    }
+  } else if (warp == 6) {
+    if (lane == 0) {
+      Ring r;
+      const int w_stages = p.w_stages, w_bytes = p.w_bytes;
       for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass) {
         const int j1 = min(count, j0 + per_pass);
-        for (int kc = kc0; kc < kc1; ++kc, ++xi) {
-          const int xs = xi % kXStages;
-          if (xi >= kXStages && !gemm_wait(smem_addr(&ctl->xempty[xs]), ((uint32_t)(xi / kXStages) & 1u) ^ 1u, abort_flag,
-                                           p.status))
-            break;
-          const uint32_t xb = smem_addr(&ctl->xfull[xs]);
-          mbar_arrive_expect_tx(xb, kXBytes);
-          tma_load_2d(sbase + (uint32_t)xs * kXBytes, &xmap, kc * kChunk, tile * kTileTokens, xb);
-          for (int j = j0; j < j1; ++j, ++wi) {
-            const int ws = wi % p.w_stages;
-            if (wi >= p.w_stages && !gemm_wait(smem_addr(&ctl->wempty[ws]), ((uint32_t)(wi / p.w_stages) & 1u) ^ 1u,
-                                               abort_flag, p.status))
-              break;
-            const uint32_t wb = smem_addr(&ctl->wfull[ws]), dst = wbase + (uint32_t)ws * p.w_bytes;
-            mbar_arrive_expect_tx(wb, p.w_bytes);
+        for (int kc = kc0; kc < kc1 && !*abort_flag; ++kc) {
+          for (int j = j0; j < j1; ++j) {
+            if (r.wrapped && !gemm_wait(smem_addr(&ctl->wempty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
+            const uint32_t wb = smem_addr(&ctl->wfull[r.s]), dst = wbase + (uint32_t)(r.s * w_bytes);
+            mbar_arrive_expect_tx(wb, w_bytes);
             if (!BACK) {
               tma_load_3d(dst, &wmap, kc * kChunk, 0, ctl->slots[j], wb);
             } else {
               for (int b = 0; b * 64 < r16; ++b) tma_load_3d(dst + b * 8192, &wmap, 64 * b, kc * kChunk, ctl->slots[j], wb);
             }
+            r.next(w_stages);
           }
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      int xi = 0, wi = 0, pass = 0;
+      Ring rx, rw;
+      const int w_stages = p.w_stages, w_bytes = p.w_bytes;
+      const uint32_t idesc = p.idesc;
+      int pass = 0;
       for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass, ++pass) {
         const int j1 = min(count, j0 + per_pass);
         if (pass > 0 && !gemm_wait(smem_addr(&ctl->acc_empty), (uint32_t)(pass - 1) & 1u, abort_flag, p.status)) break;
         tc_fence_after();
-        for (int kc = kc0; kc < kc1 && !*abort_flag; ++kc, ++xi) {
-          const int xs = xi % kXStages;
-          if (!gemm_wait(smem_addr(&ctl->xfull[xs]), (uint32_t)(xi / kXStages) & 1u, abort_flag, p.status)) break;
+        for (int kc = kc0; kc < kc1 && !*abort_flag; ++kc) {
+          const int xs = rx.s;
+          if (!gemm_wait(smem_addr(&ctl->xfull[xs]), rx.parity, abort_flag, p.status)) break;
+          rx.next(kXStages);
           const uint64_t ad = sw128_desc(sbase + (uint32_t)xs * kXBytes);
-          for (int j = j0; j < j1; ++j, ++wi) {
-            const int ws = wi % p.w_stages;
-            if (!gemm_wait(smem_addr(&ctl->wfull[ws]), (uint32_t)(wi / p.w_stages) & 1u, abort_flag, p.status)) break;
+          for (int j = j0; j < j1; ++j) {
+            const int ws = rw.s;
+            if (!gemm_wait(smem_addr(&ctl->wfull[ws]), rw.parity, abort_flag, p.status)) break;
+            rw.next(w_stages);
             tc_fence_after();
-            const uint32_t waddr = wbase + (uint32_t)ws * p.w_bytes;
+            const uint32_t waddr = wbase + (uint32_t)(ws * w_bytes);
             const uint64_t bd = BACK ? sw128_desc_mn(waddr, 8192) : sw128_desc(waddr);
 #pragma unroll
             for (int kk = 0; kk < kChunk / 16; ++kk)
               tc_mma(tmem + (uint32_t)((j - j0) * group_cols), ad + 2u * (uint64_t)kk, bd + (BACK ? 128u : 2u) * (uint64_t)kk,
-                     p.idesc, kc > kc0 || kk > 0 ? 1u : 0u);
+                     idesc, kc > kc0 || kk > 0 ? 1u : 0u);
             tc_commit(smem_addr(&ctl->wempty[ws]));
           }
           tc_commit(smem_addr(&ctl->xempty[xs]));
@@ -380,7 +390,7 @@ static_assert(sizeof(DownCtl) <= 2048, "control block");
 
 int down_splits(int m, int cols, int num_sms) {
   const int tiles = (m + kTileTokens - 1) / kTileTokens, chunks = (cols + kChunk - 1) / kChunk;
-  int s = num_sms / tiles;
+  int s = 2 * num_sms / tiles;          // two blocks per SM
   if (s > chunks / 2) s = chunks / 2;   // two chunks a block at least
   if (s > 16) s = 16;                   // the last block reads all partials
   return s < 1 ? 1 : s;

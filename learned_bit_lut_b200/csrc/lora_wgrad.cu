@@ -25,7 +25,8 @@
 // tensor memory holds (512 columns). Shares of the chunks are added by the
 // last block to arrive, in order.
 //
-// Warps: 0 = TMA, 1 = MMA, 2-5 = epilogue, 6-13 = codes and patches.
+// Warps: 0 = TMA of src, 1 = MMA, 2-5 = epilogue, 6-13 = codes and patches,
+// 14 = TMA of z.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -44,19 +45,20 @@ constexpr int kABytes = kTokens * kCols * 2;     // a chunk of src in bf16: two 
 constexpr int kRawBytes = kTokens * kCols;       // the same in codes
 constexpr int kWorkers = 8;
 constexpr int kWorkThreads = kWorkers * 32;
-constexpr int kWgradThreads = 192 + kWorkThreads;
-constexpr int kZBudget = 100 * 1024;
+constexpr int kWgradThreads = 192 + kWorkThreads + 32;
+constexpr int kZBudget = 132 * 1024;             // z stages and chunk masks, one block per SM
+constexpr int kZBudgetTwo = 44 * 1024;           // the same for two blocks per SM
 constexpr int kMaxZStages = 8;
 constexpr int kWgradBar = 1;
 constexpr int kMaxGroups = 16;                   // adapters per block: 512 columns / 32
 
 template <bool CODES>
 struct WgradCfg {
-  static constexpr int kAStages = CODES ? 3 : 6;
-  static constexpr int kRawStages = CODES ? 6 : 0;
-  static constexpr int kSrcBytes = kAStages * kABytes + kRawStages * kRawBytes;   // 96 KB both
+  static constexpr int kAStages = CODES ? 2 : 4;
+  static constexpr int kRawStages = CODES ? 4 : 0;
+  static constexpr int kSrcBytes = kAStages * kABytes + kRawStages * kRawBytes;   // 64 KB both
 };
-constexpr int kMaxAStages = 6, kMaxRawStages = 6;
+constexpr int kMaxAStages = 4, kMaxRawStages = 4;
 constexpr int kMaxSplits = 16;
 constexpr int kWgradFixed = 1024 + 1024;         // control, alignment
 constexpr int kWgradSmem = WgradCfg<false>::kSrcBytes + kZBudget + kWgradFixed;
@@ -167,7 +169,7 @@ __device__ __forceinline__ void store_grad(const WgradParams& p, int l, int col,
 // PAIRS: z is a bf16 pair and the result dA; else z is u and the result dB.
 // CODES: src is an 8-bit checkpoint.
 template <bool PAIRS, bool CODES>
-__global__ void __launch_bounds__(kWgradThreads, 1)
+__global__ void __launch_bounds__(kWgradThreads, 2)
     adapter_wgrad_kernel(const __grid_constant__ CUtensorMap smap, const __grid_constant__ CUtensorMap zmap,
                          const __grid_constant__ WgradParams p) {
   using C = WgradCfg<CODES>;
@@ -229,58 +231,68 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
 
   // Every role walks the chunks, and a chunk's adapters (the bits of its mask
   // in ascending order), alike.
+  constexpr int kSrcStages = CODES ? C::kRawStages : C::kAStages;
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA
+    // ------------------------------------------------------------ TMA of src
     if (lane == 0) {
-      int ai = 0, zi = 0;
+      Ring r;
       for (int c = c0; c < c1 && !*abort_flag; ++c) {
         const unsigned in = info[c - c0];
         if (in == 0) continue;
-        const bool mixed = in & kMixed;
+        const int s = r.s;
+        if (r.wrapped &&
+            !gemm_wait(smem_addr(CODES ? &ctl->code_empty[s] : &ctl->a_empty[s]), r.parity ^ 1u, abort_flag, p.status))
+          break;
         if (CODES) {
-          const int s = ai % (C::kRawStages > 0 ? C::kRawStages : 1);
-          const uint32_t ph = (uint32_t)(ai / (C::kRawStages > 0 ? C::kRawStages : 1)) & 1u;
-          if (ai >= C::kRawStages && !gemm_wait(smem_addr(&ctl->code_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
           const uint32_t fb = smem_addr(&ctl->code_full[s]);
           mbar_arrive_expect_tx(fb, kRawBytes);
           tma_load_2d(rbase + (uint32_t)s * kRawBytes, &smap, ct * kCols, c * kTokens, fb);
         } else {
-          const int s = ai % C::kAStages;
-          const uint32_t ph = (uint32_t)(ai / C::kAStages) & 1u;
-          if (ai >= C::kAStages && !gemm_wait(smem_addr(&ctl->a_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
+          const bool mixed = in & kMixed;
           const uint32_t fb = smem_addr(mixed ? &ctl->a_raw[s] : &ctl->a_full[s]);
           mbar_arrive_expect_tx(fb, kABytes);
           if (mixed) mbar_arrive_one(smem_addr(&ctl->a_full[s]));
           tma_load_2d(sbase + (uint32_t)s * kABytes, &smap, ct * kCols, c * kTokens, fb);
           tma_load_2d(sbase + (uint32_t)s * kABytes + kABytes / 2, &smap, ct * kCols + 64, c * kTokens, fb);
         }
-        ++ai;
+        r.next(kSrcStages);
+      }
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------------------ TMA of z
+    if (lane == 0) {
+      Ring r;
+      const int z_stages = p.z_stages, z_bytes = p.z_bytes, width = p.width;
+      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+        const unsigned in = info[c - c0];
+        const bool mixed = in & kMixed;
         for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
-          const int s = zi % p.z_stages;
-          const uint32_t ph = (uint32_t)(zi / p.z_stages) & 1u;
-          if (zi >= p.z_stages && !gemm_wait(smem_addr(&ctl->z_empty[s]), ph ^ 1u, abort_flag, p.status)) break;
-          ++zi;
+          const int s = r.s;
+          if (r.wrapped && !gemm_wait(smem_addr(&ctl->z_empty[s]), r.parity ^ 1u, abort_flag, p.status)) break;
           const uint32_t fb = smem_addr(mixed ? &ctl->z_raw[s] : &ctl->z_full[s]);
-          mbar_arrive_expect_tx(fb, p.z_bytes);
+          mbar_arrive_expect_tx(fb, z_bytes);
           if (mixed) mbar_arrive_one(smem_addr(&ctl->z_full[s]));
-          for (int b = 0; b * 64 < p.width; ++b)
-            tma_load_2d(zbase + (uint32_t)(s * p.z_bytes + b * 8192), &zmap, 64 * b, c * kTokens, fb);
+          for (int b = 0; b * 64 < width; ++b)
+            tma_load_2d(zbase + (uint32_t)(s * z_bytes + b * 8192), &zmap, 64 * b, c * kTokens, fb);
+          r.next(z_stages);
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
-      int ai = 0, zi = 0;
+      Ring ra, rz;
+      const int z_stages = p.z_stages, z_bytes = p.z_bytes, group_cols = p.group_cols;
+      const uint32_t idesc = p.idesc;
       uint32_t a_phase = 0, z_phase = 0;   // bit s: parity of stage s's next patch
       unsigned touched = 0;
       for (int c = c0; c < c1 && !*abort_flag; ++c) {
         const unsigned in = info[c - c0];
         if (in == 0) continue;
         const bool mixed = in & kMixed;
-        const int s = ai % C::kAStages;
-        const uint32_t ph = (uint32_t)(ai / C::kAStages) & 1u;
-        ++ai;
+        const int s = ra.s;
+        const uint32_t ph = ra.parity;
+        ra.next(C::kAStages);
         if (CODES) {
           if (!gemm_wait(smem_addr(&ctl->a_ready[s]), ph, abort_flag, p.status)) break;
         } else {
@@ -292,19 +304,19 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
         }
         const uint64_t ad = sw128_desc_mn(sbase + (uint32_t)s * kABytes, kABytes / 2);
         for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
-          const int g = __ffs(left) - 1, zs = zi % p.z_stages;
-          const uint32_t zph = (uint32_t)(zi / p.z_stages) & 1u;
-          ++zi;
+          const int g = __ffs(left) - 1, zs = rz.s;
+          const uint32_t zph = rz.parity;
+          rz.next(z_stages);
           if (!gemm_wait(smem_addr(&ctl->z_full[zs]), zph, abort_flag, p.status)) break;
           if (mixed) {
             if (!gemm_wait(smem_addr(&ctl->z_ready[zs]), (z_phase >> zs) & 1u, abort_flag, p.status)) break;
             z_phase ^= 1u << zs;
           }
           tc_fence_after();
-          const uint64_t bd = sw128_desc_mn(zbase + (uint32_t)(zs * p.z_bytes), 8192);
+          const uint64_t bd = sw128_desc_mn(zbase + (uint32_t)(zs * z_bytes), 8192);
 #pragma unroll
           for (int kk = 0; kk < kTokens / 16; ++kk)
-            tc_mma(tmem + (uint32_t)(g * p.group_cols), ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, p.idesc,
+            tc_mma(tmem + (uint32_t)(g * group_cols), ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, idesc,
                    kk > 0 || (touched >> g & 1u) ? 1u : 0u);
           touched |= 1u << g;
           tc_commit(smem_addr(&ctl->z_empty[zs]));
@@ -315,10 +327,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       mbar_arrive_one(smem_addr(&ctl->acc_full));
       tc_commit(smem_addr(&ctl->acc_full));
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 6) {   // 6 .. 13
     // ------------------------------------------------------------ codes and patches
     const int thread = threadIdx.x - 192;
-    int ai = 0, zi = 0;
+    Ring ra, rc, rz;
+    const int z_stages = p.z_stages;
     uint32_t a_phase = 0, z_phase = 0;
     bool ok = true;
     // codes: this thread's two runs of 16 columns (run, run + 4) of one token
@@ -341,17 +354,17 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       const uint32_t step = step_next;
       step_next = steps_of(c + 1);
       if (in == 0) continue;
-      const int s = ai % C::kAStages;
+      const int s = ra.s;
       const uint32_t abase = sbase + (uint32_t)s * kABytes;
       if (CODES) {
-        constexpr int kR = C::kRawStages > 0 ? C::kRawStages : 1;
-        const int rs = ai % kR;
-        ok = warp_wait(smem_addr(&ctl->code_full[rs]), (uint32_t)(ai / kR) & 1u, abort_flag, p.status);
+        const int rs = rc.s;
+        ok = warp_wait(smem_addr(&ctl->code_full[rs]), rc.parity, abort_flag, p.status);
         if (!ok) break;
-        if (ai >= C::kAStages) {
-          ok = warp_wait(smem_addr(&ctl->a_empty[s]), ((uint32_t)(ai / C::kAStages) & 1u) ^ 1u, abort_flag, p.status);
+        if (ra.wrapped) {
+          ok = warp_wait(smem_addr(&ctl->a_empty[s]), ra.parity ^ 1u, abort_flag, p.status);
           if (!ok) break;
         }
+        rc.next(kSrcStages);
         bool bad = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -387,9 +400,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
       }
-      ++ai;
+      ra.next(C::kAStages);
       if (!mixed) {
-        ++zi;   // its one adapter
+        rz.next(z_stages);   // its one adapter
         continue;
       }
       // four threads a token: its 16-byte pieces of each 64-column block
@@ -397,8 +410,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
       for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
         const int l = l_lo + __ffs(left) - 1;
-        const int zs = zi % p.z_stages;
-        ++zi;
+        const int zs = rz.s;
+        rz.next(z_stages);
         ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
         if (!ok) break;
         z_phase ^= 1u << zs;
@@ -519,10 +532,10 @@ WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
   if (w.per_pass > kMaxGroups) w.per_pass = kMaxGroups;
   if (w.per_pass > adapters) w.per_pass = adapters;
   w.passes = (adapters + w.per_pass - 1) / w.per_pass;
-  // shares of the chunks: one block per SM, two chunks each at least, and no
+  // shares of the chunks: two blocks per SM, two chunks each at least, and no
   // more than the last block can add up quickly
   const int units = w.tiles * w.passes;
-  int s = units < num_sms ? num_sms / units : 1;
+  int s = units < 2 * num_sms ? 2 * num_sms / units : 1;
   if (s > w.chunks / 2) s = w.chunks / 2;
   if (s > kMaxSplits) s = kMaxSplits;
   w.splits = s < 1 ? 1 : s;
@@ -541,7 +554,10 @@ cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensor
   p.r16 = rank16(p.ad.rank);
   p.z_bytes = (p.width + 63) / 64 * 8192;
   const int info_bytes = (int)align_up((size_t)(w.chunks + w.splits - 1) / w.splits * sizeof(unsigned), 16);
-  const int stages = (kZBudget - info_bytes) / p.z_bytes;
+  // two blocks per SM where two z stages fit: the issuing threads bound a
+  // block, at ~1000 cycles a chunk
+  int stages = (kZBudgetTwo - info_bytes) / p.z_bytes;
+  if (stages < 2) stages = (kZBudget - info_bytes) / p.z_bytes;
   p.z_stages = stages < kMaxZStages ? stages : kMaxZStages;
   p.idesc = tc_idesc(p.width, true, true);
   p.tmem_cols = 32;

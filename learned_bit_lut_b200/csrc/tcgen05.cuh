@@ -26,14 +26,30 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// Position in a ring of `stages` buffers: the buffer, and the parity of the
+// phase that its full barrier completes next (a division per step would cost
+// the issuing thread more than the step).
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  bool wrapped = false;   // buffers are in their second use or later
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+      wrapped = true;
+    }
+  }
+};
+
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait; false when the block is aborting or the wait timed out.
-__device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait; false when the block is aborting or the wait timed out. The
+// waiting loop is a call, so that the path of a barrier that is ready stays
+// short: the issuing threads run from the instruction cache or not at all.
+static __device__ __noinline__ bool gemm_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -44,6 +60,10 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatil
       return false;
     }
   }
+}
+__device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned* status) {
+  return mbar_try_wait(bar, parity) || gemm_wait_loop(bar, parity, abort_flag, status);
 }
 
 // gemm_wait for warps that wait long (a whole tile) and must not take issue
