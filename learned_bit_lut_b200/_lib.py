@@ -9,6 +9,7 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -300,12 +301,11 @@ def noalloc_status(device: torch.device | None = None) -> int:
     """The status word of any4_linear_noalloc on ``device`` (0: the last call
     completed normally). Synchronizes that device before reading it."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    with torch.cuda.device(dev):
-        ptr = _p()
-        _check(lib.any4_noalloc_status_word(ctypes.byref(ptr)))
-        torch.cuda.synchronize(dev)
-        word = torch.as_tensor(_DeviceWord(ptr.value), device=dev)
-        return int(word.view(torch.int32).item()) & 0xFFFFFFFF
+    ptr = _p()
+    _check(lib.any4_noalloc_status_word(ctypes.byref(ptr)))
+    torch.cuda.synchronize(dev)
+    word = torch.as_tensor(_DeviceWord(ptr.value), device=dev)
+    return int(word.view(torch.int32).item()) & 0xFFFFFFFF
 
 
 def any4_quantize(w: torch.Tensor, ex: torch.Tensor, group: int, bits: int = 4,
@@ -361,6 +361,9 @@ def any4_pack_format(fmt, idx_nib: torch.Tensor, alpha: torch.Tensor, beta: torc
 
 def _typed(t: torch.Tensor, name: str, dtypes, device: torch.device, shape) -> int:
     """Pointer of a contiguous CUDA tensor of one of ``dtypes`` on ``device``."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -369,13 +372,39 @@ def _typed(t: torch.Tensor, name: str, dtypes, device: torch.device, shape) -> i
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values, or their bit patterns
 _BYTES = (torch.uint8,)
+_INT8, _INT32, _FP32 = (torch.int8,), (torch.int32,), (torch.float32,)
+_HEADER_BYTES = lib.any4_lora_header_bytes()
+
+
+def _on_device(call):
+    """Runs ``call`` with its first tensor's device current (the library
+    launches on the current device)."""
+    @functools.wraps(call)
+    def run(first, *args, **kwargs):
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return call(first, *args, **kwargs)
+        return call(first, *args, **kwargs)
+    return run
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_need(device: int, *shape: int) -> int:
+    """any4_lora_workspace_bytes of a shape (it depends on the device's SM count)."""
+    return lib.any4_lora_workspace_bytes(*shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _grad_need(device: int, *shape: int) -> int:
+    return lib.any4_lora_grad_workspace_bytes(*shape)
+
+
+_packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_bytes_bits(*shape))
 _LORA_WORKSPACES: dict = {}
 
 
@@ -388,17 +417,17 @@ def _rows(t: torch.Tensor, name: str) -> int:
 def _adapter_workspace(need: int, device: torch.device) -> torch.Tensor:
     """A workspace with a zeroed header: kept per stream and grown on demand,
     or, while a CUDA graph is captured, one of the graph's own."""
-    header = lib.any4_lora_header_bytes()
-    if torch.cuda.is_current_stream_capturing():
+    if need == 0:
+        raise Any4Error(ANY4_ESHAPE)
+    if not torch.cuda.is_current_stream_capturing():
+        key = (device.index, _stream(device))
+        ws = _LORA_WORKSPACES.get(key)
+        if ws is not None and ws.numel() >= need:
+            return ws
+        ws = _LORA_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
-        ws[:header].zero_()
-        return ws
-    key = (device.index, _stream(device))
-    ws = _LORA_WORKSPACES.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        ws[:header].zero_()
-        _LORA_WORKSPACES[key] = ws
+    ws[:_HEADER_BYTES].zero_()
     return ws
 
 
@@ -408,15 +437,15 @@ def _adapters(a, b, scale, ids, m: int, n: int, k: int, device: torch.device):
         raise ValueError("a must be a tensor of shape (adapters, rank, K)")
     count, rank = a.shape[0], a.shape[1]
     return (_typed(a, "a", _BF16, device, (count, rank, k)), _typed(b, "b", _BF16, device, (count, n, rank)),
-            _typed(scale, "scale", (torch.float32,), device, (count,)),
-            None if ids is None else _typed(ids, "ids", (torch.int32,), device, (m,)), count, rank)
+            _typed(scale, "scale", _FP32, device, (count,)),
+            None if ids is None else _typed(ids, "ids", _INT32, device, (m,)), count, rank)
 
 
 def _weight(packed, n: int, k: int, group: int, bits: int, device: torch.device) -> int:
     """Pointer of a packed weight that is large enough for its shape."""
     if not isinstance(packed, torch.Tensor):
         raise ValueError("packed must be a CUDA tensor")
-    need = lib.any4_packed_bytes_bits(bits, n, k, group)
+    need = _packed_need(bits, n, k, group)
     if need == 0:
         raise Any4Error(ANY4_ESHAPE)
     if packed.numel() < need:
@@ -433,6 +462,7 @@ def any4_lora_grad_workspace_bytes(m: int, n: int, k: int, group: int, adapters:
     return lib.any4_lora_grad_workspace_bytes(bits, m, n, k, group, adapters, rank)
 
 
+@_on_device
 def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, group: int, a: torch.Tensor,
                      b: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor | None = None, bits: int = 4,
                      out: torch.Tensor | None = None, u: torch.Tensor | None = None,
@@ -444,23 +474,20 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
     ``u`` (M x R bf16) is written where given, for any4_linear_lora_grad."""
     m = _rows(x, "x")
     dev = x.device
-    with torch.cuda.device(dev):
-        ad = _adapters(a, b, scale, ids, m, n, k, dev)
-        if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            need = lib.any4_lora_workspace_bytes(bits, m, n, k, group, ad[4], ad[5])
-            if need == 0:
-                raise Any4Error(ANY4_ESHAPE)
-            workspace = _adapter_workspace(need, dev)
-        _check(lib.any4_linear_lora(
-            bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k,
-            group, *ad, _typed(out, "out", _BF16, dev, (m, n)),
-            None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5])),
-            _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), _stream(dev)))
+    ad = _adapters(a, b, scale, ids, m, n, k, dev)
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev)
+    _check(lib.any4_linear_lora(
+        bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k,
+        group, *ad, _typed(out, "out", _BF16, dev, (m, n)),
+        None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5])),
+        _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), _stream(dev)))
     return out
 
 
+@_on_device
 def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: torch.Tensor | None, n: int, k: int,
                           group: int, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
                           ids: torch.Tensor | None = None, bits: int = 4,
@@ -476,49 +503,46 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
     unknown = set(outputs) - {"dx", "da", "db"}
     if unknown or not outputs:
         raise ValueError(f"outputs must name some of dx, da and db, got {tuple(outputs)}")
-    with torch.cuda.device(dev):
-        ad = _adapters(a, b, scale, ids, m, n, k, dev)
-        count, rank = ad[4], ad[5]
+    ad = _adapters(a, b, scale, ids, m, n, k, dev)
+    count, rank = ad[4], ad[5]
 
-        def made(name, t, shape):
-            if name not in outputs:
-                if t is not None:
-                    raise ValueError(f"{name} was given but is not among the outputs")
-                return None, None
-            if t is None:
-                t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            return t, _typed(t, name, _BF16, dev, shape)
+    def made(name, t, shape):
+        if name not in outputs:
+            if t is not None:
+                raise ValueError(f"{name} was given but is not among the outputs")
+            return None, None
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        return t, _typed(t, name, _BF16, dev, shape)
 
-        dx, dx_p = made("dx", dx, (m, k))
-        da, da_p = made("da", da, (count, rank, k))
-        db, db_p = made("db", db, (count, n, rank))
-        x_p = codes_p = steps_p = None
-        x_group = 0
-        if da is not None:
-            if isinstance(x, (tuple, list)):
-                codes, steps = x
-                groups = steps.shape[1] if isinstance(steps, torch.Tensor) and steps.dim() == 2 else 0
-                if groups < 1 or k % groups:
-                    raise ValueError("steps must be a tensor of shape (M, K / group)")
-                x_group = k // groups
-                codes_p = _typed(codes, "codes", (torch.int8,), dev, (m, k))
-                steps_p = _typed(steps, "steps", _BF16, dev, (m, groups))
-            else:
-                x_p = _typed(x, "x", _BF16, dev, (m, k))
-        u_p = _typed(u, "u", _BF16, dev, (m, rank)) if db is not None else None
-        w_p = _weight(packed, n, k, group, bits, dev) if dx is not None else None
-        if workspace is None:
-            need = lib.any4_lora_grad_workspace_bytes(bits, m, n, k, group, count, rank)
-            if need == 0:
-                raise Any4Error(ANY4_ESHAPE)
-            workspace = _adapter_workspace(need, dev)
-        _check(lib.any4_linear_lora_grad(
-            bits, _typed(dy, "dy", _BF16, dev, (m, n)), x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad,
-            dx_p, da_p, db_p, _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
-            _stream(dev)))
+    dx, dx_p = made("dx", dx, (m, k))
+    da, da_p = made("da", da, (count, rank, k))
+    db, db_p = made("db", db, (count, n, rank))
+    x_p = codes_p = steps_p = None
+    x_group = 0
+    if da is not None:
+        if isinstance(x, (tuple, list)):
+            codes, steps = x
+            groups = steps.shape[1] if isinstance(steps, torch.Tensor) and steps.dim() == 2 else 0
+            if groups < 1 or k % groups:
+                raise ValueError("steps must be a tensor of shape (M, K / group)")
+            x_group = k // groups
+            codes_p = _typed(codes, "codes", _INT8, dev, (m, k))
+            steps_p = _typed(steps, "steps", _BF16, dev, (m, groups))
+        else:
+            x_p = _typed(x, "x", _BF16, dev, (m, k))
+    u_p = _typed(u, "u", _BF16, dev, (m, rank)) if db is not None else None
+    w_p = _weight(packed, n, k, group, bits, dev) if dx is not None else None
+    if workspace is None:
+        workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev)
+    _check(lib.any4_linear_lora_grad(
+        bits, _typed(dy, "dy", _BF16, dev, (m, n)), x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad,
+        dx_p, da_p, db_p, _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
+        _stream(dev)))
     return dx, da, db
 
 
+@_on_device
 def any4_act_pack(x: torch.Tensor, group: int, codes: torch.Tensor | None = None,
                   steps: torch.Tensor | None = None) -> tuple:
     """8-bit checkpoint of an activation x (M x K bf16): (codes, steps), one
@@ -527,17 +551,17 @@ def any4_act_pack(x: torch.Tensor, group: int, codes: torch.Tensor | None = None
     k, dev = x.shape[1], x.device
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
-    with torch.cuda.device(dev):
-        if codes is None:
-            codes = torch.empty((m, k), dtype=torch.int8, device=dev)
-        if steps is None:
-            steps = torch.empty((m, k // group), dtype=torch.bfloat16, device=dev)
-        _check(lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group,
-                                 _typed(codes, "codes", (torch.int8,), dev, (m, k)),
-                                 _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev)))
+    if codes is None:
+        codes = torch.empty((m, k), dtype=torch.int8, device=dev)
+    if steps is None:
+        steps = torch.empty((m, k // group), dtype=torch.bfloat16, device=dev)
+    _check(lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group,
+                             _typed(codes, "codes", _INT8, dev, (m, k)),
+                             _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev)))
     return codes, steps
 
 
+@_on_device
 def any4_act_unpack(codes: torch.Tensor, steps: torch.Tensor, group: int,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """The bf16 values (M x K) an 8-bit checkpoint stands for."""
@@ -545,12 +569,11 @@ def any4_act_unpack(codes: torch.Tensor, steps: torch.Tensor, group: int,
     k, dev = codes.shape[1], codes.device
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
-        _check(lib.any4_act_unpack(_typed(codes, "codes", (torch.int8,), dev, (m, k)),
-                                   _typed(steps, "steps", _BF16, dev, (m, k // group)), m, k, group,
-                                   _typed(out, "out", _BF16, dev, (m, k)), _stream(dev)))
+    if out is None:
+        out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+    _check(lib.any4_act_unpack(_typed(codes, "codes", _INT8, dev, (m, k)),
+                               _typed(steps, "steps", _BF16, dev, (m, k // group)), m, k, group,
+                               _typed(out, "out", _BF16, dev, (m, k)), _stream(dev)))
     return out
 
 

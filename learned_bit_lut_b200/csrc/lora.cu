@@ -5,13 +5,19 @@
 //
 // where many requests share W_hat and each brings its own (A_l, B_l, s_l).
 //
-// M <= 16 (decode): two small kernels ahead of the any4 decode kernel, each
-// launched as a programmatic dependent of the one before. adapter_down_kernel
-// gives every (token, rank row) its own thread block, so one token's R x K
-// matrix is read by R SMs at once; adapter_up_kernel writes the fp32 term
-// u . B^T, which the decode kernel adds to its own fp32 sums before their one
-// rounding. The adapters' bytes are few beside the weight's, so these kernels
-// are bound by latency: the decode kernel's weight prologue runs under them.
+// M <= 16 (decode): one small kernel writes the fp32 term u . B^T, which the
+// any4 decode kernel adds to its own fp32 sums before their one rounding. The
+// adapters' bytes are few beside the weight's, so it is bound by latency: a
+// cluster of 8 thread blocks takes a token (or 4096 of its output rows), its
+// blocks share the R rows of A_l, exchange the sums through distributed
+// shared memory and share the output rows. The decode kernel is its
+// programmatic dependent, launched once x is complete, and runs beside it: it
+// waits for the term only before its stores.
+//
+// M > 16: the lists of the adapters in each token tile and u = s x . A^T on
+// the tensor cores (lora_down.cu), then the prefill GEMM with u . B^T as R
+// more columns of its contraction (prefill.cu): y is written once and the
+// term costs R / K of the GEMM and no pass over y of its own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,8 +31,10 @@ namespace any4 {
 
 namespace {
 
-constexpr int kDownThreads = 128;
-constexpr int kUpThreads = 256;
+constexpr int kDeltaThreads = 256;
+constexpr int kDeltaWarps = kDeltaThreads / 32;
+constexpr int kDeltaCluster = 8;                                // ranks are multiples of 8: R / 8 rows of A per block
+constexpr int kDeltaRows = 2 * kDeltaCluster * kDeltaThreads;   // output rows per cluster
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
   const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
@@ -43,84 +51,104 @@ __device__ __forceinline__ uint16_t bf16_of(float v) {
   return *reinterpret_cast<const uint16_t*>(&h);
 }
 
-// Block (t, r): u[t][r] = s_l sum_k x[t][k] A_l[r][k] in fp32 (each thread's
-// columns in order, then the threads' sums in a fixed tree).
-__global__ void __launch_bounds__(kDownThreads) adapter_down_kernel(const uint16_t* __restrict__ x, const Adapters ad,
-                                                                    int k, float* __restrict__ u32,
-                                                                    uint16_t* __restrict__ u) {
-  __shared__ float sums[kDownThreads / 32];
-  const int t = blockIdx.x, r = blockIdx.y;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// Cluster (token t, slice of the output rows). Phase 1: the cluster's block
+// `rank` sums u[r] = s_l sum_k x[t][k] A_l[r][k] for r = rank, rank + 8, ...:
+// each warp an eighth of K for all of them, then the warps in order. Phase 2:
+// delta[t][n] = sum_r u[r] B_l[n][r], a thread per output row.
+__global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint16_t* __restrict__ x, const Adapters ad,
+                                                                      int n, int k, float* __restrict__ delta,
+                                                                      uint16_t* __restrict__ u) {
+  __shared__ float part[kDeltaWarps][kMaxRank / kDeltaCluster];
+  __shared__ __align__(16) float us[kMaxRank];
+  const int rank = blockIdx.x, t = blockIdx.y, slice = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // x is complete past the wait; only then may the dependent launch
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = adapter_of(ad, t);
-  float acc = 0.0f;
+  const int rows = ad.rank / kDeltaCluster;
   if (l >= 0) {
     const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * k);
-    const uint4* ar = reinterpret_cast<const uint4*>(ad.a + ((size_t)l * ad.rank + r) * k);
-#pragma unroll 4
-    for (int c = threadIdx.x; c < k / 8; c += kDownThreads) acc = dot8(__ldcg(ar + c), __ldcg(xr + c), acc);
-  }
+    const uint4* ar = reinterpret_cast<const uint4*>(ad.a + ((size_t)l * ad.rank + rank) * k);
+    const size_t row_step = (size_t)kDeltaCluster * (k / 8);
+    const int c0 = warp * (k / 64), c1 = c0 + k / 64;   // this warp's 16-byte pieces of a row
+    for (int i0 = 0; i0 < rows; i0 += 4) {
+      float acc[4] = {};
+      for (int c = c0 + lane; c < c1; c += 32) {
+        const uint4 xv = __ldg(xr + c);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, d);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = acc;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float v = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    v = l >= 0 ? v * __ldcg(ad.scale + l) : 0.0f;
-    u32[(size_t)t * ad.rank + r] = v;
-    if (u != nullptr) u[(size_t)t * ad.rank + r] = bf16_of(v);
-  }
-}
-
-// Thread n of token t: delta[t][n] = sum_r u[t][r] B_l[n][r] (0 without an adapter).
-__global__ void __launch_bounds__(kUpThreads) adapter_up_kernel(const Adapters ad, int n, const float* __restrict__ u32,
-                                                                float* __restrict__ delta) {
-  __shared__ float us[kMaxRank];
-  const int t = blockIdx.x, row = blockIdx.y * kUpThreads + threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int l = adapter_of(ad, t);
-  if (threadIdx.x < ad.rank) us[threadIdx.x] = __ldcg(u32 + (size_t)t * ad.rank + threadIdx.x);
-  __syncthreads();
-  if (row >= n) return;
-  float acc = 0.0f;
-  if (l >= 0) {
-    const uint4* br = reinterpret_cast<const uint4*>(ad.b + ((size_t)l * n + row) * ad.rank);
-#pragma unroll 4
-    for (int c = 0; c < ad.rank / 8; ++c) {
-      const uint4 q = __ldcg(br + c);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        for (int i = 0; i < 4; ++i)
+          if (i0 + i < rows) acc[i] = dot8(__ldcg(ar + (i0 + i) * row_step + c), xv, acc[i]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc = fmaf(us[8 * c + 2 * i], bf16_bits_to_float(w[i] & 0xFFFFu), acc);
-        acc = fmaf(us[8 * c + 2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u), acc);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], d);
+        if (lane == 0 && i0 + i < rows) part[warp][i0 + i] = acc[i];
       }
     }
   }
-  delta[(size_t)t * n + row] = acc;
+  __syncthreads();
+  // thread (peer, i): the block's sum i into peer's us[8 i + rank]
+  if (threadIdx.x < kDeltaCluster * rows) {
+    const int peer = threadIdx.x / rows, i = threadIdx.x % rows, r = kDeltaCluster * i + rank;
+    float v = 0.0f;
+    if (l >= 0) {
+#pragma unroll
+      for (int w = 0; w < kDeltaWarps; ++w) v += part[w][i];
+      v *= __ldcg(ad.scale + l);
+    }
+    const uint32_t dst = cluster_map((uint32_t)__cvta_generic_to_shared(&us[r]), (uint32_t)peer);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+    if (u != nullptr && peer == 0 && slice == 0) u[(size_t)t * ad.rank + r] = bf16_of(v);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = slice * kDeltaRows + (h * kDeltaCluster + rank) * kDeltaThreads + threadIdx.x;
+    if (row >= n) break;
+    float acc = 0.0f;
+    if (l >= 0) {
+      const uint4* br = reinterpret_cast<const uint4*>(ad.b + ((size_t)l * n + row) * ad.rank);
+#pragma unroll 4
+      for (int c = 0; c < ad.rank / 8; ++c) {
+        const uint4 q = __ldcg(br + c);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc = fmaf(us[8 * c + 2 * i], bf16_bits_to_float(w[i] & 0xFFFFu), acc);
+          acc = fmaf(us[8 * c + 2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u), acc);
+        }
+      }
+    }
+    delta[(size_t)t * n + row] = acc;
+  }
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_delta(const uint16_t* x, const Adapters& ad, int m, int n, int k, float* delta, uint16_t* u,
+                         cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3(kDeltaCluster, (unsigned)m, (unsigned)((n + kDeltaRows - 1) / kDeltaRows));
+  cfg.blockDim = dim3(kDeltaThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kDeltaCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, adapter_delta_kernel, x, ad, n, k, delta, u);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// The workspace: any4_linear's own, then for M <= 16 the inner values u in
-// fp32 and the fp32 term, else u as a bf16 pair, the adapters of each token
+// The workspace: any4_linear's own, then for M <= 16 the fp32 term, else u as a bf16 pair, the adapters of each token
 // tile and the partial sums of u.
 struct LoraSpace {
-  size_t u32, delta, pairs, lists, partials, total;
+  size_t delta, pairs, lists, partials, total;
 };
 LoraSpace lora_space(const LinearPlan& plan, int m, int n, int k, int rank, int sms) {
   LoraSpace s{};
@@ -131,7 +159,6 @@ LoraSpace lora_space(const LinearPlan& plan, int m, int n, int k, int rank, int 
     return here;
   };
   if (plan.mode != 3) {
-    s.u32 = take((size_t)m * rank * sizeof(float));
     s.delta = take((size_t)m * n * sizeof(float));
   } else {
     s.pairs = take(pairs_bytes(m, rank));
@@ -188,11 +215,8 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = (cudaStream_t)stream;
   if (plan.mode != 3) {
-    float* u32 = reinterpret_cast<float*>(ws + space.u32);
     float* delta = reinterpret_cast<float*>(ws + space.delta);
-    const dim3 up((unsigned)m, (unsigned)((n + kUpThreads - 1) / kUpThreads));
-    e = launch_pdl(adapter_down_kernel, dim3((unsigned)m, (unsigned)rank), kDownThreads, st, x, ad, k, u32, u);
-    if (e == cudaSuccess) e = launch_pdl(adapter_up_kernel, up, kUpThreads, st, ad, n, (const float*)u32, delta);
+    e = launch_delta(x, ad, m, n, k, delta, u, st);
     if (e == cudaSuccess) e = launch_linear(x, w, L, m, y, workspace, plan, st, delta);
   } else {
     AdapterTerm term{};

@@ -320,3 +320,28 @@ def test_adapters_at_far_offsets():
             ref[t] += v[t] @ a[l].double()
             bound[t] += (vb[t] + 2.0 ** -14 * v[t].abs()) @ a[l].double().abs()
         check(dx, ref, bound, "dx")
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (3, 4096, 4096), (7, 4096, 4096), (16, 272, 1024), (16, 14336, 1024)])
+def test_decode_reads_what_the_kernel_before_it_wrote(m, n, k):
+    """Back-to-back calls whose inputs the kernel right before each call
+    overwrites: the decode kernel runs beside the adapters' kernel and may not
+    read its inputs early."""
+    c = Case(m, n, k, 128, 4, 6, 16, "mixed", seed=13)
+    packed = c.packed()
+    xs = [torch.randn(m, k, device="cuda").to(torch.bfloat16) for _ in range(8)]
+    ids = [torch.randint(0, 6, (m,), device="cuda", dtype=torch.int32) for _ in range(8)]
+    want = [a4.any4_linear_lora(x, packed, *c.shape(), c.a, c.b, c.scale, i) for x, i in zip(xs, ids)]
+    torch.cuda.synchronize()
+    x, i, outs = xs[0].clone(), ids[0].clone(), []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            for xv, iv in zip(xs, ids):
+                torch.mul(xv, 1.0, out=x)
+                torch.add(iv, 0, out=i)
+                outs.append(a4.any4_linear_lora(x, packed, *c.shape(), c.a, c.b, c.scale, i))
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[j % 8]) for j, o in enumerate(outs))
