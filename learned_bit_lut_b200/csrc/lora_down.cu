@@ -1,21 +1,22 @@
 // The adapters' inner values z[t] = s_l in[t] . M_l for many tokens (lora.cuh),
 // on the tensor cores, and the lists of the adapters in each token tile.
 //
-// A block takes 128 tokens and a slice of the contraction (in's columns).
-// Their `in` chunks (128 x 64) come in once by TMA; against each goes the
-// 64-column chunk of every adapter that has a token in the tile, so a tile of
-// J adapters computes 128 x (J R) products into J groups of tensor-memory
-// columns and each token keeps the columns of its own adapter. The work is
-// bound by reading `in` and the adapters once (the tensor pipe idles), so
-// products that no token keeps cost nothing that shows until J is large. A
-// value of one adapter or token reaches no other token: rows and column
-// groups of a product do not mix.
+// A block takes 128 tokens, a slice of the contraction (in's columns) and a
+// group of the tile's adapters. The tokens' `in` chunk (128 x 64) is one
+// operand, the same chunk of the group's adapters, one under the other, the
+// other: one instruction multiplies with up to 256 adapter columns, and each
+// token keeps the columns of its own adapter. The work is bound by reading
+// `in` and the adapters once (the tensor pipe idles), so products that no
+// token keeps cost nothing that shows. A value of one adapter or token
+// reaches no other token: rows and columns of a product do not mix.
 //
 // Forward, M_l = A_l^T: A_l [R][K] is K-major like `in`. Backward, M_l = B_l
 // [N][R]: the contraction runs down its rows, an MN-major operand; the same
 // TMA boxes serve both. When there are fewer token tiles than SMs, the
-// contraction is split and the last block of a tile to arrive adds the
-// others' fp32 partials in order (deterministic).
+// contraction is split and the last block of a tile's group to arrive adds
+// the others' fp32 partials in order (deterministic). Waiting and issuing
+// cost a block's threads ~1000 cycles a stage, so a stage holds two chunks
+// where it can and two blocks share an SM.
 //
 // Warps: 0 = TMA of `in`, 1 = MMA, 2-5 = epilogue, 6 = TMA of the adapters.
 #include <cuda_bf16.h>
@@ -113,35 +114,37 @@ __global__ void __launch_bounds__(kListTile) slot_lists_kernel(const Adapters ad
 
 constexpr int kTileTokens = 128;
 constexpr int kChunk = 64;                          // contraction columns per stage
-constexpr int kXStages = 4;
 constexpr int kXBytes = kTileTokens * kChunk * 2;   // 16 KB
-constexpr int kMaxWStages = 16;
-constexpr int kWBudget = 44 * 1024;                 // adapter stages: two blocks per SM
+constexpr int kMaxDownStages = 8;
 constexpr int kDownTcThreads = 224;
-constexpr int kMaxTmemCols = 512;
+constexpr int kMaxProductCols = 256;                // adapter columns of one instruction
 constexpr int kDownBar = 1;
+constexpr int kStageBudget = 104 * 1024;         // a block's stages: two blocks share an SM
 
 struct DownCtl {
-  uint64_t xfull[kXStages], xempty[kXStages];
-  uint64_t wfull[kMaxWStages], wempty[kMaxWStages];
-  uint64_t acc_full, acc_empty;
+  uint64_t full[kMaxDownStages], empty[kMaxDownStages];
+  uint64_t acc_full;
   uint32_t tmem_base;
   int abort_flag;
   int leave, last;   // the epilogue's own agreements
-  int slots[kTileTokens];
+  int slots[kMaxProductCols / 16];
 };
+static_assert(sizeof(DownCtl) <= 1024, "control block");
 
 struct DownParams {
   Adapters ad;
   SlotLists lists;
-  int m, chunks, splits;
+  int m, steps, splits;        // a step is `chunks` chunks of the contraction
+  int groups, per_group;       // adapter groups of a tile, adapters per group
+  int chunks, stages;          // chunks per stage, stages
   int r16;                     // R rounded up to 16
-  int w_bytes, w_stages;       // one adapter chunk, and how many stages hold one
-  uint32_t idesc, tmem_cols;
+  int cols;                    // product columns per adapter: R16, or whole 64-column boxes (backward)
+  int m_bytes;                 // one chunk of one adapter
+  uint32_t tmem_cols;
   uint16_t* pairs;
   uint16_t* rounded;
   float* partials;             // [tile][split][token][R16]
-  unsigned* counters;
+  unsigned* counters;          // [tile][group]
   unsigned* status;
 };
 
@@ -178,133 +181,117 @@ __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, 
 template <bool BACK>
 __global__ void __launch_bounds__(kDownTcThreads, 2)
     adapter_down_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                           const DownParams p) {
+                           const __grid_constant__ DownParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
-  const uint32_t wbase = sbase + kXStages * kXBytes;
-  DownCtl* ctl = reinterpret_cast<DownCtl*>(smem_raw + (wbase - raw) + (size_t)p.w_stages * p.w_bytes);
+  const uint32_t x_bytes = (uint32_t)p.chunks * kXBytes, group_bytes = (uint32_t)(p.per_group * p.m_bytes);
+  const uint32_t stage_bytes = x_bytes + (uint32_t)p.chunks * group_bytes;
+  DownCtl* ctl = reinterpret_cast<DownCtl*>(smem_raw + (sbase - raw) + (size_t)p.stages * stage_bytes);
   volatile int* abort_flag = &ctl->abort_flag;
-  const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  const int kc0 = (int)((long long)split * p.chunks / p.splits);
-  const int kc1 = (int)((long long)(split + 1) * p.chunks / p.splits);
+  const int split = blockIdx.x % p.splits, tg = blockIdx.x / p.splits;
+  const int group = tg % p.groups, tile = tg / p.groups;
+  const int k0 = (int)((long long)split * p.steps / p.splits);
+  const int k1 = (int)((long long)(split + 1) * p.steps / p.splits);
   const int r16 = p.r16;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists and `in` are ready, the outputs are free
+  const SlotHead head = slot_head(p.lists, tile);
+  const int j0 = group * p.per_group, count = min(head.count - j0, p.per_group);
+  if (group > 0 && count <= 0) return;   // group 0 also clears the tokens without an adapter
+
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kXStages; ++s) {
-      mbar_init(smem_addr(&ctl->xfull[s]), 1);
-      mbar_init(smem_addr(&ctl->xempty[s]), 1);
-    }
-    for (int s = 0; s < p.w_stages; ++s) {
-      mbar_init(smem_addr(&ctl->wfull[s]), 1);
-      mbar_init(smem_addr(&ctl->wempty[s]), 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_addr(&ctl->full[s]), 2);    // expect_tx of `in` and of the adapters
+      mbar_init(smem_addr(&ctl->empty[s]), 1);   // tcgen05.commit
     }
     mbar_init(smem_addr(&ctl->acc_full), 1);
-    mbar_init(smem_addr(&ctl->acc_empty), 4);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists and `in` are ready, the outputs are free
-  const SlotHead head = slot_head(p.lists, tile);
-  const int count = head.count;
-  for (int j = threadIdx.x; j < count; j += kDownTcThreads) ctl->slots[j] = slot_at(p.lists, tile, head, j);
+  if ((int)threadIdx.x < count) ctl->slots[threadIdx.x] = slot_at(p.lists, tile, head, j0 + threadIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int group_cols = (r16 + 31) / 32 * 32;                // an adapter's columns start at multiples of 32
-  const int per_pass = (int)p.tmem_cols / group_cols;         // adapters that fit tensor memory at once
 
+  // a tile without adapters has nothing to multiply: only its MMA thread's
+  // commit and the epilogue run
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
-      for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass) {
-        for (int kc = kc0; kc < kc1; ++kc) {
-          if (r.wrapped && !gemm_wait(smem_addr(&ctl->xempty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
-          const uint32_t xb = smem_addr(&ctl->xfull[r.s]);
-          mbar_arrive_expect_tx(xb, kXBytes);
-          tma_load_2d(sbase + (uint32_t)r.s * kXBytes, &xmap, kc * kChunk, tile * kTileTokens, xb);
-          r.next(kXStages);
-        }
+      for (int k = k0; k < k1 && count > 0; ++k) {
+        if (r.wrapped && !gemm_wait(smem_addr(&ctl->empty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
+        const uint32_t fb = smem_addr(&ctl->full[r.s]), dst = sbase + (uint32_t)r.s * stage_bytes;
+        mbar_arrive_expect_tx(fb, x_bytes);
+        for (int c = 0; c < p.chunks; ++c)
+          tma_load_2d(dst + c * kXBytes, &xmap, (k * p.chunks + c) * kChunk, tile * kTileTokens, fb);
+        r.next(p.stages);
       }
     }
   } else if (warp == 6) {
     if (lane == 0) {
       Ring r;
-      const int w_stages = p.w_stages, w_bytes = p.w_bytes;
-      for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass) {
-        const int j1 = min(count, j0 + per_pass);
-        for (int kc = kc0; kc < kc1 && !*abort_flag; ++kc) {
-          for (int j = j0; j < j1; ++j) {
-            if (r.wrapped && !gemm_wait(smem_addr(&ctl->wempty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
-            const uint32_t wb = smem_addr(&ctl->wfull[r.s]), dst = wbase + (uint32_t)(r.s * w_bytes);
-            mbar_arrive_expect_tx(wb, w_bytes);
+      for (int k = k0; k < k1 && count > 0; ++k) {
+        if (r.wrapped && !gemm_wait(smem_addr(&ctl->empty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
+        const uint32_t fb = smem_addr(&ctl->full[r.s]);
+        uint32_t dst = sbase + (uint32_t)r.s * stage_bytes + x_bytes;
+        mbar_arrive_expect_tx(fb, (uint32_t)(p.chunks * count * p.m_bytes));
+        for (int c = 0; c < p.chunks; ++c, dst += group_bytes) {
+          const int at = (k * p.chunks + c) * kChunk;
+          for (int j = 0; j < count; ++j) {
+            const int l = ctl->slots[j];
             if (!BACK) {
-              tma_load_3d(dst, &wmap, kc * kChunk, 0, ctl->slots[j], wb);
+              tma_load_3d(dst + (uint32_t)(j * p.m_bytes), &wmap, at, 0, l, fb);
             } else {
-              for (int b = 0; b * 64 < r16; ++b) tma_load_3d(dst + b * 8192, &wmap, 64 * b, kc * kChunk, ctl->slots[j], wb);
+              for (int b = 0; b * 64 < r16; ++b)
+                tma_load_3d(dst + (uint32_t)(j * p.m_bytes + b * 8192), &wmap, 64 * b, at, l, fb);
             }
-            r.next(w_stages);
           }
         }
+        r.next(p.stages);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      Ring rx, rw;
-      const int w_stages = p.w_stages, w_bytes = p.w_bytes;
-      const uint32_t idesc = p.idesc;
-      int pass = 0;
-      for (int j0 = 0; j0 < count && !*abort_flag; j0 += per_pass, ++pass) {
-        const int j1 = min(count, j0 + per_pass);
-        if (pass > 0 && !gemm_wait(smem_addr(&ctl->acc_empty), (uint32_t)(pass - 1) & 1u, abort_flag, p.status)) break;
+      Ring r;
+      const uint32_t idesc = tc_idesc(count * p.cols, false, BACK);
+      for (int k = k0; k < k1 && count > 0; ++k) {
+        if (!gemm_wait(smem_addr(&ctl->full[r.s]), r.parity, abort_flag, p.status)) break;
         tc_fence_after();
-        for (int kc = kc0; kc < kc1 && !*abort_flag; ++kc) {
-          const int xs = rx.s;
-          if (!gemm_wait(smem_addr(&ctl->xfull[xs]), rx.parity, abort_flag, p.status)) break;
-          rx.next(kXStages);
-          const uint64_t ad = sw128_desc(sbase + (uint32_t)xs * kXBytes);
-          for (int j = j0; j < j1; ++j) {
-            const int ws = rw.s;
-            if (!gemm_wait(smem_addr(&ctl->wfull[ws]), rw.parity, abort_flag, p.status)) break;
-            rw.next(w_stages);
-            tc_fence_after();
-            const uint32_t waddr = wbase + (uint32_t)(ws * w_bytes);
-            const uint64_t bd = BACK ? sw128_desc_mn(waddr, 8192) : sw128_desc(waddr);
+        uint32_t xa = sbase + (uint32_t)r.s * stage_bytes, ma = xa + x_bytes;
+        for (int c = 0; c < p.chunks; ++c, xa += kXBytes, ma += group_bytes) {
+          const uint64_t ad = sw128_desc(xa), bd = BACK ? sw128_desc_mn(ma, 8192) : sw128_desc(ma);
 #pragma unroll
-            for (int kk = 0; kk < kChunk / 16; ++kk)
-              tc_mma(tmem + (uint32_t)((j - j0) * group_cols), ad + 2u * (uint64_t)kk, bd + (BACK ? 128u : 2u) * (uint64_t)kk,
-                     idesc, kc > kc0 || kk > 0 ? 1u : 0u);
-            tc_commit(smem_addr(&ctl->wempty[ws]));
-          }
-          tc_commit(smem_addr(&ctl->xempty[xs]));
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            tc_mma(tmem, ad + 2u * (uint64_t)kk, bd + (BACK ? 128u : 2u) * (uint64_t)kk, idesc,
+                   k > k0 || c > 0 || kk > 0 ? 1u : 0u);
         }
-        tc_commit(smem_addr(&ctl->acc_full));
+        tc_commit(smem_addr(&ctl->empty[r.s]));
+        r.next(p.stages);
       }
+      tc_commit(smem_addr(&ctl->acc_full));
     }
   } else {
     const int q = warp & 3, row = 32 * q + lane, t = tile * kTileTokens + row;
     const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
     const float scale = mine >= 0 ? __ldcg(p.ad.scale + mine) : 0.0f;
-    float* part = p.partials + ((size_t)blockIdx.x * kTileTokens + row) * r16;
-    int pass = 0;
-    for (int j0 = 0; j0 < count; j0 += per_pass, ++pass) {
-      const int j1 = min(count, j0 + per_pass);
-      gemm_wait(smem_addr(&ctl->acc_full), (uint32_t)pass & 1u, abort_flag, p.status);
-      down_epilogue_sync();
-      if (row == 0) ctl->leave = *abort_flag;
-      down_epilogue_sync();   // all four warps leave together if any wait gave up
-      if (ctl->leave) break;
+    float* part = p.partials + ((size_t)(tile * p.splits + split) * kTileTokens + row) * r16;
+    gemm_wait_idle(smem_addr(&ctl->acc_full), 0u, abort_flag, p.status);
+    down_epilogue_sync();
+    if (row == 0) ctl->leave = *abort_flag;
+    down_epilogue_sync();   // all four warps leave together if any wait gave up
+    if (!ctl->leave) {
       tc_fence_after();
-      for (int j = j0; j < j1; ++j) {
+      for (int j = 0; j < count; ++j) {
         const bool keep = mine >= 0 && ctl->slots[j] == mine;
         if (!__any_sync(0xFFFFFFFFu, keep)) continue;
         for (int r0 = 0; r0 < r16; r0 += 16) {
           uint32_t v[16];
-          tc_ld_x16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((j - j0) * group_cols + r0), v);
+          tc_ld_x16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(j * p.cols + r0), v);
           tc_wait_ld();
           if (keep && p.splits > 1) {
 #pragma unroll
@@ -321,27 +308,27 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
           __syncwarp();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty));
-    }
-    if (p.splits == 1) {
-      if (t < p.m && mine < 0) {
-        const float zero[16] = {};
-        for (int r0 = 0; r0 < r16; r0 += 16) store_inner(p, t, r0, zero);
-      }
-    } else {
-      __threadfence();
-      down_epilogue_sync();
-      if (row == 0) ctl->last = atomicAdd(p.counters + tile, 1u) == (unsigned)(p.splits - 1);
-      down_epilogue_sync();
-      if (ctl->last) {
+      if (p.splits > 1) {
         __threadfence();
-        const int groups = r16 / 16;
-        for (int e = row; e < kTileTokens * groups; e += 128) {
-          const int tr = e / groups, r0 = e % groups * 16, tt = tile * kTileTokens + tr;
-          if (tt >= p.m) continue;
+        down_epilogue_sync();
+        if (row == 0) ctl->last = atomicAdd(p.counters + tg, 1u) == (unsigned)(p.splits - 1);
+        down_epilogue_sync();
+      }
+      if (p.splits == 1) {
+        if (group == 0 && t < p.m && mine < 0) {
+          const float zero[16] = {};
+          for (int r0 = 0; r0 < r16; r0 += 16) store_inner(p, t, r0, zero);
+        }
+      } else if (ctl->last) {
+        __threadfence();
+        const int parts = r16 / 16;
+        for (int e = row; e < kTileTokens * parts; e += 128) {
+          const int tr = e / parts, r0 = e % parts * 16, tt = tile * kTileTokens + tr;
+          if (tt >= p.m) break;
           const int l = adapter_of(p.ad, tt);
+          bool own = l < 0 && group == 0;   // the token is this group's to write
+          for (int j = 0; j < count; ++j) own |= l >= 0 && ctl->slots[j] == l;
+          if (!own) continue;
           float z[16] = {};
           if (l >= 0) {
             const float* src = p.partials + ((size_t)tile * p.splits * kTileTokens + tr) * r16 + r0;
@@ -362,7 +349,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
           }
           store_inner(p, tt, r0, z);
         }
-        if (row == 0) p.counters[tile] = 0u;   // ready for the next call
+        if (row == 0) p.counters[tg] = 0u;   // ready for the next call
       }
     }
   }
@@ -385,8 +372,7 @@ cudaError_t allow_down_smem(int bytes) {
   return e;
 }
 
-constexpr int kDownSmem = kXStages * kXBytes + kWBudget + 2048 + 1024;   // stages, control, alignment
-static_assert(sizeof(DownCtl) <= 2048, "control block");
+constexpr int kDownSmem = kStageBudget + 1024 + 1024;   // stages, control, alignment
 
 int down_splits(int m, int cols, int num_sms) {
   const int tiles = (m + kTileTokens - 1) / kTileTokens, chunks = (cols + kChunk - 1) / kChunk;
@@ -431,19 +417,28 @@ cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, c
                         uint16_t* pairs, uint16_t* rounded, float* partials, unsigned* counters, unsigned* status,
                         int num_sms, cudaStream_t stream) {
   const int cols = backward ? n : k;
+  const int tiles = (m + kTileTokens - 1) / kTileTokens;
   DownParams p{};
   p.ad = ad;
   p.lists = lists;
   p.m = m;
-  p.chunks = (cols + kChunk - 1) / kChunk;
   p.splits = down_splits(m, cols, num_sms);
   p.r16 = rank16(ad.rank);
-  p.w_bytes = backward ? (p.r16 + 63) / 64 * 8192 : p.r16 * 128;
-  p.w_stages = kWBudget / p.w_bytes < kMaxWStages ? kWBudget / p.w_bytes : kMaxWStages;
-  p.idesc = tc_idesc(p.r16, false, backward);
-  const int most = (ad.ids != nullptr ? (ad.count < kTileTokens ? ad.count : kTileTokens) : 1) * ((p.r16 + 31) / 32 * 32);
+  p.cols = backward ? (p.r16 + 63) / 64 * 64 : p.r16;
+  p.m_bytes = p.cols * 128;
+  // a tile has at most min(L, 128) adapters
+  const int most = ad.ids == nullptr ? 1 : ad.count < kTileTokens ? ad.count : kTileTokens;
+  p.per_group = kMaxProductCols / p.cols < most ? kMaxProductCols / p.cols : most;
+  p.groups = (most + p.per_group - 1) / p.per_group;
+  // a stage of two chunks where two such stages leave room for a second block
+  const int one = kXBytes + p.per_group * p.m_bytes;
+  p.chunks = 4 * one <= kStageBudget ? 2 : 1;
+  p.stages = kStageBudget / (p.chunks * one);
+  if (p.stages > kMaxDownStages) p.stages = kMaxDownStages;
+  p.steps = ((cols + kChunk - 1) / kChunk + p.chunks - 1) / p.chunks;
+  if (p.splits > p.steps) p.splits = p.steps;
   p.tmem_cols = 32;
-  while ((int)p.tmem_cols < most && p.tmem_cols < kMaxTmemCols) p.tmem_cols *= 2;
+  while ((int)p.tmem_cols < p.per_group * p.cols) p.tmem_cols *= 2;
   p.pairs = pairs;
   p.rounded = rounded;
   p.partials = partials;
@@ -457,9 +452,9 @@ cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, c
   cudaError_t e = backward ? allow_down_smem<true>(kDownSmem) : allow_down_smem<false>(kDownSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((m + kTileTokens - 1) / kTileTokens * p.splits));
+  cfg.gridDim = dim3((unsigned)(tiles * p.groups * p.splits));
   cfg.blockDim = dim3(kDownTcThreads);
-  cfg.dynamicSmemBytes = (size_t)kXStages * kXBytes + (size_t)p.w_stages * p.w_bytes + 2048 + 1024;
+  cfg.dynamicSmemBytes = (size_t)p.stages * p.chunks * one + 1024 + 1024;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.cuh"
+#include "regdecode.cuh"
 
 namespace any4 {
 
@@ -218,83 +219,102 @@ __global__ void dequant_bits_kernel(const uint8_t* __restrict__ packed, Layout L
   }
 }
 
-// Tiled dequant: one thread block per (panel, 8 chunks = 512 columns). The
-// block decodes its words into a shared [32 rows][512 columns] bf16 tile
-// (same fp32 fma + round-to-nearest-even as dequant_kernel) and writes each
-// row segment with 16-byte stores, so the N x K output is written coalesced.
-constexpr int kDqChunks = 8;
-constexpr int kDqRow = kDqChunks * kChunkCols + 8;   // bf16 per tile row (16-byte pad)
+// Dequant for outputs aligned to 16 bytes (WIDE: 32): a warp takes 64-column
+// chunks of one 32-row panel. Its lane (g, t) holds the tables of rows g, g+8,
+// g+16, g+24 in registers (regdecode.cuh; a table look-up in shared memory per
+// weight costs more than the weight's HBM traffic) and expands its own words
+// of a chunk, 16 consecutive columns of each of those rows, which it stores as
+// one 32-byte run: the 4 lanes of a row write a 128-byte line. Codes of 3 and
+// 2 bits are first spread to the 4-bit words of the same steps. Same fp32 fma
+// and nearest-even rounding as dequant_kernel, so the same bits.
+// B200, 14336 x 4096: 38.4 us any4, 39.4 us any3, 38.9 us any2, the rate at
+// which 117 MB can be written; by look-ups in shared memory any4 took 38.8
+// us, in global memory any3 took 4096 x 4096 in 93 us.
+constexpr int kDqWarps = 8;
+constexpr int kDqChunks = 4;   // chunks of a warp in a row: the tables are loaded once
 
-__global__ void __launch_bounds__(256) dequant_tile_kernel(const uint8_t* __restrict__ packed, Layout L,
-                                                           uint16_t* __restrict__ w) {
-  __shared__ __align__(16) uint16_t tile[kPanelRows * kDqRow];
-  __shared__ float lut[kPanelRows * 16];
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(packed + L.w_off);
-  const uint16_t* lutsec = reinterpret_cast<const uint16_t*>(packed + L.lut_off);
-  const uint32_t* ab = reinterpret_cast<const uint32_t*>(packed + L.ab_off);
-  const int P = blockIdx.y;
-  const int c_begin = blockIdx.x * kDqChunks;
-  const int nch = min(kDqChunks, L.kchunks - c_begin);
-  // word j of this thread: e = threadIdx.x + 256 j (chunk j of the strip, word
-  // threadIdx.x of the chunk); its weights and scales are loaded before the
-  // table barrier so the loads overlap
-  const int wi = threadIdx.x;
-  const int i = wi & 3, ln = (wi >> 2) & 31, h = wi >> 7;
-  const int g = ln >> 2, t = ln & 3;
-  const int c0 = 16 * t + 2 * (4 * h + i);   // column within a chunk
-  const int gshift = __ffs(L.g) - 1;         // G is a power of two
-  const uint32_t* wsrc = words + ((size_t)P * L.kchunks + c_begin) * 256 + wi;
-  const uint4* ssrc = reinterpret_cast<const uint4*>(ab) + (size_t)P * L.groups * 8 + g;
-  uint32_t word[kDqChunks];
-  uint4 sc[kDqChunks];
-#pragma unroll
-  for (int j = 0; j < kDqChunks; ++j) {
-    if (j < nch) {
-      const int col0 = (c_begin + j) * kChunkCols + c0;
-      word[j] = __ldg(wsrc + j * 256);
-      sc[j] = __ldg(ssrc + (size_t)(col0 >> gshift) * 8);
-    }
+// The 4-bit word of step s (a row-pair code per byte) from the lane's packed bits.
+template <int BITS>
+__device__ __forceinline__ uint32_t step_word(const uint32_t (&wd)[8], int s) {
+  if (BITS == 4) return wd[s];
+  if (BITS == 3) {   // 24 bits: four 6-bit codes
+    const int bit = 24 * s, word = bit >> 5, off = bit & 31;
+    const uint32_t v = off == 0 ? wd[word] : __funnelshift_r(wd[word], wd[word + 1], off);
+    const uint32_t t = (v & 0xFFFu) | ((v & 0xFFF000u) << 4);
+    const uint32_t w = (t & 0x003F003Fu) | ((t & 0x0FC00FC0u) << 2);
+    return (w & 0x07070707u) | ((w & 0x38383838u) << 1);
   }
-  for (int e = threadIdx.x; e < kPanelRows * 16; e += blockDim.x)
-    lut[e] = bf16_bits_to_float(lutsec[(size_t)P * kPanelRows * 16 + e]);
-  __syncthreads();
+  const uint32_t v = (wd[s >> 1] >> (16 * (s & 1))) & 0xFFFFu;   // 16 bits: four 4-bit codes
+  uint32_t w = (v | (v << 8)) & 0x00FF00FFu;
+  w = (w | (w << 4)) & 0x0F0F0F0Fu;
+  return (w | (w << 2)) & 0x33333333u;
+}
+
+__device__ __forceinline__ uint32_t scale_pair(uint32_t pair, float a, float c) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, bf16_bits_to_float(pair & 0xFFFFu), c),
+                                                 fmaf(a, __uint_as_float(pair & 0xFFFF0000u), c));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int BITS, bool WIDE>
+__global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8_t* __restrict__ packed, Layout L,
+                                                                     uint16_t* __restrict__ w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int P = blockIdx.y, c0 = (blockIdx.x * kDqWarps + warp) * kDqChunks;
+  const uint4* lsec = reinterpret_cast<const uint4*>(packed + L.lut_off) + (size_t)P * kPanelRows * 2;
+  const uint4* asec = reinterpret_cast<const uint4*>(packed + L.ab_off) + (size_t)P * L.groups * 8 + g;
+  const int gshift = __ffs(L.g) - 1;   // G is a power of two
+  Planes T[4];
 #pragma unroll
-  for (int j = 0; j < kDqChunks; ++j) {
-    if (j < nch) {
-      const uint32_t sw[4] = {sc[j].x, sc[j].y, sc[j].z, sc[j].w};
+  for (int r = 0; r < 4; ++r) T[r] = to_planes(ld_nc_v4(lsec + (g + 8 * r) * 2), ld_nc_v4(lsec + (g + 8 * r) * 2 + 1));
+#pragma unroll 2
+  for (int c = c0; c < min(c0 + kDqChunks, L.kchunks); ++c) {
+    const uint8_t* chunk = packed + L.w_off + ((size_t)P * L.kchunks + c) * L.chunk_bytes;
+    uint32_t wd[8] = {};
+    const uint4 lo = ld_stream_v4(chunk + lane * 16);
+    wd[0] = lo.x; wd[1] = lo.y; wd[2] = lo.z; wd[3] = lo.w;
+    if (BITS == 4) {
+      const uint4 hi = ld_stream_v4(chunk + 512 + lane * 16);
+      wd[4] = hi.x; wd[5] = hi.y; wd[6] = hi.z; wd[7] = hi.w;
+    } else if (BITS == 3) {
+      const uint2 hi = __ldg(reinterpret_cast<const uint2*>(chunk + 512) + lane);
+      wd[4] = hi.x; wd[5] = hi.y;
+    }
+    const uint4 rec = __ldg(asec + (size_t)((c * kChunkCols) >> gshift) * 8);
+    // rows g, g+8, g+16, g+24: alpha and beta
+    const float al[4] = {bf16_bits_to_float(rec.x & 0xFFFFu), bf16_bits_to_float(rec.z & 0xFFFFu),
+                         __uint_as_float(rec.x & 0xFFFF0000u), __uint_as_float(rec.z & 0xFFFF0000u)};
+    const float be[4] = {bf16_bits_to_float(rec.y & 0xFFFFu), bf16_bits_to_float(rec.w & 0xFFFFu),
+                         __uint_as_float(rec.y & 0xFFFF0000u), __uint_as_float(rec.w & 0xFFFF0000u)};
+    uint32_t o[4][8];   // [row][column pair]
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+    for (int j = 0; j < 4; ++j) {   // columns 16t + 4j .. + 3
+      uint32_t t0, t1, a[4], b[4];
+      rowpair_to_selectors(step_word<BITS>(wd, 2 * j), step_word<BITS>(wd, 2 * j + 1), t0, t1);
+      decode8(T[0], T[1], t0, a);
+      decode8(T[2], T[3], t1, b);
+      o[0][2 * j] = scale_pair(a[0], al[0], be[0]);
+      o[0][2 * j + 1] = scale_pair(a[2], al[0], be[0]);
+      o[1][2 * j] = scale_pair(a[1], al[1], be[1]);
+      o[1][2 * j + 1] = scale_pair(a[3], al[1], be[1]);
+      o[2][2 * j] = scale_pair(b[0], al[2], be[2]);
+      o[2][2 * j + 1] = scale_pair(b[2], al[2], be[2]);
+      o[3][2 * j] = scale_pair(b[1], al[3], be[3]);
+      o[3][2 * j + 1] = scale_pair(b[3], al[3], be[3]);
+    }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = g + 8 * half + 16 * u;
-          const float a = bf16_bits_to_float((sw[2 * half] >> (16 * u)) & 0xFFFFu);
-          const float c = bf16_bits_to_float((sw[2 * half + 1] >> (16 * u)) & 0xFFFFu);
-          const uint32_t i0 = (word[j] >> (8 * half + 4 * u)) & 0xFu;         // column c0
-          const uint32_t i1 = (word[j] >> (8 * (half + 2) + 4 * u)) & 0xFu;   // column c0 + 1
-          // one fp32 rounding each, then bf16 nearest-even
-          const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, lut[r * 16 + i0], c), fmaf(a, lut[r * 16 + i1], c));
-          *reinterpret_cast<__nv_bfloat162*>(&tile[r * kDqRow + j * kChunkCols + c0]) = v;
-        }
+    for (int r = 0; r < 4; ++r) {
+      const int row = P * kPanelRows + g + 8 * r;
+      if (row >= L.n) continue;
+      uint16_t* out = w + (size_t)row * L.k + c * kChunkCols + 16 * t;
+      if (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out), "r"(o[r][0]), "r"(o[r][1]),
+                     "r"(o[r][2]), "r"(o[r][3]), "r"(o[r][4]), "r"(o[r][5]), "r"(o[r][6]), "r"(o[r][7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4*>(out)[0] = make_uint4(o[r][0], o[r][1], o[r][2], o[r][3]);
+        reinterpret_cast<uint4*>(out)[1] = make_uint4(o[r][4], o[r][5], o[r][6], o[r][7]);
       }
-    }
-  }
-  __syncthreads();
-  uint16_t* wp = w + (size_t)P * kPanelRows * L.k + (size_t)c_begin * kChunkCols;
-  const int rows = min(kPanelRows, L.n - P * kPanelRows);
-  if (nch == kDqChunks) {   // full strip: 64 16-byte units per row, 4 rows per pass
-    const int u = threadIdx.x & 63;
-#pragma unroll
-    for (int r = threadIdx.x >> 6; r < kPanelRows; r += 4)
-      if (r < rows)
-        *reinterpret_cast<uint4*>(wp + (size_t)r * L.k + u * 8) =
-            *reinterpret_cast<const uint4*>(&tile[r * kDqRow + u * 8]);
-  } else {
-    const int units = nch * kChunkCols / 8;   // 16-byte units per row
-    for (int e = threadIdx.x; e < kPanelRows * units; e += blockDim.x) {
-      const int r = e / units, u = e % units;
-      if (r < rows)
-        *reinterpret_cast<uint4*>(wp + (size_t)r * L.k + u * 8) =
-            *reinterpret_cast<const uint4*>(&tile[r * kDqRow + u * 8]);
     }
   }
 }
@@ -343,19 +363,30 @@ cudaError_t launch_pack_fixed(const uint8_t* idx_nib, const uint16_t (&lut)[16],
   return cudaGetLastError();
 }
 
+template <int BITS>
+static void launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream) {
+  const int per_block = kDqWarps * kDqChunks;
+  const dim3 grid((L.kchunks + per_block - 1) / per_block, L.panels);
+  if ((reinterpret_cast<uintptr_t>(w) & 31) == 0)
+    dequant_rows_kernel<BITS, true><<<grid, kDqWarps * 32, 0, stream>>>(packed, L, w);
+  else
+    dequant_rows_kernel<BITS, false><<<grid, kDqWarps * 32, 0, stream>>>(packed, L, w);
+}
+
 cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w,
                            cudaStream_t stream) {
   const int th = 256;
   const size_t lanes = (size_t)L.panels * L.kchunks * 32;
+  const bool runs = (reinterpret_cast<uintptr_t>(w) & 15) == 0;   // else w is only 4-byte aligned
   if (L.bits == 3) {
-    dequant_bits_kernel<3><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
+    if (runs) launch_dequant_rows<3>(packed, L, w, stream);
+    else dequant_bits_kernel<3><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else if (L.bits == 2) {
-    dequant_bits_kernel<2><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
-  } else if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {   // 16-byte stores need a 16-byte aligned w
-    const dim3 grid((L.kchunks + kDqChunks - 1) / kDqChunks, L.panels);
-    dequant_tile_kernel<<<grid, th, 0, stream>>>(packed, L, w);
+    if (runs) launch_dequant_rows<2>(packed, L, w, stream);
+    else dequant_bits_kernel<2><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else {
-    dequant_kernel<<<grid_for((size_t)L.n_pad * L.k / 8, th), th, 0, stream>>>(packed, L, w);
+    if (runs) launch_dequant_rows<4>(packed, L, w, stream);
+    else dequant_kernel<<<grid_for((size_t)L.n_pad * L.k / 8, th), th, 0, stream>>>(packed, L, w);
   }
   return cudaGetLastError();
 }

@@ -19,7 +19,7 @@
 //    N = 16..256), so at small M the MMA count, not the FLOPs, bounds the
 //    tensor side, and the byte-permute decode (integer pipe) bounds the rest.
 //  * any4 M > 512, any3 / any2: dequantize W into a bf16 N x K scratch in the
-//    caller's workspace (dequant_tile_kernel in pack_dequant.cu, bit-exact
+//    caller's workspace (dequant_rows_kernel in pack_dequant.cu, bit-exact
 //    like any4_dequant), then prefill_gemm_kernel brings both operands in by
 //    TMA (tiles of 128 rows x 256 tokens). The decode then runs once per
 //    call instead of once per 256-token tile.
@@ -85,8 +85,8 @@ __device__ __forceinline__ void epilogue_sync() {
 // accumulators: behind a tile's main loop come extra stages that hold M's
 // tile where W's goes and z's where x's goes. z is a bf16 pair, leading and
 // trailing part; for R <= 32 both lie in one 64-column row and share a stage,
-// beyond that each 64 rank columns take one stage per part. Only the last of
-// a tile's K splits takes them.
+// beyond that each 64 rank columns take one stage per part. A tile's K splits
+// share them.
 //
 // A tile whose tokens do not all have one adapter runs the stages of each of
 // its adapters, with z zeroed in the rows of the other tokens. So that an
@@ -105,6 +105,9 @@ struct LoraArgs {
   const uint16_t* pairs;
   int r16;
 };
+
+// This split's share of a tile's `count` extra stages.
+__device__ __forceinline__ int extra_begin(int count, int split, int splits) { return count * split / splits; }
 
 struct Extra {
   int rank0, zcol, steps;   // first rank column, column of the pairs, 16-deep steps
@@ -221,16 +224,18 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           tma_load_2d(sb(s), &xmap, kc * kBK, mt * kBN, fb);
         }
         if constexpr (LORA) {
-          if (u % splits != splits - 1) continue;
           const SlotHead head = slot_head(lora.lists, mt);
           const bool mixed = head.mixed;
           const int per = extra_stages(lora.r16), count = head.count * per;
-          for (int e = 0; e < count; ++e, ++it) {
+          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
+          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;   // read one stage ahead
+          for (int e = e0; e < e1; ++e, ++it) {
             const int s = it % kStages;
             const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+            const int l = l_next;
+            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
             if (it >= kStages && !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
             const Extra ex = extra_stage(lora.r16, e % per);
-            const int l = slot_at(lora.lists, mt, head, e / per);
             // a stage to be patched lands on a barrier of its own: the patching
             // warps see only those stages, so they cannot count the others
             const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
@@ -254,8 +259,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
-        if constexpr (LORA)
-          if (u % splits == splits - 1) head = slot_head(lora.lists, (u / splits) % m_tiles);
+        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
@@ -276,8 +280,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           tc_commit(smem_addr(&ctl->empty[s]));   // the stage is free once these MMAs are done
         }
         if constexpr (LORA) {
-          const int per = extra_stages(lora.r16);
-          for (int e = 0; e < head.count * per; ++e, ++it) {
+          const int per = extra_stages(lora.r16), sp = u % splits;
+          const int e1 = extra_begin(head.count * per, sp + 1, splits);
+          for (int e = extra_begin(head.count * per, sp, splits); e < e1; ++e, ++it) {
             const int s = it % kStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kStages) & 1u, abort_flag, status)) break;
             if (head.mixed) {
@@ -309,10 +314,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         int kc0, kc1;
         k_range(u, kc0, kc1);
         it += kc1 - kc0;
-        if (u % splits != splits - 1) continue;
         const SlotHead head = slot_head(lora.lists, mt);
         const bool mixed = head.mixed;
         const int per = extra_stages(lora.r16), count = head.count * per;
+        const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
         if (mixed) {
           int id[kBN / kPatchThreads];
 #pragma unroll
@@ -321,9 +326,11 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             id[i] = t < m ? adapter_of(lora.ad, t) : -1;
           }
           bool ok = true;
-          for (int e = 0; e < count && ok; ++e) {
-            const int s = (it + e) % kStages;
-            const int l = slot_at(lora.lists, mt, head, e / per);
+          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
+          for (int e = e0; e < e1; ++e) {
+            const int s = (it + e - e0) % kStages;
+            const int l = l_next;
+            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
             ok = __all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->raw[s]), (raw_phase >> s) & 1u, abort_flag, status));
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           }
           if (!ok) break;
         }
-        it += count;
+        it += e1 - e0;
       }
     }
   } else {
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         // the adapters' stages come whole by TMA; the decoders count them in
         // and patch those of tiles with several adapters
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok && u % splits == splits - 1) {
+        if (ok) {
           asm volatile("griddepcontrol.wait;" ::: "memory");   // lists, ids and pairs are ready
           const int mt = (u / splits) % m_tiles, thread = threadIdx.x - 6 * 32;
           const SlotHead head = slot_head(lora.lists, mt);
@@ -642,7 +649,11 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           const int per = extra_stages(lora.r16), count = head.count * per;
           const int t = mt * BN + thread;
           const int id = mixed && thread < BN && t < m ? adapter_of(lora.ad, t) : -1;
-          for (int e = 0; e < count && ok; ++e) {
+          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
+          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
+          for (int e = e0; e < e1; ++e) {
+            const int l = l_next;
+            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
             const int s = it % kFusedStages;
             const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
             ++it;
@@ -651,7 +662,6 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             if (!ok) break;   // the whole warp leaves
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->full[s]));
             if (!mixed) continue;
-            const int l = slot_at(lora.lists, mt, head, e / per);
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
             if (patch_finite(sa(s), kAStageBytes, thread, 32 * kFusedDecoders)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
@@ -685,18 +695,21 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           tma_load_2d(sb(s), &xmap, kc * kBK, mt * BN, fb);
         }
         if constexpr (LORA) {
-          if (u % splits != splits - 1) continue;
           const int nt = (u / splits) / m_tiles;
           const SlotHead head = slot_head(lora.lists, mt);
           const int per = extra_stages(lora.r16), count = head.count * per;
-          for (int e = 0; e < count; ++e, ++it) {
+          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
+          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
+          for (int e = e0; e < e1; ++e, ++it) {
+            const int l = l_next;
+            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
             const int s = it % kFusedStages;
             const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
             if (it >= kFusedStages && !gemm_wait_idle(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
             const Extra ex = extra_stage(lora.r16, e % per);
             const uint32_t fb = smem_addr(&ctl->full[s]);
             mbar_arrive_expect_tx(fb, C::kStage);
-            tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, slot_at(lora.lists, mt, head, e / per), fb);
+            tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, fb);
             tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * BN, fb);
           }
         }
@@ -710,8 +723,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       if (LORA) asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists are ready
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
-        if constexpr (LORA)
-          if (u % splits == splits - 1) head = slot_head(lora.lists, (u / splits) % m_tiles);
+        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status)) break;
@@ -731,8 +743,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           tc_commit(smem_addr(&ctl->empty[s]));
         }
         if constexpr (LORA) {
-          const int per = extra_stages(lora.r16);
-          for (int e = 0; e < head.count * per; ++e, ++it) {
+          const int per = extra_stages(lora.r16), sp = u % splits;
+          const int e1 = extra_begin(head.count * per, sp + 1, splits);
+          for (int e = extra_begin(head.count * per, sp, splits); e < e1; ++e, ++it) {
             const int s = it % kFusedStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kFusedStages) & 1u, abort_flag, status)) break;
             if (head.mixed) {
