@@ -6,23 +6,23 @@
 // Both are a tall skinny product src^T z with the tokens as the contraction:
 // src is x or dy (128 of its columns per block), z the R inner values. A
 // 64-token chunk of src is a tile with the contraction down its rows, an
-// MN-major operand as TMA brings it in, and so is z's. Against one chunk of
-// src go the z tiles of every adapter that has a token in it, each into its
-// own tensor-memory columns; v is a bf16 pair whose two parts are 2 R16
+// MN-major operand as TMA brings it in, and so is z's. An adapter's sums have
+// their own tensor-memory columns; v is a bf16 pair whose two parts are 2 R16
 // columns of one instruction and are added in the epilogue.
 //
 // src is read once and bounds the work (R <= 64; the rest is small and comes
 // from L2), so x kept in 8 bits halves it: 8 warps turn the codes into the
 // bf16 values they stand for (act8.cuh) on their way into the operand tile.
 //
-// A chunk whose tokens do not all have one adapter is patched by the same
-// warps: the rows of other tokens are zeroed in z, and infinities and NaN are
-// taken out of src, where 0 times them would be NaN; for the columns and
-// adapters they belong to the epilogue then sums anew in fp32. So a padding token's or
-// another request's values reach no sum but their own.
+// For a chunk whose tokens do not all have one adapter the same warps build
+// z's tile: each token's values in the columns of its own adapter, zeros in
+// the others', so that one product serves all adapters of the block. They also
+// take infinities and NaN out of src, where 0 times them would be NaN; for the
+// columns and adapters they belong to the epilogue then sums anew in fp32. So
+// a padding token's or another request's values reach no sum but their own.
 //
 // Blocks: 128 columns of src x a share of the chunks x as many adapters as
-// tensor memory holds (512 columns). Shares of the chunks are added by the
+// one instruction holds (256 columns). Shares of the chunks are added by the
 // last block to arrive, in order.
 //
 // Warps: 0 = TMA of src, 1 = MMA, 2-5 = epilogue, 6-13 = codes and patches,
@@ -50,7 +50,8 @@ constexpr int kZBudget = 132 * 1024;             // z stages and chunk masks, on
 constexpr int kZBudgetTwo = 44 * 1024;           // the same for two blocks per SM
 constexpr int kMaxZStages = 8;
 constexpr int kWgradBar = 1;
-constexpr int kMaxGroups = 16;                   // adapters per block: 512 columns / 32
+constexpr int kMaxZCols = 256;                   // z columns of one instruction:
+constexpr int kMaxPass = kMaxZCols / 32;         // at most so many adapters per block
 
 template <bool CODES>
 struct WgradCfg {
@@ -72,7 +73,7 @@ struct alignas(1024) WgradCtl {
   uint64_t a_raw[kMaxAStages], a_ready[kMaxAStages];     // bytes of a chunk to be patched; patched or converted
   uint64_t code_full[kMaxRawStages], code_empty[kMaxRawStages];
   uint64_t z_full[kMaxZStages], z_empty[kMaxZStages];
-  uint64_t z_raw[kMaxZStages], z_ready[kMaxZStages];
+  uint64_t z_raw[kMaxZStages], z_ready[kMaxZStages];     // a z tile to be built is free; built
   uint64_t acc_full;
   uint32_t tmem_base;
   int abort_flag;
@@ -90,8 +91,8 @@ struct WgradParams {
   int width;                  // z columns of one instruction: 2 R16 (pairs) or R16
   int r16;
   int group_cols, per_pass;   // tensor-memory columns per adapter, adapters per block
-  int z_bytes, z_stages;
-  uint32_t idesc, tmem_cols;
+  int z_bytes, z_stage, z_stages;   // an adapter's z tile, a stage (that or all adapters'), stages
+  uint32_t idesc, idesc_all, tmem_cols;
   const uint16_t* src;        // bf16 src, or
   const uint8_t* codes;
   const uint16_t* steps;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   const uint32_t rbase = sbase + C::kAStages * kABytes, zbase = sbase + C::kSrcBytes;
-  WgradCtl* ctl = reinterpret_cast<WgradCtl*>(smem_raw + (zbase - raw) + (size_t)p.z_stages * p.z_bytes);
+  WgradCtl* ctl = reinterpret_cast<WgradCtl*>(smem_raw + (zbase - raw) + (size_t)p.z_stages * p.z_stage);
   // chunk c0 + i: bit g is adapter l_lo + g, kMixed: its tokens do not all have one adapter
   unsigned* info = reinterpret_cast<unsigned*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort_flag;
@@ -212,6 +213,14 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
     fence_mbar_init();
   }
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  if (warp >= 2 && warp < 6) {   // the sums start at zero: products of one adapter and of all add to them alike
+    for (uint32_t c = 0; c < p.tmem_cols; c += 32) tc_zero_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c);
+    tc_wait_st();
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int c = c0 + threadIdx.x; c < c1; c += kWgradThreads) {
@@ -227,16 +236,14 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
 
-  // Every role walks the chunks, and a chunk's adapters (the bits of its mask
-  // in ascending order), alike.
+  // Every role walks the chunks alike; each takes one stage of src and one of z.
   constexpr int kSrcStages = CODES ? C::kRawStages : C::kAStages;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA of src
     if (lane == 0) {
       Ring r;
-      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+      for (int c = c0; c < c1; ++c) {
         const unsigned in = info[c - c0];
         if (in == 0) continue;
         const int s = r.s;
@@ -263,65 +270,62 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
     if (lane == 0) {
       Ring r;
       const int z_stages = p.z_stages, z_bytes = p.z_bytes, width = p.width;
-      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+      for (int c = c0; c < c1; ++c) {
         const unsigned in = info[c - c0];
-        const bool mixed = in & kMixed;
-        for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
-          const int s = r.s;
-          if (r.wrapped && !gemm_wait(smem_addr(&ctl->z_empty[s]), r.parity ^ 1u, abort_flag, p.status)) break;
-          const uint32_t fb = smem_addr(mixed ? &ctl->z_raw[s] : &ctl->z_full[s]);
+        if (in == 0) continue;
+        const int s = r.s;
+        if (r.wrapped && !gemm_wait(smem_addr(&ctl->z_empty[s]), r.parity ^ 1u, abort_flag, p.status)) break;
+        const uint32_t fb = smem_addr(&ctl->z_full[s]);
+        if (in & kMixed) {   // the workers build this one
+          mbar_arrive_one(smem_addr(&ctl->z_raw[s]));
+          mbar_arrive_one(fb);
+        } else {
           mbar_arrive_expect_tx(fb, z_bytes);
-          if (mixed) mbar_arrive_one(smem_addr(&ctl->z_full[s]));
           for (int b = 0; b * 64 < width; ++b)
-            tma_load_2d(zbase + (uint32_t)(s * z_bytes + b * 8192), &zmap, 64 * b, c * kTokens, fb);
-          r.next(z_stages);
+            tma_load_2d(zbase + (uint32_t)(s * p.z_stage + b * 8192), &zmap, 64 * b, c * kTokens, fb);
         }
+        r.next(z_stages);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
       Ring ra, rz;
-      const int z_stages = p.z_stages, z_bytes = p.z_bytes, group_cols = p.group_cols;
-      const uint32_t idesc = p.idesc;
+      const int z_stages = p.z_stages, z_stage = p.z_stage, group_cols = p.group_cols;
+      const uint32_t idesc = p.idesc, idesc_all = p.idesc_all;
       uint32_t a_phase = 0, z_phase = 0;   // bit s: parity of stage s's next patch
       unsigned touched = 0;
-      for (int c = c0; c < c1 && !*abort_flag; ++c) {
+      for (int c = c0; c < c1; ++c) {
         const unsigned in = info[c - c0];
         if (in == 0) continue;
         const bool mixed = in & kMixed;
-        const int s = ra.s;
-        const uint32_t ph = ra.parity;
-        ra.next(C::kAStages);
+        const int s = ra.s, zs = rz.s;
         if (CODES) {
-          if (!gemm_wait(smem_addr(&ctl->a_ready[s]), ph, abort_flag, p.status)) break;
+          if (!gemm_wait(smem_addr(&ctl->a_ready[s]), ra.parity, abort_flag, p.status)) break;
         } else {
-          if (!gemm_wait(smem_addr(&ctl->a_full[s]), ph, abort_flag, p.status)) break;
+          if (!gemm_wait(smem_addr(&ctl->a_full[s]), ra.parity, abort_flag, p.status)) break;
           if (mixed) {
             if (!gemm_wait(smem_addr(&ctl->a_ready[s]), (a_phase >> s) & 1u, abort_flag, p.status)) break;
             a_phase ^= 1u << s;
           }
         }
-        const uint64_t ad = sw128_desc_mn(sbase + (uint32_t)s * kABytes, kABytes / 2);
-        for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
-          const int g = __ffs(left) - 1, zs = rz.s;
-          const uint32_t zph = rz.parity;
-          rz.next(z_stages);
-          if (!gemm_wait(smem_addr(&ctl->z_full[zs]), zph, abort_flag, p.status)) break;
-          if (mixed) {
-            if (!gemm_wait(smem_addr(&ctl->z_ready[zs]), (z_phase >> zs) & 1u, abort_flag, p.status)) break;
-            z_phase ^= 1u << zs;
-          }
-          tc_fence_after();
-          const uint64_t bd = sw128_desc_mn(zbase + (uint32_t)(zs * z_bytes), 8192);
-#pragma unroll
-          for (int kk = 0; kk < kTokens / 16; ++kk)
-            tc_mma(tmem + (uint32_t)(g * group_cols), ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, idesc,
-                   kk > 0 || (touched >> g & 1u) ? 1u : 0u);
-          touched |= 1u << g;
-          tc_commit(smem_addr(&ctl->z_empty[zs]));
+        if (!gemm_wait(smem_addr(&ctl->z_full[zs]), rz.parity, abort_flag, p.status)) break;
+        if (mixed) {
+          if (!gemm_wait(smem_addr(&ctl->z_ready[zs]), (z_phase >> zs) & 1u, abort_flag, p.status)) break;
+          z_phase ^= 1u << zs;
         }
+        ra.next(C::kAStages);
+        rz.next(z_stages);
+        tc_fence_after();
+        const uint64_t ad = sw128_desc_mn(sbase + (uint32_t)s * kABytes, kABytes / 2);
+        const uint64_t bd = sw128_desc_mn(zbase + (uint32_t)(zs * z_stage), 8192);
+        const uint32_t d = mixed ? tmem : tmem + (uint32_t)((__ffs(in) - 1) * group_cols);
+        const uint32_t id = mixed ? idesc_all : idesc;
+#pragma unroll
+        for (int kk = 0; kk < kTokens / 16; ++kk) tc_mma(d, ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, id, 1u);
+        tc_commit(smem_addr(&ctl->z_empty[zs]));
         tc_commit(smem_addr(&ctl->a_empty[s]));
+        touched |= in & ~kMixed;
       }
       *(volatile unsigned*)&ctl->touched = touched;
       mbar_arrive_one(smem_addr(&ctl->acc_full));
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
       return two;
     };
     uint32_t step_next = steps_of(c0);
-    for (int c = c0; c < c1 && ok && !*abort_flag; ++c) {
+    for (int c = c0; c < c1 && ok; ++c) {
       const unsigned in = info[c - c0];
       const bool mixed = in & kMixed;
       const uint32_t step = step_next;
@@ -395,37 +399,38 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
         ok = warp_wait(smem_addr(&ctl->a_raw[s]), (a_phase >> s) & 1u, abort_flag, p.status);
         if (!ok) break;
         a_phase ^= 1u << s;
-        if (patch_finite(abase, kABytes, thread, kWorkThreads)) *(volatile int*)&ctl->spoilt = 1;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kABytes / 16 / kWorkThreads; ++i) bad |= patch_finite(abase + (uint32_t)(thread + i * kWorkThreads) * 16u);
+        if (bad) *(volatile int*)&ctl->spoilt = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
       }
       ra.next(C::kAStages);
-      if (!mixed) {
-        rz.next(z_stages);   // its one adapter
-        continue;
-      }
-      // four threads a token: its 16-byte pieces of each 64-column block
-      const int zt = thread >> 2, zq = thread & 3, t = c * kTokens + zt;
+      const int zs = rz.s;
+      rz.next(z_stages);
+      if (!mixed) continue;
+      // z's tile: four threads a token, which take its 8-column pieces in turn
+      const int zt = thread >> 2, t = c * kTokens + zt;
       const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
-      for (unsigned left = in & ~kMixed; left != 0; left &= left - 1u) {
-        const int l = l_lo + __ffs(left) - 1;
-        const int zs = rz.s;
-        rz.next(z_stages);
-        ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
-        if (!ok) break;
-        z_phase ^= 1u << zs;
-        if (mine != l) {
-          for (int b = 0; b * 64 < p.width; ++b) {
-            const uint32_t zrow = zbase + (uint32_t)(zs * p.z_bytes + b * 8192 + zt * 128);
-            sts128(zrow + 16u * zq, 0u, 0u, 0u, 0u);
-            sts128(zrow + 16u * (zq + 4), 0u, 0u, 0u, 0u);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_one(smem_addr(&ctl->z_ready[zs]));
+      const int first = mine >= l_lo && mine < l_hi ? (mine - l_lo) * p.group_cols : -p.width;   // its own columns
+      const int have = min(p.width, p.z_stride);   // u has R columns, which may be fewer than R16
+      const uint16_t* zrow = p.z + (size_t)t * p.z_stride;
+      ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
+      if (!ok) break;
+      z_phase ^= 1u << zs;
+      const uint32_t ztile = zbase + (uint32_t)(zs * p.z_stage + zt * 128);
+      const int all_cols = (l_hi - l_lo) * p.group_cols;
+#pragma unroll 4
+      for (int col = 8 * (thread & 3); col < all_cols; col += 32) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (col >= first && col < first + have) v = __ldcg(reinterpret_cast<const uint4*>(zrow + (col - first)));
+        sts128(ztile + (uint32_t)((col >> 6) * 8192 + ((((col >> 3) & 7) ^ (zt & 7)) << 4)), v.x, v.y, v.z, v.w);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_one(smem_addr(&ctl->z_ready[zs]));
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -461,7 +466,14 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
             }
-            if (spoilt && col < p.cols) spoilt_sums<PAIRS>(p, c0, c1, l, col, r0, v);
+            if (spoilt && col < p.cols) {
+              float w[16];   // a copy: the call's argument lives in memory, v in registers
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = v[i];
+              spoilt_sums<PAIRS>(p, c0, c1, l, col, r0, w);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = w[i];
+            }
             __syncwarp();
           }
           if (p.splits > 1) {
@@ -480,19 +492,35 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
         wgrad_epilogue_sync();
         if (ctl->last) {
           __threadfence();
-          const unsigned* masks = p.masks + (size_t)tp * p.splits;
+          // adapter g: bit sp set where share sp has a product
+          unsigned shares[kMaxPass];
+#pragma unroll
+          for (int g = 0; g < kMaxPass; ++g) shares[g] = 0;
+          unsigned mask[kMaxSplits];
+#pragma unroll
+          for (int sp = 0; sp < kMaxSplits; ++sp)
+            mask[sp] = sp < p.splits ? __ldcg(p.masks + (size_t)tp * p.splits + sp) : 0u;
+#pragma unroll
+          for (int sp = 0; sp < kMaxSplits; ++sp)
+#pragma unroll
+            for (int g = 0; g < kMaxPass; ++g) shares[g] |= (mask[sp] >> g & 1u) << sp;
           const float* base = p.partials + (size_t)tp * p.splits * unit_floats + row;
-          for (int l = l_lo; l < l_hi; ++l) {
-            const int g = l - l_lo;
+#pragma unroll
+          for (int g = 0; g < kMaxPass; ++g) {
+            if (l_lo + g >= l_hi) break;
             for (int r0 = 0; r0 < p.r16; r0 += 16) {
               float v[16] = {};
-              for (int sp = 0; sp < p.splits; ++sp) {
-                if (!(__ldcg(masks + sp) >> g & 1u)) continue;
-                const float* src = base + (size_t)sp * unit_floats + (size_t)(g * p.r16 + r0) * kCols;
+              const float* src = base + (size_t)(g * p.r16 + r0) * kCols;
+#pragma unroll 2
+              for (unsigned left = shares[g]; left != 0; left &= left - 1u) {   // in order of the shares
+                const float* part = src + (size_t)(__ffs(left) - 1) * unit_floats;
+                float w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += __ldcg(src + i * kCols);
+                for (int i = 0; i < 16; ++i) w[i] = __ldcg(part + i * kCols);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += w[i];
               }
-              if (col < p.cols) store_grad<PAIRS>(p, l, col, r0, v);
+              if (col < p.cols) store_grad<PAIRS>(p, l_lo + g, col, r0, v);
             }
           }
           if (row == 0) p.counters[tp] = 0u;   // ready for the next call
@@ -528,8 +556,7 @@ WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
   w.tiles = (cols + kCols - 1) / kCols;
   w.chunks = (m + kTokens - 1) / kTokens;
   w.group_cols = (width + 31) / 32 * 32;
-  w.per_pass = 512 / w.group_cols;
-  if (w.per_pass > kMaxGroups) w.per_pass = kMaxGroups;
+  w.per_pass = kMaxZCols / w.group_cols;
   if (w.per_pass > adapters) w.per_pass = adapters;
   w.passes = (adapters + w.per_pass - 1) / w.per_pass;
   // shares of the chunks: two blocks per SM, two chunks each at least, and no
@@ -553,13 +580,16 @@ cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensor
   p.per_pass = w.per_pass;
   p.r16 = rank16(p.ad.rank);
   p.z_bytes = (p.width + 63) / 64 * 8192;
+  const int all_cols = w.per_pass * w.group_cols;
+  p.z_stage = p.ad.ids == nullptr ? p.z_bytes : (all_cols + 63) / 64 * 8192;
   const int info_bytes = (int)align_up((size_t)(w.chunks + w.splits - 1) / w.splits * sizeof(unsigned), 16);
   // two blocks per SM where two z stages fit: the issuing threads bound a
   // block, at ~1000 cycles a chunk
-  int stages = (kZBudgetTwo - info_bytes) / p.z_bytes;
-  if (stages < 2) stages = (kZBudget - info_bytes) / p.z_bytes;
+  int stages = (kZBudgetTwo - info_bytes) / p.z_stage;
+  if (stages < 2) stages = (kZBudget - info_bytes) / p.z_stage;
   p.z_stages = stages < kMaxZStages ? stages : kMaxZStages;
   p.idesc = tc_idesc(p.width, true, true);
+  p.idesc_all = tc_idesc(all_cols, true, true);
   p.tmem_cols = 32;
   while ((int)p.tmem_cols < w.per_pass * w.group_cols) p.tmem_cols *= 2;
   const size_t units = (size_t)w.tiles * w.passes * w.splits;
@@ -570,7 +600,7 @@ cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensor
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units);
   cfg.blockDim = dim3(kWgradThreads);
-  cfg.dynamicSmemBytes = (size_t)WgradCfg<CODES>::kSrcBytes + (size_t)p.z_stages * p.z_bytes + info_bytes + kWgradFixed;
+  cfg.dynamicSmemBytes = (size_t)WgradCfg<CODES>::kSrcBytes + (size_t)p.z_stages * p.z_stage + info_bytes + kWgradFixed;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

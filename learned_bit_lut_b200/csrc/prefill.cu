@@ -120,6 +120,27 @@ __device__ __forceinline__ Extra extra_stage(int r16, int h) {
   return {rank0, (h & 1) * r16 + rank0, min(4, (r16 - rank0) / 16), false};
 }
 
+// Patches the first `steps` 16-deep steps of M's tile (128 rows x 64 rank
+// columns, or TRANS two halves of 64 rank rows x 64 columns); true if this
+// thread took anything out.
+template <bool TRANS, int THREADS>
+__device__ __forceinline__ bool patch_tile(uint32_t tile, int steps, int thread) {
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4 * 256 / THREADS; ++i) {
+    const int e = thread + i * THREADS;   // 256 16-byte pieces a step
+    if (e >= 256 * steps) break;
+    if (TRANS) {
+      const int per_half = 128 * steps;
+      found |= patch_finite(tile + (uint32_t)(e < per_half ? e * 16 : kAStageBytes / 2 + (e - per_half) * 16));
+    } else {
+      const int row = e & 127, c = e >> 7;
+      found |= patch_finite(tile + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
+    }
+  }
+  return found;
+}
+
 // What patch_finite took out of the products of token t and output row: the
 // non-finite entries of its adapter's row times z.
 template <bool TRANS>
@@ -331,17 +352,17 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             const int s = (it + e - e0) % kStages;
             const int l = l_next;
             if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
-            ok = __all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->raw[s]), (raw_phase >> s) & 1u, abort_flag, status));
+            // the first one comes at the end of the tile's main loop
+            const uint32_t rb = smem_addr(&ctl->raw[s]), rp = (raw_phase >> s) & 1u;
+            ok = __all_sync(0xFFFFFFFFu, e == e0 ? gemm_wait_idle(rb, rp, abort_flag, status)
+                                                 : gemm_wait(rb, rp, abort_flag, status));
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
-            if (patch_finite(sa(s), kAStageBytes, thread, kPatchThreads)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (patch_tile<TRANS, kPatchThreads>(sa(s), extra_stage(lora.r16, e % per).steps, thread))
+              *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
 #pragma unroll
             for (int i = 0; i < kBN / kPatchThreads; ++i)
-              if (id[i] != l) {
-                const uint32_t zrow = sb(s) + (uint32_t)(thread + i * kPatchThreads) * 128u;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) sts128(zrow + 16u * c, 0u, 0u, 0u, 0u);
-              }
+              if (id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
@@ -664,11 +685,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             if (!mixed) continue;
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
-            if (patch_finite(sa(s), kAStageBytes, thread, 32 * kFusedDecoders)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
-            if (thread < BN && id != l) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) sts128(sb(s) + (uint32_t)thread * 128u + 16u * c, 0u, 0u, 0u, 0u);
-            }
+            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), extra_stage(lora.r16, e % per).steps, thread))
+              *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (thread < BN && id != l) zero_row(sb(s), thread);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));

@@ -134,6 +134,16 @@ __device__ __forceinline__ void tc_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
       : "memory");
 }
 
+// Zeroes 32 columns of this warp's tensor-memory lanes.
+__device__ __forceinline__ void tc_zero_x32(uint32_t taddr) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, "
+      "%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr),
+      "r"(0u)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
@@ -189,19 +199,21 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in eac
   return ~((bad >> 15) * 0xFFFFu);
 }
 
-// Takes the infinities and NaN out of `bytes` of shared memory; true if this
-// thread found any.
-__device__ __forceinline__ bool patch_finite(uint32_t addr, int bytes, int thread, int threads) {
-  bool found = false;
-  for (int e = thread * 16; e < bytes; e += threads * 16) {
-    const uint4 v = lds128(addr + e);
-    const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
-    if ((a & b & c & d) != 0xFFFFFFFFu) {
-      sts128(addr + e, v.x & a, v.y & b, v.z & c, v.w & d);
-      found = true;
-    }
-  }
+// Takes the infinities and NaN out of the 16 bytes at addr; true if there were any.
+__device__ __forceinline__ bool patch_finite(uint32_t addr) {
+  const uint4 v = lds128(addr);
+  const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
+  const bool found = (a & b & c & d) != 0xFFFFFFFFu;
+  if (found) sts128(addr, v.x & a, v.y & b, v.z & c, v.w & d);
   return found;
+}
+
+// Zeroes row `row` (128 bytes) of a tile at addr; neighbouring threads take
+// neighbouring rows, so the pieces go in the swizzle's order, which keeps 8
+// rows on different banks.
+__device__ __forceinline__ void zero_row(uint32_t addr, int row) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) sts128(addr + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)), 0u, 0u, 0u, 0u);
 }
 
 // bf16 matrix of rows x cols (row-major) as 2-D boxes of box_rows x 64
