@@ -379,18 +379,27 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values, or their bi
 _BYTES = (torch.uint8,)
 _INT8, _INT32, _FP32 = (torch.int8,), (torch.int32,), (torch.float32,)
 _HEADER_BYTES = lib.any4_lora_header_bytes()
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
-def _on_device(call):
-    """Runs ``call`` with its first tensor's device current (the library
-    launches on the current device)."""
-    @functools.wraps(call)
-    def run(first, *args, **kwargs):
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return call(first, *args, **kwargs)
-        return call(first, *args, **kwargs)
-    return run
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _on_device(name: str):
+    """Runs a call with the device of its first tensor, argument ``name``,
+    current (the library launches on the current device)."""
+    def wrap(call):
+        @functools.wraps(call)
+        def run(*args, **kwargs):
+            t = args[0] if args else kwargs.get(name)
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+                raise ValueError(f"{name} must be a 2-dimensional CUDA tensor")
+            if t.get_device() == _current_device():
+                return call(*args, **kwargs)
+            with torch.cuda.device(t.device):
+                return call(*args, **kwargs)
+        return run
+    return wrap
 
 
 @functools.lru_cache(maxsize=1024)
@@ -408,19 +417,13 @@ _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_
 _LORA_WORKSPACES: dict = {}
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-dimensional CUDA tensor")
-    return t.shape[0]
-
-
-def _adapter_workspace(need: int, device: torch.device) -> torch.Tensor:
+def _adapter_workspace(need: int, device: torch.device, stream: int) -> torch.Tensor:
     """A workspace with a zeroed header: kept per stream and grown on demand,
     or, while a CUDA graph is captured, one of the graph's own."""
     if need == 0:
         raise Any4Error(ANY4_ESHAPE)
-    if not torch.cuda.is_current_stream_capturing():
-        key = (device.index, _stream(device))
+    if not _capturing():
+        key = (device.index, stream)
         ws = _LORA_WORKSPACES.get(key)
         if ws is not None and ws.numel() >= need:
             return ws
@@ -462,7 +465,7 @@ def any4_lora_grad_workspace_bytes(m: int, n: int, k: int, group: int, adapters:
     return lib.any4_lora_grad_workspace_bytes(bits, m, n, k, group, adapters, rank)
 
 
-@_on_device
+@_on_device("x")
 def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, group: int, a: torch.Tensor,
                      b: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor | None = None, bits: int = 4,
                      out: torch.Tensor | None = None, u: torch.Tensor | None = None,
@@ -472,22 +475,26 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
     token (a: L x R x K, b: L x N x R bf16, scale: L fp32, ids: M int32; ids
     outside [0, L) have no adapter, None is adapter 0 for every token).
     ``u`` (M x R bf16) is written where given, for any4_linear_lora_grad."""
-    m = _rows(x, "x")
-    dev = x.device
+    m, dev = x.shape[0], x.device
     ad = _adapters(a, b, scale, ids, m, n, k, dev)
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        out_p = out.data_ptr()
+    else:
+        out_p = _typed(out, "out", _BF16, dev, (m, n))
+    stream = _stream(dev)
     if workspace is None:
-        workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev)
-    _check(lib.any4_linear_lora(
-        bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k,
-        group, *ad, _typed(out, "out", _BF16, dev, (m, n)),
+        workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev, stream)
+    st = lib.any4_linear_lora(
+        bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k, group, *ad, out_p,
         None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5])),
-        _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), _stream(dev)))
+        _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), stream)
+    if st != ANY4_OK:
+        raise Any4Error(st)
     return out
 
 
-@_on_device
+@_on_device("dy")
 def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: torch.Tensor | None, n: int, k: int,
                           group: int, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
                           ids: torch.Tensor | None = None, bits: int = 4,
@@ -498,8 +505,7 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
     not named in ``outputs``. ``x`` is the forward's bf16 input or the
     (codes, steps) pair any4_act_pack made of it (needed for da), ``u`` what
     the forward wrote (needed for db), ``packed`` the weight (for dx)."""
-    m = _rows(dy, "dy")
-    dev = dy.device
+    m, dev = dy.shape[0], dy.device
     unknown = set(outputs) - {"dx", "da", "db"}
     if unknown or not outputs:
         raise ValueError(f"outputs must name some of dx, da and db, got {tuple(outputs)}")
@@ -513,6 +519,7 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
             return None, None
         if t is None:
             t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            return t, t.data_ptr()
         return t, _typed(t, name, _BF16, dev, shape)
 
     dx, dx_p = made("dx", dx, (m, k))
@@ -533,40 +540,40 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
             x_p = _typed(x, "x", _BF16, dev, (m, k))
     u_p = _typed(u, "u", _BF16, dev, (m, rank)) if db is not None else None
     w_p = _weight(packed, n, k, group, bits, dev) if dx is not None else None
+    stream = _stream(dev)
     if workspace is None:
-        workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev)
+        workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev, stream)
     _check(lib.any4_linear_lora_grad(
         bits, _typed(dy, "dy", _BF16, dev, (m, n)), x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad,
         dx_p, da_p, db_p, _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
-        _stream(dev)))
+        stream))
     return dx, da, db
 
 
-@_on_device
+@_on_device("x")
 def any4_act_pack(x: torch.Tensor, group: int, codes: torch.Tensor | None = None,
                   steps: torch.Tensor | None = None) -> tuple:
     """8-bit checkpoint of an activation x (M x K bf16): (codes, steps), one
     int8 per value and one bf16 step per token and ``group`` columns."""
-    m = _rows(x, "x")
-    k, dev = x.shape[1], x.device
+    (m, k), dev = x.shape, x.device
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
     if codes is None:
         codes = torch.empty((m, k), dtype=torch.int8, device=dev)
     if steps is None:
         steps = torch.empty((m, k // group), dtype=torch.bfloat16, device=dev)
-    _check(lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group,
-                             _typed(codes, "codes", _INT8, dev, (m, k)),
-                             _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev)))
+    st = lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group, _typed(codes, "codes", _INT8, dev, (m, k)),
+                           _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev))
+    if st != ANY4_OK:
+        raise Any4Error(st)
     return codes, steps
 
 
-@_on_device
+@_on_device("codes")
 def any4_act_unpack(codes: torch.Tensor, steps: torch.Tensor, group: int,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """The bf16 values (M x K) an 8-bit checkpoint stands for."""
-    m = _rows(codes, "codes")
-    k, dev = codes.shape[1], codes.device
+    (m, k), dev = codes.shape, codes.device
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
     if out is None:

@@ -73,6 +73,8 @@ template <int RUNS>
 __global__ void __launch_bounds__(kActThreads) act_pack_kernel(const uint16_t* __restrict__ x, size_t runs,
                                                                int lanes_shift, uint8_t* __restrict__ codes,
                                                                uint16_t* __restrict__ steps) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const size_t thread = (size_t)blockIdx.x * kActThreads + threadIdx.x;
   const int lanes = 1 << lanes_shift;
   const size_t group = thread >> lanes_shift;   // lanes divides 32: a group never leaves its warp
@@ -120,6 +122,8 @@ __global__ void __launch_bounds__(kActThreads) act_pack_kernel(const uint16_t* _
 __global__ void __launch_bounds__(kActThreads) act_unpack_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint16_t* __restrict__ steps, size_t runs,
                                                                  int runs_shift, uint16_t* __restrict__ x) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const size_t run = (size_t)blockIdx.x * kActThreads + threadIdx.x;
   if (run >= runs) return;
   const uint4 c = ld_stream_v4(codes + run * 16);
@@ -133,6 +137,21 @@ __global__ void __launch_bounds__(kActThreads) act_unpack_kernel(const uint8_t* 
   uint4* out = reinterpret_cast<uint4*>(x + run * 16);
   out[0] = lo;
   out[1] = hi;
+}
+
+// As a programmatic dependent: the launch overlaps the previous kernel's end.
+template <typename... P, typename... A>
+cudaError_t launch_act(void (*kernel)(P...), unsigned blocks, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kActThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -154,11 +173,8 @@ ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* c
   while ((16 * per << shift) < group) ++shift;
   const unsigned blocks = (unsigned)((runs / per + any4::kActThreads - 1) / any4::kActThreads);
   uint8_t* c = reinterpret_cast<uint8_t*>(codes);
-  if (per == 2)
-    any4::act_pack_kernel<2><<<blocks, any4::kActThreads, 0, (cudaStream_t)stream>>>(x, runs, shift, c, steps);
-  else
-    any4::act_pack_kernel<1><<<blocks, any4::kActThreads, 0, (cudaStream_t)stream>>>(x, runs, shift, c, steps);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = any4::launch_act(per == 2 ? any4::act_pack_kernel<2> : any4::act_pack_kernel<1>, blocks,
+                                         (cudaStream_t)stream, x, runs, shift, c, steps);
   return e == cudaSuccess ? ANY4_OK : any4::record_cuda_error(e);
 }
 
@@ -171,9 +187,8 @@ ANY4_API int any4_act_unpack(const int8_t* codes, const uint16_t* steps, int m, 
   int shift = 0;
   while ((16 << shift) < group) ++shift;
   const unsigned blocks = (unsigned)((runs + any4::kActThreads - 1) / any4::kActThreads);
-  any4::act_unpack_kernel<<<blocks, any4::kActThreads, 0, (cudaStream_t)stream>>>(
-      reinterpret_cast<const uint8_t*>(codes), steps, runs, shift, x);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = any4::launch_act(any4::act_unpack_kernel, blocks, (cudaStream_t)stream,
+                                         reinterpret_cast<const uint8_t*>(codes), steps, runs, shift, x);
   return e == cudaSuccess ? ANY4_OK : any4::record_cuda_error(e);
 }
 
