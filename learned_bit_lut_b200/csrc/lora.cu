@@ -67,24 +67,36 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = adapter_of(ad, t);
   const int rows = ad.rank / kDeltaCluster;
+  const int row0 = slice * kDeltaRows + rank * kDeltaThreads + threadIdx.x;   // and kDeltaCluster * kDeltaThreads on
   if (l >= 0) {
+    // phase 2's rows of B towards L2 while phase 1 runs
+    for (int row = row0; row < n && row < row0 + 2 * kDeltaCluster * kDeltaThreads; row += kDeltaCluster * kDeltaThreads) {
+      const uint16_t* br = ad.b + ((size_t)l * n + row) * ad.rank;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(br));
+      if (ad.rank > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(br + 64));
+    }
     const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * k);
     const uint4* ar = reinterpret_cast<const uint4*>(ad.a + ((size_t)l * ad.rank + rank) * k);
     const size_t row_step = (size_t)kDeltaCluster * (k / 8);
     const int c0 = warp * (k / 64), c1 = c0 + k / 64;   // this warp's 16-byte pieces of a row
-    for (int i0 = 0; i0 < rows; i0 += 4) {
-      float acc[4] = {};
+    for (int i0 = 0; i0 < rows; i0 += 8) {   // 8 rows' loads in flight
+      float acc[8] = {};
       for (int c = c0 + lane; c < c1; c += 32) {
         const uint4 xv = __ldg(xr + c);
+        uint4 av[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i0 + i < rows) acc[i] = dot8(__ldcg(ar + (i0 + i) * row_step + c), xv, acc[i]);
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < rows) av[i] = __ldcg(ar + (i0 + i) * row_step + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < rows) acc[i] = dot8(av[i], xv, acc[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i >= rows) break;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], d);
-        if (lane == 0 && i0 + i < rows) part[warp][i0 + i] = acc[i];
+        if (lane == 0) part[warp][i0 + i] = acc[i];
       }
     }
   }
@@ -105,19 +117,29 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int row = slice * kDeltaRows + (h * kDeltaCluster + rank) * kDeltaThreads + threadIdx.x;
+    const int row = row0 + h * kDeltaCluster * kDeltaThreads;
     if (row >= n) break;
     float acc = 0.0f;
     if (l >= 0) {
       const uint4* br = reinterpret_cast<const uint4*>(ad.b + ((size_t)l * n + row) * ad.rank);
-#pragma unroll 4
-      for (int c = 0; c < ad.rank / 8; ++c) {
-        const uint4 q = __ldcg(br + c);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      for (int c0 = 0; c0 < ad.rank / 8; c0 += 8) {   // 64 ranks' loads in flight
+        uint4 q[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc = fmaf(us[8 * c + 2 * i], bf16_bits_to_float(w[i] & 0xFFFFu), acc);
-          acc = fmaf(us[8 * c + 2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u), acc);
+        for (int i = 0; i < 8; ++i)
+          if (c0 + i < ad.rank / 8) q[i] = __ldcg(br + c0 + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (c0 + i >= ad.rank / 8) break;
+          const float4* uv = reinterpret_cast<const float4*>(us + 8 * (c0 + i));
+          const float4 u0 = uv[0], u1 = uv[1];
+          acc = fmaf(u0.x, bf16_bits_to_float(q[i].x & 0xFFFFu), acc);
+          acc = fmaf(u0.y, __uint_as_float(q[i].x & 0xFFFF0000u), acc);
+          acc = fmaf(u0.z, bf16_bits_to_float(q[i].y & 0xFFFFu), acc);
+          acc = fmaf(u0.w, __uint_as_float(q[i].y & 0xFFFF0000u), acc);
+          acc = fmaf(u1.x, bf16_bits_to_float(q[i].z & 0xFFFFu), acc);
+          acc = fmaf(u1.y, __uint_as_float(q[i].z & 0xFFFF0000u), acc);
+          acc = fmaf(u1.z, bf16_bits_to_float(q[i].w & 0xFFFFu), acc);
+          acc = fmaf(u1.w, __uint_as_float(q[i].w & 0xFFFF0000u), acc);
         }
       }
     }

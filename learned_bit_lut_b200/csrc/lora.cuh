@@ -82,15 +82,21 @@ struct AdapterTerm {
   const uint16_t* pairs;
 };
 
-// dA (of the kept input: bf16 x, or codes and steps with groups of x_group) and
-// dB, from v as pairs and the kept u (lora_wgrad.cu). `space` holds
-// wgrad_partials_bytes of partial sums.
-size_t wgrad_partials_bytes(int m, int cols, int adapters, int width, int num_sms);
-cudaError_t launch_da(const uint16_t* x, const int8_t* codes, const uint16_t* steps, int x_group, const uint16_t* pairs,
-                      const Adapters& ad, const SlotLists& lists, int m, int k, uint16_t* da, void* space,
-                      unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
-cudaError_t launch_db(const uint16_t* dy, const uint16_t* u, const Adapters& ad, const SlotLists& lists, int m, int n,
-                      uint16_t* db, void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
+// The forward's input as it was kept: bf16, or codes and steps with groups of
+// `group` columns (x null).
+struct KeptInput {
+  const uint16_t* x;
+  const int8_t* codes;
+  const uint16_t* steps;
+  int group;
+};
+
+// dA and dB (either may be null), from v as pairs and the kept input and u
+// (lora_wgrad.cu). `space` holds wgrad_partials_bytes of partial sums.
+size_t wgrad_partials_bytes(int m, int n, int k, int adapters, int rank, int num_sms);
+cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t* pairs, const uint16_t* u,
+                         const Adapters& ad, const SlotLists& lists, int m, int n, int k, uint16_t* da, uint16_t* db,
+                         void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
 
 // y = x . W_hat^T + u . B_l^T for M > 16 (prefill.cu); the workspace is
 // any4_linear's.

@@ -24,8 +24,8 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The workspace: any4_linear's header, W_hat in bf16, v as a bf16 pair, the
-// adapters of each token tile, then the partial sums of v, dx, dA and dB
-// (which follow each other).
+// adapters of each token tile, then the partial sums of v, of dx and of
+// dA and dB (which follow each other).
 struct GradSpace {
   size_t what, pairs, lists, partials, total;
 };
@@ -41,9 +41,7 @@ GradSpace grad_space(const Layout& L, int m, int adapters, int rank, int sms) {
   s.pairs = take(pairs_bytes(m, rank));
   s.lists = take(slot_lists_bytes(m));
   const size_t down = down_partials_bytes(m, L.n, rank, sms), dx = dx_partials_bytes(L, m, sms);
-  const size_t da = wgrad_partials_bytes(m, L.k, adapters, 2 * rank16(rank), sms);
-  const size_t db = wgrad_partials_bytes(m, L.n, adapters, rank16(rank), sms);
-  s.partials = take(std::max(std::max(down, dx), std::max(da, db)));
+  s.partials = take(std::max(std::max(down, dx), wgrad_partials_bytes(m, L.n, L.k, adapters, rank, sms)));
   s.total = at;
   return s;
 }
@@ -112,10 +110,10 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
   if (e == cudaSuccess && (dx || da))
     e = launch_down(true, dy, ad, term.lists[1], m, n, k, pairs, nullptr, partials, counters, status, sms, st);
   if (e == cudaSuccess && dx) e = launch_dx(dy, what, L, m, dx, partials, counters, status, sms, term, st);
-  if (e == cudaSuccess && da)
-    e = launch_da(kept8 ? nullptr : x, x_codes, x_steps, x_group, pairs, ad, term.lists[0], m, k, da, partials, counters,
-                  status, sms, st);
-  if (e == cudaSuccess && db) e = launch_db(dy, u, ad, term.lists[0], m, n, db, partials, counters, status, sms, st);
+  if (e == cudaSuccess && (da || db)) {
+    const KeptInput kept = {kept8 ? nullptr : x, x_codes, x_steps, x_group};
+    e = launch_wgrad(dy, kept, pairs, u, ad, term.lists[0], m, n, k, da, db, partials, counters, status, sms, st);
+  }
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);
 }
 

@@ -23,7 +23,8 @@
 //
 // Blocks: 128 columns of src x a share of the chunks x as many adapters as
 // one instruction holds (256 columns). Shares of the chunks are added by the
-// last block to arrive, in order.
+// last block to arrive, with all its threads, in order. dA and dB are one
+// launch: neither fills the GPU for few tokens.
 //
 // Warps: 0 = TMA of src, 1 = MMA, 2-5 = epilogue, 6-13 = codes and patches,
 // 14 = TMA of z.
@@ -141,7 +142,7 @@ __device__ __noinline__ void spoilt_sums(const WgradParams& p, int c0, int c1, i
   }
 }
 
-// 16 rank values of one src column to the output: dA [L][R][cols] (PAIRS) or
+// 16 rank values of one src column to the output (one share of the chunks): dA [L][R][cols] (PAIRS) or
 // dB [L][cols][R].
 template <bool PAIRS>
 __device__ __forceinline__ void store_grad(const WgradParams& p, int l, int col, int r0, const float (&v)[16]) {
@@ -167,12 +168,11 @@ __device__ __forceinline__ void store_grad(const WgradParams& p, int l, int col,
   }
 }
 
-// PAIRS: z is a bf16 pair and the result dA; else z is u and the result dB.
-// CODES: src is an 8-bit checkpoint.
+// One block. PAIRS: z is a bf16 pair and the result dA; else z is u and the
+// result dB. CODES: src is an 8-bit checkpoint.
 template <bool PAIRS, bool CODES>
-__global__ void __launch_bounds__(kWgradThreads, 2)
-    adapter_wgrad_kernel(const __grid_constant__ CUtensorMap smap, const __grid_constant__ CUtensorMap zmap,
-                         const __grid_constant__ WgradParams p) {
+__device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUtensorMap& zmap, const WgradParams& p,
+                                            const int unit) {
   using C = WgradCfg<CODES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
   unsigned* info = reinterpret_cast<unsigned*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort_flag;
   // unit: column tile, then pass, then share of the chunks
-  const int unit = blockIdx.x, split = unit % p.splits, tp = unit / p.splits;
+  const int split = unit % p.splits, tp = unit / p.splits;
   const int pass = tp % p.passes, ct = tp / p.passes;
   const int c0 = (int)((long long)split * p.chunks / p.splits), c1 = (int)((long long)(split + 1) * p.chunks / p.splits);
   const int l_lo = pass * p.per_pass, l_hi = min(p.ad.count, l_lo + p.per_pass);
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
     ctl->abort_flag = 0;
     ctl->spoilt = 0;
     ctl->touched = 0;
+    ctl->last = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
       const unsigned touched = *(volatile unsigned*)&ctl->touched;
       const int spoilt = *(volatile int*)&ctl->spoilt;
       const size_t unit_floats = (size_t)p.per_pass * p.r16 * kCols;
-      float* part = p.partials + (size_t)unit * unit_floats + row;
+      // PAIRS [adapter][rank][column], else [adapter][column][rank]: as the output's
+      float* part = p.partials + (size_t)unit * unit_floats + (PAIRS ? row : row * p.r16);
       for (int l = l_lo; l < l_hi; ++l) {
         const int g = l - l_lo;
         const bool has = touched >> g & 1u;
@@ -477,8 +479,15 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
             __syncwarp();
           }
           if (p.splits > 1) {
+            if (PAIRS) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) __stcg(part + ((size_t)g * p.r16 + r0 + i) * kCols, v[i]);
+              for (int i = 0; i < 16; ++i) __stcg(part + (g * p.r16 + r0 + i) * kCols, v[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                __stcg(reinterpret_cast<float4*>(part + g * p.r16 * kCols + r0) + i,
+                       make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            }
           } else if (col < p.cols) {
             store_grad<PAIRS>(p, l, col, r0, v);
           }
@@ -489,49 +498,68 @@ __global__ void __launch_bounds__(kWgradThreads, 2)
         __threadfence();
         wgrad_epilogue_sync();
         if (row == 0) ctl->last = atomicAdd(p.counters + tp, 1u) == (unsigned)(p.splits - 1);
-        wgrad_epilogue_sync();
-        if (ctl->last) {
-          __threadfence();
-          // adapter g: bit sp set where share sp has a product
-          unsigned shares[kMaxPass];
-#pragma unroll
-          for (int g = 0; g < kMaxPass; ++g) shares[g] = 0;
-          unsigned mask[kMaxSplits];
-#pragma unroll
-          for (int sp = 0; sp < kMaxSplits; ++sp)
-            mask[sp] = sp < p.splits ? __ldcg(p.masks + (size_t)tp * p.splits + sp) : 0u;
-#pragma unroll
-          for (int sp = 0; sp < kMaxSplits; ++sp)
-#pragma unroll
-            for (int g = 0; g < kMaxPass; ++g) shares[g] |= (mask[sp] >> g & 1u) << sp;
-          const float* base = p.partials + (size_t)tp * p.splits * unit_floats + row;
-#pragma unroll
-          for (int g = 0; g < kMaxPass; ++g) {
-            if (l_lo + g >= l_hi) break;
-            for (int r0 = 0; r0 < p.r16; r0 += 16) {
-              float v[16] = {};
-              const float* src = base + (size_t)(g * p.r16 + r0) * kCols;
-#pragma unroll 2
-              for (unsigned left = shares[g]; left != 0; left &= left - 1u) {   // in order of the shares
-                const float* part = src + (size_t)(__ffs(left) - 1) * unit_floats;
-                float w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __ldcg(part + i * kCols);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += w[i];
-              }
-              if (col < p.cols) store_grad<PAIRS>(p, l_lo + g, col, r0, v);
-            }
-          }
-          if (row == 0) p.counters[tp] = 0u;   // ready for the next call
-        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (ctl->last) {
+    __threadfence();
+    unsigned* shares = info;   // adapter g: bit sp set where share sp has a product
+    if (threadIdx.x < kMaxPass) {
+      unsigned bits = 0;
+#pragma unroll 4
+      for (int sp = 0; sp < p.splits; ++sp) bits |= (__ldcg(p.masks + (size_t)tp * p.splits + sp) >> threadIdx.x & 1u) << sp;
+      shares[threadIdx.x] = bits;
+    }
+    __syncthreads();
+    const size_t unit_floats = (size_t)p.per_pass * p.r16 * kCols;
+    const float* base = p.partials + (size_t)tp * p.splits * unit_floats;
+    const int per_adapter = p.r16 * (kCols / 4);   // four values a step, in the output's order
+#pragma unroll 2
+    for (int i = threadIdx.x; i < (l_hi - l_lo) * per_adapter; i += kWgradThreads) {
+      const int g = i / per_adapter, q = i - g * per_adapter;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float* src = base + (size_t)i * 4;
+#pragma unroll 4
+      for (int sp = 0; sp < p.splits; ++sp) {   // in order of the shares
+        if (!(shares[g] >> sp & 1u)) continue;
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src + (size_t)sp * unit_floats));
+        v.x += f.x;
+        v.y += f.y;
+        v.z += f.z;
+        v.w += f.w;
+      }
+      const int r = PAIRS ? q / (kCols / 4) : q % (p.r16 / 4) * 4;
+      const int col = ct * kCols + (PAIRS ? q % (kCols / 4) * 4 : q / (p.r16 / 4));
+      if (r >= p.ad.rank || col >= p.cols) continue;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      const size_t at = PAIRS ? ((size_t)(l_lo + g) * p.ad.rank + r) * p.cols + col
+                              : ((size_t)(l_lo + g) * p.cols + col) * p.ad.rank + r;
+      *reinterpret_cast<uint2*>(p.out + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    if (threadIdx.x == 0) p.counters[tp] = 0u;   // ready for the next call
+  }
   if (warp == 1) tc_free(tmem, p.tmem_cols);
+}
+
+struct WgradJob {
+  CUtensorMap smap, zmap;
+  WgradParams p;
+  int units;
+};
+
+// The blocks of dB, then those of dA (either may have none).
+template <bool CODES>
+__global__ void __launch_bounds__(kWgradThreads, 2)
+    adapter_wgrad_kernel(const __grid_constant__ WgradJob db, const __grid_constant__ WgradJob da) {
+  const int unit = blockIdx.x;
+  if (unit < db.units)
+    wgrad_block<false, false>(db.smap, db.zmap, db.p, unit);
+  else
+    wgrad_block<true, CODES>(da.smap, da.zmap, da.p, unit - db.units);
 }
 
 template <auto Kernel>
@@ -569,9 +597,9 @@ WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
   return w;
 }
 
-template <bool PAIRS, bool CODES>
-cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensorMap& zmap, void* space, int num_sms,
-                         cudaStream_t stream) {
+// Fills in a job's plan; the shared memory its blocks need.
+size_t plan_job(WgradJob* job, void* space, int num_sms) {
+  WgradParams& p = job->p;
   const WgradPlan w = wgrad_plan(p.m, p.cols, p.ad.count, p.width, num_sms);
   p.chunks = w.chunks;
   p.splits = w.splits;
@@ -582,7 +610,8 @@ cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensor
   p.z_bytes = (p.width + 63) / 64 * 8192;
   const int all_cols = w.per_pass * w.group_cols;
   p.z_stage = p.ad.ids == nullptr ? p.z_bytes : (all_cols + 63) / 64 * 8192;
-  const int info_bytes = (int)align_up((size_t)(w.chunks + w.splits - 1) / w.splits * sizeof(unsigned), 16);
+  const int info_words = (w.chunks + w.splits - 1) / w.splits;
+  const int info_bytes = (int)align_up((size_t)(info_words > kMaxPass ? info_words : kMaxPass) * sizeof(unsigned), 16);
   // two blocks per SM where two z stages fit: the issuing threads bound a
   // block, at ~1000 cycles a chunk
   int stages = (kZBudgetTwo - info_bytes) / p.z_stage;
@@ -591,82 +620,92 @@ cudaError_t launch_wgrad(WgradParams& p, const CUtensorMap& smap, const CUtensor
   p.idesc = tc_idesc(p.width, true, true);
   p.idesc_all = tc_idesc(all_cols, true, true);
   p.tmem_cols = 32;
-  while ((int)p.tmem_cols < w.per_pass * w.group_cols) p.tmem_cols *= 2;
-  const size_t units = (size_t)w.tiles * w.passes * w.splits;
+  while ((int)p.tmem_cols < all_cols) p.tmem_cols *= 2;
+  job->units = w.tiles * w.passes * w.splits;
   p.masks = static_cast<unsigned*>(space);
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + align_up(units * sizeof(unsigned), kAlign));
-  cudaError_t e = allow_smem<adapter_wgrad_kernel<PAIRS, CODES>>(kWgradSmem);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + align_up((size_t)job->units * sizeof(unsigned), kAlign));
+  return (size_t)WgradCfg<false>::kSrcBytes + (size_t)p.z_stages * p.z_stage + info_bytes + kWgradFixed;
+}
+
+size_t job_bytes(int m, int cols, int adapters, int rank, int width, int num_sms) {
+  const WgradPlan w = wgrad_plan(m, cols, adapters, width, num_sms);
+  if (w.splits == 1) return 0;
+  const size_t units = (size_t)w.tiles * w.passes * w.splits;
+  return align_up(units * sizeof(unsigned), kAlign) +
+         align_up(units * w.per_pass * rank16(rank) * kCols * sizeof(float), kAlign);
+}
+
+}  // namespace
+
+size_t wgrad_partials_bytes(int m, int n, int k, int adapters, int rank, int num_sms) {
+  return job_bytes(m, n, adapters, rank, rank16(rank), num_sms) +
+         job_bytes(m, k, adapters, rank, 2 * rank16(rank), num_sms);
+}
+
+cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t* pairs, const uint16_t* u,
+                         const Adapters& ad, const SlotLists& lists, int m, int n, int k, uint16_t* da, uint16_t* db,
+                         void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
+  WgradJob ja{}, jb{};
+  size_t smem = 0;
+  if (db != nullptr) {
+    WgradParams& p = jb.p;
+    p.ad = ad;
+    p.lists = lists;
+    p.m = m;
+    p.cols = n;
+    p.width = rank16(ad.rank);
+    p.src = dy;
+    p.z = u;
+    p.z_stride = ad.rank;
+    p.out = db;
+    p.counters = counters;
+    p.status = status;
+    if (!encode_bf16_map(&jb.smap, dy, m, n, kTokens) || !encode_bf16_map(&jb.zmap, u, m, ad.rank, kTokens))
+      return cudaErrorInvalidValue;
+    smem = plan_job(&jb, space, num_sms);
+    if (jb.p.splits > 1) counters += jb.units / jb.p.splits;
+  }
+  if (da != nullptr) {
+    WgradParams& p = ja.p;
+    p.ad = ad;
+    p.lists = lists;
+    p.m = m;
+    p.cols = k;
+    p.width = 2 * rank16(ad.rank);
+    p.src = x.x;
+    p.codes = reinterpret_cast<const uint8_t*>(x.codes);
+    p.steps = x.steps;
+    p.z = pairs;
+    p.z_stride = p.width;
+    p.out = da;
+    p.counters = counters;
+    p.status = status;
+    if (!encode_bf16_map(&ja.zmap, pairs, m, p.width, kTokens)) return cudaErrorInvalidValue;
+    if (x.codes != nullptr) {
+      while ((1 << p.step_shift) < x.group) ++p.step_shift;
+      p.step_cols = k >> p.step_shift;
+    }
+    if (x.codes != nullptr ? !encode_u8_map(&ja.smap, x.codes, m, k, kTokens) : !encode_bf16_map(&ja.smap, x.x, m, k, kTokens))
+      return cudaErrorInvalidValue;
+    const size_t db_bytes = db != nullptr ? job_bytes(m, n, ad.count, ad.rank, rank16(ad.rank), num_sms) : 0;
+    const size_t bytes = plan_job(&ja, static_cast<uint8_t*>(space) + db_bytes, num_sms);
+    if (bytes > smem) smem = bytes;
+  }
+  cudaError_t e = x.codes != nullptr ? allow_smem<adapter_wgrad_kernel<true>>(kWgradSmem)
+                                     : allow_smem<adapter_wgrad_kernel<false>>(kWgradSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units);
+  cfg.gridDim = dim3((unsigned)(ja.units + jb.units));
   cfg.blockDim = dim3(kWgradThreads);
-  cfg.dynamicSmemBytes = (size_t)WgradCfg<CODES>::kSrcBytes + (size_t)p.z_stages * p.z_stage + info_bytes + kWgradFixed;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<PAIRS, CODES>, smap, zmap, p);
-}
-
-}  // namespace
-
-size_t wgrad_partials_bytes(int m, int cols, int adapters, int width, int num_sms) {
-  const WgradPlan w = wgrad_plan(m, cols, adapters, width, num_sms);
-  if (w.splits == 1) return 0;
-  const size_t units = (size_t)w.tiles * w.passes * w.splits;
-  const int r16 = width;   // at least the rows of a partial sum
-  return align_up(units * sizeof(unsigned), kAlign) + align_up(units * w.per_pass * r16 * kCols * sizeof(float), kAlign);
-}
-
-cudaError_t launch_da(const uint16_t* x, const int8_t* codes, const uint16_t* steps, int x_group, const uint16_t* pairs,
-                      const Adapters& ad, const SlotLists& lists, int m, int k, uint16_t* da, void* space,
-                      unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
-  WgradParams p{};
-  p.ad = ad;
-  p.lists = lists;
-  p.m = m;
-  p.cols = k;
-  p.width = 2 * rank16(ad.rank);
-  p.src = x;
-  p.codes = reinterpret_cast<const uint8_t*>(codes);
-  p.steps = steps;
-  p.z = pairs;
-  p.z_stride = p.width;
-  p.out = da;
-  p.counters = counters;
-  p.status = status;
-  CUtensorMap smap, zmap;
-  if (!encode_bf16_map(&zmap, pairs, m, p.width, kTokens)) return cudaErrorInvalidValue;
-  if (codes == nullptr) {
-    if (!encode_bf16_map(&smap, x, m, k, kTokens)) return cudaErrorInvalidValue;
-    return launch_wgrad<true, false>(p, smap, zmap, space, num_sms, stream);
-  }
-  while ((1 << p.step_shift) < x_group) ++p.step_shift;
-  p.step_cols = k >> p.step_shift;
-  if (!encode_u8_map(&smap, codes, m, k, kTokens)) return cudaErrorInvalidValue;
-  return launch_wgrad<true, true>(p, smap, zmap, space, num_sms, stream);
-}
-
-cudaError_t launch_db(const uint16_t* dy, const uint16_t* u, const Adapters& ad, const SlotLists& lists, int m, int n,
-                      uint16_t* db, void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
-  WgradParams p{};
-  p.ad = ad;
-  p.lists = lists;
-  p.m = m;
-  p.cols = n;
-  p.width = rank16(ad.rank);
-  p.src = dy;
-  p.z = u;
-  p.z_stride = ad.rank;
-  p.out = db;
-  p.counters = counters;
-  p.status = status;
-  CUtensorMap smap, zmap;
-  if (!encode_bf16_map(&smap, dy, m, n, kTokens) || !encode_bf16_map(&zmap, u, m, ad.rank, kTokens))
-    return cudaErrorInvalidValue;
-  return launch_wgrad<false, false>(p, smap, zmap, space, num_sms, stream);
+  return x.codes != nullptr ? cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<true>, jb, ja)
+                            : cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<false>, jb, ja);
 }
 
 }  // namespace any4

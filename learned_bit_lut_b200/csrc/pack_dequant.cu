@@ -267,6 +267,9 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8
   Planes T[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) T[r] = to_planes(ld_nc_v4(lsec + (g + 8 * r) * 2), ld_nc_v4(lsec + (g + 8 * r) * 2 + 1));
+  // the packed weight is immutable; w is free, and a dependent may launch, from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 2
   for (int c = c0; c < min(c0 + kDqChunks, L.kchunks); ++c) {
     const uint8_t* chunk = packed + L.w_off + ((size_t)P * L.kchunks + c) * L.chunk_bytes;
@@ -364,13 +367,20 @@ cudaError_t launch_pack_fixed(const uint8_t* idx_nib, const uint16_t (&lut)[16],
 }
 
 template <int BITS>
-static void launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream) {
+static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream) {
   const int per_block = kDqWarps * kDqChunks;
-  const dim3 grid((L.kchunks + per_block - 1) / per_block, L.panels);
-  if ((reinterpret_cast<uintptr_t>(w) & 31) == 0)
-    dequant_rows_kernel<BITS, true><<<grid, kDqWarps * 32, 0, stream>>>(packed, L, w);
-  else
-    dequant_rows_kernel<BITS, false><<<grid, kDqWarps * 32, 0, stream>>>(packed, L, w);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((L.kchunks + per_block - 1) / per_block, L.panels);
+  cfg.blockDim = dim3(kDqWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (reinterpret_cast<uintptr_t>(w) & 31) == 0
+             ? cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, true>, packed, L, w)
+             : cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, false>, packed, L, w);
 }
 
 cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w,
@@ -379,14 +389,14 @@ cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w,
   const size_t lanes = (size_t)L.panels * L.kchunks * 32;
   const bool runs = (reinterpret_cast<uintptr_t>(w) & 15) == 0;   // else w is only 4-byte aligned
   if (L.bits == 3) {
-    if (runs) launch_dequant_rows<3>(packed, L, w, stream);
-    else dequant_bits_kernel<3><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
+    if (runs) return launch_dequant_rows<3>(packed, L, w, stream);
+    dequant_bits_kernel<3><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else if (L.bits == 2) {
-    if (runs) launch_dequant_rows<2>(packed, L, w, stream);
-    else dequant_bits_kernel<2><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
+    if (runs) return launch_dequant_rows<2>(packed, L, w, stream);
+    dequant_bits_kernel<2><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else {
-    if (runs) launch_dequant_rows<4>(packed, L, w, stream);
-    else dequant_kernel<<<grid_for((size_t)L.n_pad * L.k / 8, th), th, 0, stream>>>(packed, L, w);
+    if (runs) return launch_dequant_rows<4>(packed, L, w, stream);
+    dequant_kernel<<<grid_for((size_t)L.n_pad * L.k / 8, th), th, 0, stream>>>(packed, L, w);
   }
   return cudaGetLastError();
 }

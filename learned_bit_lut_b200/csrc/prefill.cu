@@ -44,25 +44,29 @@ namespace any4 {
 namespace {
 
 constexpr int kBM = 128;                       // weight rows per tile (MMA M)
-constexpr int kBN = 256;                       // tokens per tile (MMA N)
 constexpr int kBK = 64;                        // K per stage: one 128-byte swizzle row
-constexpr int kStages = 4;
 constexpr int kAStageBytes = kBM * kBK * 2;    // 16 KB
-constexpr int kBStageBytes = kBN * kBK * 2;    // 32 KB
-constexpr int kStageBytes = kAStageBytes + kBStageBytes;
 constexpr int kGemmThreads = 192;
 constexpr int kPatchThreads = 128;             // with adapters: 4 warps more
-constexpr uint32_t kAccCols = kBN;             // fp32 columns per accumulator
-constexpr uint32_t kTmemCols = 2 * kAccCols;   // two accumulators
-constexpr int kGemmSmem = kStages * kStageBytes + 1024 + 1024;   // stages, control, alignment
+
+// BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
+template <int BN>
+struct GemmCfg {
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStageBytes = kAStageBytes + BN * kBK * 2;
+  static constexpr uint32_t kTmem = 2 * BN;                              // two fp32 accumulators
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 1024;      // stages, control, alignment
+};
+constexpr int kBN = 256;
+constexpr int kMaxStages = 6;
 
 struct GemmCtl {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
-  uint64_t raw[kStages];       // TMA bytes of a stage to be patched
-  uint64_t patched[kStages];
+  uint64_t raw[kMaxStages];       // TMA bytes of a stage to be patched
+  uint64_t patched[kMaxStages];
   uint32_t tmem_base;
   int abort_flag;
   int last_split;   // epilogue: this block finishes the tile's split-K sum
@@ -70,7 +74,7 @@ struct GemmCtl {
 };
 
 constexpr int kEpilogueBar = 1;                 // named barrier of the 4 epilogue warps
-constexpr int kPartialFloats = kBM * kBN;       // one split's fp32 tile [token][row]
+constexpr int kPartialFloats = kBM * kBN;       // one split's fp32 tile [token][row] (room for BN = 256)
 constexpr int kMinSplitChunks = 8;              // K per split >= 8 stages (512 columns)
 constexpr int kMaxSplits = 4;                   // the last block reads all splits' partials
 
@@ -162,22 +166,24 @@ __device__ __noinline__ float spoilt_term(const LoraArgs& la, int t, int row, in
 // of `k`: W K-major (N x K), or with TRANS the K axis down W's rows (dx: row =
 // input column, contraction over the N outputs; a last chunk past `k` reads
 // zeros). X: NoLora, or LoraArgs for the adapters' term.
-template <bool TRANS, typename X>
+template <int BN, bool TRANS, typename X>
 __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0), 1)
     prefill_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         uint16_t* __restrict__ y, int m, int n, int k, int splits, float* __restrict__ partials,
                         unsigned* counters, unsigned* status, const __grid_constant__ X lora) {
   constexpr bool LORA = std::is_same<X, LoraArgs>::value;
+  using C = GemmCfg<BN>;
+  constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;   // swizzle atoms need 1024-byte alignment
-  GemmCtl* ctl = reinterpret_cast<GemmCtl*>(smem_raw + (sbase - raw) + kStages * kStageBytes);
-  auto sa = [&](int s) { return sbase + (uint32_t)s * kStageBytes; };
-  auto sb = [&](int s) { return sbase + (uint32_t)s * kStageBytes + kAStageBytes; };
+  GemmCtl* ctl = reinterpret_cast<GemmCtl*>(smem_raw + (sbase - raw) + kStages * C::kStageBytes);
+  auto sa = [&](int s) { return sbase + (uint32_t)s * C::kStageBytes; };
+  auto sb = [&](int s) { return sbase + (uint32_t)s * C::kStageBytes + kAStageBytes; };
   volatile int* abort_flag = &ctl->abort_flag;
 
-  const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + kBN - 1) / kBN;
+  const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + BN - 1) / BN;
   const int tiles = n_tiles * m_tiles, kch = (k + kBK - 1) / kBK;
   const int units = tiles * splits;   // unit u: tile u / splits, K split u % splits
   auto k_range = [&](int u, int& kc0, int& kc1) {
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     kc1 = (int)((long long)(sp + 1) * kch / splits);
   };
 
-  constexpr uint32_t idesc = tc_idesc(kBN, TRANS);
+  constexpr uint32_t idesc = tc_idesc(BN, TRANS);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);    // TMA expect_tx arrival + bytes
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&ctl->tmem_base)),
-                 "r"(kTmemCols)
+                 "r"(C::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -235,14 +241,14 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
               !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status))
             break;
           const uint32_t fb = smem_addr(&ctl->full[s]);
-          mbar_arrive_expect_tx(fb, kStageBytes);
+          mbar_arrive_expect_tx(fb, C::kStageBytes);
           if (TRANS) {
             tma_load_2d(sa(s), &wmap, nt * kBM, kc * kBK, fb);
             tma_load_2d(sa(s) + kAStageBytes / 2, &wmap, nt * kBM + 64, kc * kBK, fb);
           } else {
             tma_load_2d(sa(s), &wmap, kc * kBK, nt * kBM, fb);
           }
-          tma_load_2d(sb(s), &xmap, kc * kBK, mt * kBN, fb);
+          tma_load_2d(sb(s), &xmap, kc * kBK, mt * BN, fb);
         }
         if constexpr (LORA) {
           const SlotHead head = slot_head(lora.lists, mt);
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             // a stage to be patched lands on a barrier of its own: the patching
             // warps see only those stages, so they cannot count the others
             const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
-            mbar_arrive_expect_tx(fb, kStageBytes);
+            mbar_arrive_expect_tx(fb, C::kStageBytes);
             if (mixed) mbar_arrive_one(smem_addr(&ctl->full[s]));
             if (TRANS) {
               tma_load_3d(sa(s), &lora.mmap, nt * kBM, ex.rank0, l, fb);
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             } else {
               tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, fb);
             }
-            tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * kBN, fb);
+            tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * BN, fb);
           }
         }
       }
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
           break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)b * kAccCols;
+        const uint32_t d = tmem + (uint32_t)b * BN;
         int kc0, kc1;
         k_range(u, kc0, kc1);
         for (int kc = kc0; kc < kc1; ++kc, ++it) {
@@ -340,11 +346,12 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         const int per = extra_stages(lora.r16), count = head.count * per;
         const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
         if (mixed) {
-          int id[kBN / kPatchThreads];
+          constexpr int kOwn = (BN + kPatchThreads - 1) / kPatchThreads;   // this thread's token rows
+          int id[kOwn];
 #pragma unroll
-          for (int i = 0; i < kBN / kPatchThreads; ++i) {
-            const int t = mt * kBN + thread + i * kPatchThreads;
-            id[i] = t < m ? adapter_of(lora.ad, t) : -1;
+          for (int i = 0; i < kOwn; ++i) {
+            const int row = thread + i * kPatchThreads, t = mt * BN + row;
+            id[i] = row < BN && t < m ? adapter_of(lora.ad, t) : -1;
           }
           bool ok = true;
           int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             if (patch_tile<TRANS, kPatchThreads>(sa(s), extra_stage(lora.r16, e % per).steps, thread))
               *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
 #pragma unroll
-            for (int i = 0; i < kBN / kPatchThreads; ++i)
-              if (id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
+            for (int i = 0; i < kOwn; ++i)
+              if (thread + i * kPatchThreads < BN && id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
@@ -388,14 +395,14 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       [[maybe_unused]] int spoilt = 0;
       if constexpr (LORA) spoilt = *(volatile int*)&ctl->spoilt[tcount & 3];
       const int r = 32 * q + lane, row = nt * kBM + r;
-      const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * kAccCols;
+      const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * BN;
       float* part = partials + (size_t)u * kPartialFloats;   // [token][row] of this split
 #pragma unroll 1
-      for (int j = 0; j < kBN / 32; ++j) {
+      for (int j = 0; j < BN / 32; ++j) {
         uint32_t v[32];
         tc_ld_x32(tbase + 32u * (uint32_t)j, v);
         tc_wait_ld();
-        const int m0 = mt * kBN + 32 * j;
+        const int m0 = mt * BN + 32 * j;
         if constexpr (LORA)
           if (spoilt && row < n) {
 #pragma unroll
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           if (row < n) {
             // 32 tokens at a time, so 32 loads of each split are in flight together
 #pragma unroll 1
-            for (int j0 = 0; j0 < kBN && mt * kBN + j0 < m; j0 += 32) {
+            for (int j0 = 0; j0 < BN && mt * BN + j0 < m; j0 += 32) {
               float acc[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
               }
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const int mm = mt * kBN + j0 + i;
+                const int mm = mt * BN + j0 + i;
                 if (mm < m) {
                   const __nv_bfloat16 h = __float2bfloat16_rn(acc[i]);
                   y[(size_t)mm * n + row] = *reinterpret_cast<const uint16_t*>(&h);
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   __syncthreads();
   tc_fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem)
                  : "memory");
 }
 
@@ -967,31 +974,32 @@ cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout&
 
 // The GEMM over `rows` output rows and a contraction of `cols`, from W_hat in
 // bf16 (N x K; TRANS: rows = K, cols = N).
-template <bool TRANS, typename X>
+template <int BN, bool TRANS, typename X>
 cudaError_t launch_gemm(const uint16_t* in, const uint16_t* what, const Layout& L, int m, uint16_t* out, int splits,
                         float* partials, unsigned* counters, unsigned* status, int num_sms, const AdapterTerm* term,
                         cudaStream_t stream) {
-  cudaError_t e = allow_smem<prefill_gemm_kernel<TRANS, X>>(kGemmSmem);
+  using C = GemmCfg<BN>;
+  cudaError_t e = allow_smem<prefill_gemm_kernel<BN, TRANS, X>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int rows = TRANS ? L.k : L.n, cols = TRANS ? L.n : L.k;
   CUtensorMap wmap, xmap;
   X lora;
-  if (!encode_bf16_map(&wmap, what, L.n, L.k, TRANS ? kBK : kBM) || !encode_bf16_map(&xmap, in, m, cols, kBN) ||
-      !fill_lora(&lora, term, L, m, kBN, TRANS))
+  if (!encode_bf16_map(&wmap, what, L.n, L.k, TRANS ? kBK : kBM) || !encode_bf16_map(&xmap, in, m, cols, BN) ||
+      !fill_lora(&lora, term, L, m, BN, TRANS))
     return cudaErrorInvalidValue;
-  const int tiles = ((rows + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+  const int tiles = ((rows + kBM - 1) / kBM) * ((m + BN - 1) / BN);
   const int units = tiles * splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units < num_sms ? units : num_sms);
   cfg.blockDim = dim3(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0));
-  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel<TRANS, X>, wmap, xmap, out, m, rows, cols, splits, partials,
+  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel<BN, TRANS, X>, wmap, xmap, out, m, rows, cols, splits, partials,
                             counters, status, lora);
 }
 
@@ -1001,9 +1009,10 @@ size_t prefill_scratch_offset() { return kHeaderBytes; }
 
 bool prefill_fused(const Layout& L, int m) { return fused_path(L, m); }
 
-// K splits of a GEMM with `rows` output rows and a contraction of `cols`.
-static int gemm_splits(int rows, int cols, int m, int num_sms) {
-  const int tiles = ((rows + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+// K splits of a GEMM with `rows` output rows, a contraction of `cols` and bn
+// tokens per tile.
+static int gemm_splits(int rows, int cols, int m, int bn, int num_sms) {
+  const int tiles = ((rows + kBM - 1) / kBM) * ((m + bn - 1) / bn);
   const int kch = cols / kBK;
   int s = tiles < num_sms ? num_sms / tiles : 1;
   const int smax = kch / kMinSplitChunks > 0 ? kch / kMinSplitChunks : 1;
@@ -1012,7 +1021,7 @@ static int gemm_splits(int rows, int cols, int m, int num_sms) {
   return s < 1 ? 1 : s;
 }
 
-int prefill_splits(const Layout& L, int m, int num_sms) { return gemm_splits(L.n, L.k, m, num_sms); }
+int prefill_splits(const Layout& L, int m, int num_sms) { return gemm_splits(L.n, L.k, m, kBN, num_sms); }
 
 size_t prefill_partials_offset(const Layout& L) {
   return kHeaderBytes + align_up((size_t)L.n * L.k * 2, kAlign);
@@ -1044,7 +1053,7 @@ static cudaError_t launch_prefill_any(const uint16_t* x, const uint8_t* packed, 
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + prefill_scratch_offset());
   const cudaError_t e = launch_dequant(packed, L, what, stream);   // bf16 W_hat, N x K
   if (e != cudaSuccess) return e;
-  return launch_gemm<false, X>(x, what, L, m, y, prefill_splits(L, m, num_sms),
+  return launch_gemm<kBN, false, X>(x, what, L, m, y, prefill_splits(L, m, num_sms),
                                reinterpret_cast<float*>(ws + prefill_partials_offset(L)), reinterpret_cast<unsigned*>(ws),
                                reinterpret_cast<unsigned*>(ws + kCountersBytes), num_sms, term, stream);
 }
@@ -1059,16 +1068,25 @@ cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const 
   return launch_prefill_any<LoraArgs>(x, packed, L, m, y, workspace, num_sms, &term, stream);
 }
 
+// dx takes the fused path's token tiles: 64 or 128 for few tokens (B200,
+// 4096 x 4096, M = 64: DXB us against DXA us in a 256-token tile).
 size_t dx_partials_bytes(const Layout& L, int m, int num_sms) {
-  const int splits = gemm_splits(L.k, L.n, m, num_sms);
-  const int tiles = ((L.k + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, num_sms);
+  const int tiles = ((L.k + kBM - 1) / kBM) * ((m + bn - 1) / bn);
   return splits > 1 ? align_up((size_t)tiles * splits * kPartialFloats * sizeof(float), kAlign) : 0;
 }
 
 cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
                       unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream) {
-  return launch_gemm<true, LoraArgs>(dy, what, L, m, dx, gemm_splits(L.k, L.n, m, num_sms), partials, counters, status,
-                                     num_sms, &term, stream);
+  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, num_sms);
+  switch (bn) {
+    case 64:
+      return launch_gemm<64, true, LoraArgs>(dy, what, L, m, dx, splits, partials, counters, status, num_sms, &term, stream);
+    case 128:
+      return launch_gemm<128, true, LoraArgs>(dy, what, L, m, dx, splits, partials, counters, status, num_sms, &term, stream);
+    default:
+      return launch_gemm<256, true, LoraArgs>(dy, what, L, m, dx, splits, partials, counters, status, num_sms, &term, stream);
+  }
 }
 
 }  // namespace any4
