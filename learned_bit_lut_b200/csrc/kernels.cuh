@@ -85,10 +85,7 @@ cudaError_t launch_linear_small(const uint16_t* x, const uint8_t* packed, const 
                                 void* workspace, int cluster, cudaStream_t stream, const float* delta);
 
 // delta (M <= 16): an fp32 [M][N] term added to each sum before its one
-// rounding to bf16, or null. The kernel launched just before on the stream
-// writes it, as a programmatic dependent that waits for its predecessors
-// before it lets its own dependent launch: so x and the workspace are ready
-// when this grid runs, and it waits for that kernel only before its stores.
+// rounding to bf16, or null.
 cudaError_t launch_linear(const uint16_t* x, const uint8_t* packed, const Layout& L, int m,
                           uint16_t* y, void* workspace, const LinearPlan& plan,
                           cudaStream_t stream, const float* delta = nullptr);

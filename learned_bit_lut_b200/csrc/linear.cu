@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
   // work on the panel, adds them after its own sum in thread-block order
   // (deterministic) and resets the counter for the next call.
   if (warp == NW + 1) {
-    if (p.delta == nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");   // y, partials, counters
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // y, partials, counters
     for (int P = P0; P <= P1; ++P) {
       const int b = (P - P0) & 1;
       const bool split = is_split(P);
@@ -517,8 +517,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
             }
           }
         }
-        if (p.delta != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll
+      #pragma unroll
         for (int i = 0; i < NF; ++i) store_out<MODE>(p, P, lane * NF + i, v[i] + other[i]);
         if (split && !clustered && lane == 0) p.counters[P] = 0u;   // ready for the next call
       } else if (clustered) {   // send this block's partial to rank 0
@@ -692,10 +691,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
       if (P + 1 < P1) load_lut(P + 2, nw, nh);
     }
     if (P == P0) {
-      // activations, y and the workspace are touched only from here on (with
-      // delta its kernel came between: it was launched, and let this grid
-      // launch, after x was complete, so only the reducer waits, for delta)
-      if (p.delta == nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+      // activations, y and the workspace are touched only from here on
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       next_operands();
     }
     consumer_sync(NCT);   // tables ready

@@ -112,9 +112,7 @@ __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(
 
   // ---- activations: lane (g, t) feeds token g (+8 for the second tile) with
   // columns 16t .. 16t+15 of each chunk; tokens >= M are zero
-  // (with delta, its kernel let this grid launch after x was complete, and
-  // the wait is for delta, before the stores)
-  if (p.delta == nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool tok0 = g < p.m, tok1 = NT8 > 1 && g + 8 < p.m;
   const uint16_t* x0 = p.x + (size_t)(tok0 ? g : 0) * p.k + 16 * t;
   const uint16_t* x1 = p.x + (size_t)(tok1 ? g + 8 : 0) * p.k + 16 * t;
@@ -231,7 +229,6 @@ __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(
           v[u][h][0] += q.x; v[u][h][1] += q.y; v[u][h][2] += q.z; v[u][h][3] += q.w;
         }
   }
-  if (p.delta != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
   // D fragment: (row g, tokens 2t, 2t+1), (row g+8, tokens 2t, 2t+1) per tile
 #pragma unroll
   for (int u = 0; u < 2; ++u)

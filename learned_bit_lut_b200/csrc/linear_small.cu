@@ -142,10 +142,8 @@ __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kern
   __syncthreads();
   if (csz > 1) cluster_sync_init();   // rank 0's receive barrier is armed before any rank sends
 
-  // ---- activations and scales (after the grid-dependency wait; with delta,
-  // its kernel let this grid launch after x was complete, and the wait is for
-  // delta, before the stores)
-  if (p.delta == nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- activations and scales (after the grid-dependency wait)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t baseA = tab | ((uint32_t)g << 4) | ((uint32_t)t << 2);   // pairs (g, g+16)
   const uint32_t baseB = baseA | 128u;                                         // pairs (g+8, g+24)
   const uint16_t* xrow[NX];
@@ -287,7 +285,6 @@ __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kern
         v[4 * i + 3] += __uint_as_float(q.w);
       }
   }
-  if (p.delta != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
   // result i of this lane: (token, row) as in linear.cu
 #pragma unroll
   for (int i = 0; i < NF; ++i) {

@@ -8,11 +8,12 @@
 // M <= 16 (decode): one small kernel writes the fp32 term u . B^T, which the
 // any4 decode kernel adds to its own fp32 sums before their one rounding. The
 // adapters' bytes are few beside the weight's, so it is bound by latency: a
-// cluster of 8 thread blocks takes a token (or 4096 of its output rows), its
+// cluster of 8 thread blocks takes a token and a slice of its output rows, its
 // blocks share the R rows of A_l, exchange the sums through distributed
 // shared memory and share the output rows. The decode kernel is its
-// programmatic dependent, launched once x is complete, and runs beside it: it
-// waits for the term only before its stores.
+// programmatic dependent, but one of its blocks fills an SM, so it follows
+// rather than overlaps (waiting for the term only before its stores measured
+// the same).
 //
 // M > 16: the lists of the adapters in each token tile and u = s x . A^T on
 // the tensor cores (lora_down.cu), then the prefill GEMM with u . B^T as R
@@ -31,10 +32,9 @@ namespace any4 {
 
 namespace {
 
-constexpr int kDeltaThreads = 256;
+constexpr int kDeltaThreads = 512;
 constexpr int kDeltaWarps = kDeltaThreads / 32;
 constexpr int kDeltaCluster = 8;                                // ranks are multiples of 8: R / 8 rows of A per block
-constexpr int kDeltaRows = 2 * kDeltaCluster * kDeltaThreads;   // output rows per cluster
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
   const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
@@ -53,8 +53,10 @@ __device__ __forceinline__ uint16_t bf16_of(float v) {
 
 // Cluster (token t, slice of the output rows). Phase 1: the cluster's block
 // `rank` sums u[r] = s_l sum_k x[t][k] A_l[r][k] for r = rank, rank + 8, ...:
-// each warp an eighth of K for all of them, then the warps in order. Phase 2:
-// delta[t][n] = sum_r u[r] B_l[n][r], a thread per output row.
+// each warp its share of K for all of them, then the warps in order. Phase 2:
+// delta[t][n] = sum_r u[r] B_l[n][r], R / 8 lanes per output row, 16 bytes
+// each: a warp reads consecutive rows whole (a thread per row took 3 times as
+// long over a kernel's 4 KB strides of 16-byte pieces).
 __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint16_t* __restrict__ x, const Adapters ad,
                                                                       int n, int k, float* __restrict__ delta,
                                                                       uint16_t* __restrict__ u) {
@@ -62,26 +64,26 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
   __shared__ __align__(16) float us[kMaxRank];
   const int rank = blockIdx.x, t = blockIdx.y, slice = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // x is complete past the wait; only then may the dependent launch
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int l = adapter_of(ad, t);
   const int rows = ad.rank / kDeltaCluster;
-  const int row0 = slice * kDeltaRows + rank * kDeltaThreads + threadIdx.x;   // and kDeltaCluster * kDeltaThreads on
+  // phase 2: the slice's warps take `per_warp` consecutive output rows in turn
+  const int parts = ad.rank / 8, per_warp = 32 / parts, part_of = lane % parts;
+  const int warps = (int)gridDim.z * kDeltaCluster * kDeltaWarps;
+  const int first = ((slice * kDeltaCluster + rank) * kDeltaWarps + warp) * per_warp + lane / parts;
+  const bool works = lane < per_warp * parts;
+  const uint16_t* brow = ad.b + ((size_t)(l < 0 ? 0 : l) * n + first) * ad.rank + 8 * part_of;
+  const size_t b_step = (size_t)warps * per_warp * ad.rank;
   if (l >= 0) {
-    // phase 2's rows of B towards L2 while phase 1 runs
-    for (int row = row0; row < n && row < row0 + 2 * kDeltaCluster * kDeltaThreads; row += kDeltaCluster * kDeltaThreads) {
-      const uint16_t* br = ad.b + ((size_t)l * n + row) * ad.rank;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(br));
-      if (ad.rank > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(br + 64));
-    }
+    // its first rows of B towards L2 while phase 1 runs
+    if (works && first < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(brow));
     const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * k);
     const uint4* ar = reinterpret_cast<const uint4*>(ad.a + ((size_t)l * ad.rank + rank) * k);
     const size_t row_step = (size_t)kDeltaCluster * (k / 8);
-    const int c0 = warp * (k / 64), c1 = c0 + k / 64;   // this warp's 16-byte pieces of a row
     for (int i0 = 0; i0 < rows; i0 += 8) {   // 8 rows' loads in flight
       float acc[8] = {};
-      for (int c = c0 + lane; c < c1; c += 32) {
+      for (int c = threadIdx.x; c < k / 8; c += kDeltaThreads) {   // 16-byte pieces of a row
         const uint4 xv = __ldg(xr + c);
         uint4 av[8];
 #pragma unroll
@@ -115,42 +117,46 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
     if (u != nullptr && peer == 0 && slice == 0) u[(size_t)t * ad.rank + r] = bf16_of(v);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  float uv[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = row0 + h * kDeltaCluster * kDeltaThreads;
-    if (row >= n) break;
-    float acc = 0.0f;
-    if (l >= 0) {
-      const uint4* br = reinterpret_cast<const uint4*>(ad.b + ((size_t)l * n + row) * ad.rank);
-      for (int c0 = 0; c0 < ad.rank / 8; c0 += 8) {   // 64 ranks' loads in flight
-        uint4 q[8];
+  for (int i = 0; i < 8; ++i) uv[i] = us[8 * part_of + i];
+  float* out = delta + (size_t)t * n;
+  for (int row = first; row - lane / parts < n; row += 4 * warps * per_warp, brow += 4 * b_step) {
+    uint4 q[4];   // four steps' loads in flight
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c0 + i < ad.rank / 8) q[i] = __ldcg(br + c0 + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (c0 + i >= ad.rank / 8) break;
-          const float4* uv = reinterpret_cast<const float4*>(us + 8 * (c0 + i));
-          const float4 u0 = uv[0], u1 = uv[1];
-          acc = fmaf(u0.x, bf16_bits_to_float(q[i].x & 0xFFFFu), acc);
-          acc = fmaf(u0.y, __uint_as_float(q[i].x & 0xFFFF0000u), acc);
-          acc = fmaf(u0.z, bf16_bits_to_float(q[i].y & 0xFFFFu), acc);
-          acc = fmaf(u0.w, __uint_as_float(q[i].y & 0xFFFF0000u), acc);
-          acc = fmaf(u1.x, bf16_bits_to_float(q[i].z & 0xFFFFu), acc);
-          acc = fmaf(u1.y, __uint_as_float(q[i].z & 0xFFFF0000u), acc);
-          acc = fmaf(u1.z, bf16_bits_to_float(q[i].w & 0xFFFFu), acc);
-          acc = fmaf(u1.w, __uint_as_float(q[i].w & 0xFFFF0000u), acc);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (l >= 0 && works && row + i * warps * per_warp < n) q[i] = __ldcg(reinterpret_cast<const uint4*>(brow + i * b_step));
     }
-    delta[(size_t)t * n + row] = acc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      float acc = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc = fmaf(uv[2 * j], bf16_bits_to_float(w[j] & 0xFFFFu), acc);
+        acc = fmaf(uv[2 * j + 1], __uint_as_float(w[j] & 0xFFFF0000u), acc);
+      }
+      if (l < 0) acc = 0.0f;
+      for (int d = 1; d < parts; d <<= 1) {   // the sum over a row's lanes arrives at its first
+        const float v = __shfl_down_sync(0xFFFFFFFFu, acc, d);
+        if (part_of + d < parts) acc += v;
+      }
+      const int at = row + i * warps * per_warp;
+      if (works && part_of == 0 && at < n) out[at] = acc;
+    }
   }
 }
 
 cudaError_t launch_delta(const uint16_t* x, const Adapters& ad, int m, int n, int k, float* delta, uint16_t* u,
-                         cudaStream_t stream) {
+                         int num_sms, cudaStream_t stream) {
+  // slices: a thread block per SM over all tokens (each slice sums u anew),
+  // with four steps of rows for every warp
+  const int per_pass = kDeltaCluster * kDeltaWarps * (32 / (ad.rank / 8)) * 4, most = (n + per_pass - 1) / per_pass;
+  int slices = num_sms / (kDeltaCluster * m);
+  slices = slices < 1 ? 1 : slices > most ? most : slices;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kDeltaCluster, (unsigned)m, (unsigned)((n + kDeltaRows - 1) / kDeltaRows));
+  cfg.gridDim = dim3(kDeltaCluster, (unsigned)m, (unsigned)slices);
   cfg.blockDim = dim3(kDeltaThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -238,7 +244,7 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
   const cudaStream_t st = (cudaStream_t)stream;
   if (plan.mode != 3) {
     float* delta = reinterpret_cast<float*>(ws + space.delta);
-    e = launch_delta(x, ad, m, n, k, delta, u, st);
+    e = launch_delta(x, ad, m, n, k, delta, u, sms, st);
     if (e == cudaSuccess) e = launch_linear(x, w, L, m, y, workspace, plan, st, delta);
   } else {
     AdapterTerm term{};
