@@ -15,11 +15,15 @@
 // group of zeros has step 0; a group that holds an infinity or a NaN has step
 // NaN and reads back as NaN, so neither is lost in the codes.
 //
-// The pack moves 3 bytes and the unpack 3 bytes per value and both are bound
-// by HBM. Groups divide the rows, so the tensor is one flat run of groups: a
-// thread takes 16 consecutive values (two 16-byte loads, one 16-byte store of
-// codes), G/16 neighbouring lanes share a group and its maximum by shuffles
-// (G = 1024: 64 threads' worth, as two runs of 16 per lane).
+// Both move 3 bytes per value and are bound by HBM, which writes at about half
+// the rate it reads: unpacking 8192 x 14336 (235 MB written) takes 54 us on
+// B200, packing it (235 MB read) 57 us, where a plain copy of as many bytes
+// takes 56 us; the pack's instructions per value come next, so a lane packs 16
+// values and the group's arithmetic is one multiply and one reciprocal.
+// Groups divide the rows, so the tensor is one flat run of groups. Loads and
+// stores of a warp are whole lines: 32 bytes of x and 16 of codes a lane (8
+// and 16 when unpacking); up to 32 neighbouring lanes share a group and its
+// maximum by shuffles (G = 1024: two runs per lane).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -33,6 +37,8 @@ namespace any4 {
 namespace {
 
 constexpr int kActThreads = 256;
+constexpr int kActItems = 2;                         // runs per thread ...
+constexpr size_t kActManyRuns = (size_t)1 << 18;     // ... from 2^22 values on: blocks for every SM
 
 // 2^-120: below this step, 1 / step leaves the range where x * (1 / step) is
 // good to 2^-22, so the codes are divided out.
@@ -45,12 +51,11 @@ __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 // x / step as x * inv is off by at most 2^-22 of itself, which could move an
 // exact half. A quotient of two 8-bit significands that is not a half itself
 // is at least 1/1020 away from one, so snapping the product to multiples of
-// 2^-11 (by adding and taking off 1.5 * 2^12) restores exact halves and
-// crosses none; the second addition rounds half to even and leaves the code
-// in the low byte.
+// 2^-11 (adding 1.5 * 2^12) restores exact halves and crosses none; the second
+// addition takes that off and adds 1.5 * 2^23, which rounds half to even and
+// leaves the code in the low byte.
 __device__ __forceinline__ uint32_t code_byte(float v, float inv) {
-  const float snapped = __fadd_rn(__fmaf_rn(v, inv, 6144.0f), -6144.0f);
-  return __float_as_uint(__fadd_rn(snapped, 12582912.0f));
+  return __float_as_uint(__fadd_rn(__fmaf_rn(v, inv, 6144.0f), 12582912.0f - 6144.0f));
 }
 __device__ __forceinline__ uint32_t codes4(uint32_t p0, uint32_t p1, float inv) {
   const uint32_t a = code_byte(bf16_bits_to_float(p0 & 0xFFFFu), inv), b = code_byte(__uint_as_float(p0 & 0xFFFF0000u), inv);
@@ -67,76 +72,104 @@ __device__ __forceinline__ uint32_t codes4_divide(uint32_t p0, uint32_t p1, floa
 
 __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t p) { return __vmaxu2(m, p & 0x7FFF7FFFu); }
 
-// RUNS runs of 16 values per thread of one group (1, or 2 for G = 1024);
-// 2^lanes_shift = threads of a group, within one warp.
-template <int RUNS>
+// A thread packs ITEMS runs of 16 values, kActThreads apart but for the RUNS of
+// them that belong to one group; all their loads are in flight together.
+// 2^lanes_shift threads share a group, within one warp. WIDE: x is 32-byte
+// aligned.
+template <int RUNS, int ITEMS, bool WIDE>
 __global__ void __launch_bounds__(kActThreads) act_pack_kernel(const uint16_t* __restrict__ x, size_t runs,
                                                                int lanes_shift, uint8_t* __restrict__ codes,
                                                                uint16_t* __restrict__ steps) {
+  constexpr int GROUPS = ITEMS / RUNS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const size_t thread = (size_t)blockIdx.x * kActThreads + threadIdx.x;
-  const int lanes = 1 << lanes_shift;
-  const size_t group = thread >> lanes_shift;   // lanes divides 32: a group never leaves its warp
-  const int in_group = (int)(thread & (unsigned)(lanes - 1));
-  uint4 v[RUNS][2];
-  bool live[RUNS];
-  size_t at[RUNS];
-  uint32_t top2 = 0;
+  const int lanes = 1 << lanes_shift, in_group = threadIdx.x & (lanes - 1);
+  size_t group[GROUPS], at[GROUPS][RUNS];
+  uint4 v[GROUPS][RUNS][2];
 #pragma unroll
-  for (int i = 0; i < RUNS; ++i) {
-    at[i] = group * (size_t)(lanes * RUNS) + (size_t)(i * lanes + in_group);
-    live[i] = at[i] < runs;
-    v[i][0] = live[i] ? ld_stream_v4(x + at[i] * 16) : zero4();
-    v[i][1] = live[i] ? ld_stream_v4(x + at[i] * 16 + 8) : zero4();
-  }
+  for (int g = 0; g < GROUPS; ++g) {
+    // lanes divides 32, so a group never leaves its warp
+    group[g] = (((size_t)blockIdx.x * GROUPS + g) * kActThreads + threadIdx.x) >> lanes_shift;
 #pragma unroll
-  for (int i = 0; i < RUNS; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, v[i][h].x), v[i][h].y), v[i][h].z), v[i][h].w);
-  uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);   // bf16 magnitudes order like integers, NaN above infinity
-  for (int d = lanes >> 1; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  const bool finite = top < 0x7F80u;
-  uint32_t step_bits = 0x7FC0u;
-  if (finite) step_bits = (__float_as_uint(__fdiv_rn(bf16_bits_to_float(top), 127.0f)) + 0xFFFFu) >> 16;
-  const float step = bf16_bits_to_float(step_bits);
-  const bool tiny = finite && step < kTinyStep && step > 0.0f;
-  const float inv = finite && step >= kTinyStep ? __fdiv_rn(1.0f, step) : 0.0f;
-#pragma unroll
-  for (int i = 0; i < RUNS; ++i) {
-    if (!live[i]) continue;
-    uint4 c = zero4();
-    if (tiny) {
-      c = make_uint4(codes4_divide(v[i][0].x, v[i][0].y, step), codes4_divide(v[i][0].z, v[i][0].w, step),
-                     codes4_divide(v[i][1].x, v[i][1].y, step), codes4_divide(v[i][1].z, v[i][1].w, step));
-    } else if (finite) {
-      c = make_uint4(codes4(v[i][0].x, v[i][0].y, inv), codes4(v[i][0].z, v[i][0].w, inv),
-                     codes4(v[i][1].x, v[i][1].y, inv), codes4(v[i][1].z, v[i][1].w, inv));
+    for (int i = 0; i < RUNS; ++i) {
+      at[g][i] = group[g] * (size_t)(lanes * RUNS) + (size_t)(i * lanes + in_group);
+      v[g][i][0] = v[g][i][1] = zero4();
+      if (at[g][i] < runs) {
+        const uint16_t* src = x + at[g][i] * 16;
+        if (WIDE) {
+          ld_nc_v8(src, v[g][i][0], v[g][i][1]);
+        } else {
+          v[g][i][0] = ld_nc_v4(src);
+          v[g][i][1] = ld_nc_v4(src + 8);
+        }
+      }
     }
-    *reinterpret_cast<uint4*>(codes + at[i] * 16) = c;
   }
-  if (in_group == 0 && live[0]) steps[group] = (uint16_t)step_bits;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, v[g][i][h].x), v[g][i][h].y), v[g][i][h].z), v[g][i][h].w);
+    uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);   // bf16 magnitudes order like integers, NaN above infinity
+    for (int d = lanes >> 1; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    // top / 127 as a product is off by less than 2^-22 of itself; the quotient
+    // of an 8-bit significand by 127 is a bf16 number or at least 2^-16 away
+    // from one, so rounding up gives the same (127 itself: 1 or just below)
+    const bool finite = top < 0x7F80u;
+    uint32_t step_bits = 0x7FC0u;
+    if (finite) step_bits = (__float_as_uint(__fmul_rn(bf16_bits_to_float(top), 1.0f / 127.0f)) + 0xFFFFu) >> 16;
+    const float step = bf16_bits_to_float(step_bits);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));   // off by a step of fp32
+    const bool tiny = step < kTinyStep;
+    if (!finite || tiny) inv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+      const uint4 lo = v[g][i][0], hi = v[g][i][1];
+      uint4 c = make_uint4(codes4(lo.x, lo.y, inv), codes4(lo.z, lo.w, inv), codes4(hi.x, hi.y, inv),
+                           codes4(hi.z, hi.w, inv));
+      if (!finite) c = zero4();
+      if (tiny && step > 0.0f)   // also false for NaN
+        c = make_uint4(codes4_divide(lo.x, lo.y, step), codes4_divide(lo.z, lo.w, step), codes4_divide(hi.x, hi.y, step),
+                       codes4_divide(hi.z, hi.w, step));
+      if (at[g][i] < runs) *reinterpret_cast<uint4*>(codes + at[g][i] * 16) = c;
+    }
+    if (in_group == 0 && at[g][0] < runs) steps[group[g]] = (uint16_t)step_bits;
+  }
 }
 
+// Unpacks ITEMS pieces of 8 values per thread.
+template <int ITEMS>
 __global__ void __launch_bounds__(kActThreads) act_unpack_kernel(const uint8_t* __restrict__ codes,
-                                                                 const uint16_t* __restrict__ steps, size_t runs,
-                                                                 int runs_shift, uint16_t* __restrict__ x) {
+                                                                 const uint16_t* __restrict__ steps, size_t pieces,
+                                                                 int pieces_shift, uint16_t* __restrict__ x) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const size_t run = (size_t)blockIdx.x * kActThreads + threadIdx.x;
-  if (run >= runs) return;
-  const uint4 c = ld_stream_v4(codes + run * 16);
-  const uint32_t s = ld_nc_u16(steps + (run >> runs_shift));
-  const uint32_t step2 = s | (s << 16);
-  uint4 lo, hi;
-  act8_values4(c.x, step2, lo.x, lo.y);
-  act8_values4(c.y, step2, lo.z, lo.w);
-  act8_values4(c.z, step2, hi.x, hi.y);
-  act8_values4(c.w, step2, hi.z, hi.w);
-  uint4* out = reinterpret_cast<uint4*>(x + run * 16);
-  out[0] = lo;
-  out[1] = hi;
+  uint2 c[ITEMS];
+  uint32_t s[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const size_t at = ((size_t)blockIdx.x * ITEMS + i) * kActThreads + threadIdx.x;
+    c[i] = make_uint2(0u, 0u);
+    s[i] = 0;
+    if (at < pieces) {
+      c[i] = __ldcs(reinterpret_cast<const uint2*>(codes) + at);
+      s[i] = ld_nc_u16(steps + (at >> pieces_shift));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const size_t at = ((size_t)blockIdx.x * ITEMS + i) * kActThreads + threadIdx.x;
+    if (at >= pieces) break;
+    const uint32_t step2 = s[i] | (s[i] << 16);
+    uint4 v;
+    act8_values4(c[i].x, step2, v.x, v.y);
+    act8_values4(c[i].y, step2, v.z, v.w);
+    reinterpret_cast<uint4*>(x)[at] = v;
+  }
 }
 
 // As a programmatic dependent: the launch overlaps the previous kernel's end.
@@ -154,6 +187,18 @@ cudaError_t launch_act(void (*kernel)(P...), unsigned blocks, cudaStream_t strea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <bool WIDE>
+cudaError_t launch_act_pack(const uint16_t* x, size_t runs, int group, uint8_t* codes, uint16_t* steps, cudaStream_t stream) {
+  const int per = group / 16 > 32 ? 2 : 1;   // runs of a group per lane
+  int shift = 0;
+  while ((16 * per << shift) < group) ++shift;
+  const bool many = runs >= kActManyRuns;
+  const size_t block = (size_t)(per == 2 || many ? 2 : 1) * kActThreads;
+  static_assert(kActItems == 2, "a group of two runs, or two groups");
+  return launch_act(per == 2 ? act_pack_kernel<2, 2, WIDE> : many ? act_pack_kernel<1, 2, WIDE> : act_pack_kernel<1, 1, WIDE>,
+                    (unsigned)((runs + block - 1) / block), stream, x, runs, shift, codes, steps);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
@@ -167,14 +212,12 @@ ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* c
   if (!x || !codes || !steps) return ANY4_EINVAL;
   if (!any4::act_shape_ok(m, k, group)) return ANY4_ESHAPE;
   if (!any4::aligned16(x) || !any4::aligned16(codes) || (reinterpret_cast<uintptr_t>(steps) & 1)) return ANY4_EALIGN;
+  using namespace any4;
   const size_t runs = (size_t)m * k / 16;
-  const int per = group / 16 > 32 ? 2 : 1;
-  int shift = 0;
-  while ((16 * per << shift) < group) ++shift;
-  const unsigned blocks = (unsigned)((runs / per + any4::kActThreads - 1) / any4::kActThreads);
   uint8_t* c = reinterpret_cast<uint8_t*>(codes);
-  const cudaError_t e = any4::launch_act(per == 2 ? any4::act_pack_kernel<2> : any4::act_pack_kernel<1>, blocks,
-                                         (cudaStream_t)stream, x, runs, shift, c, steps);
+  const cudaError_t e = (reinterpret_cast<uintptr_t>(x) & 31) == 0
+                            ? launch_act_pack<true>(x, runs, group, c, steps, (cudaStream_t)stream)
+                            : launch_act_pack<false>(x, runs, group, c, steps, (cudaStream_t)stream);
   return e == cudaSuccess ? ANY4_OK : any4::record_cuda_error(e);
 }
 
@@ -183,12 +226,15 @@ ANY4_API int any4_act_unpack(const int8_t* codes, const uint16_t* steps, int m, 
   if (!x || !codes || !steps) return ANY4_EINVAL;
   if (!any4::act_shape_ok(m, k, group)) return ANY4_ESHAPE;
   if (!any4::aligned16(x) || !any4::aligned16(codes) || (reinterpret_cast<uintptr_t>(steps) & 1)) return ANY4_EALIGN;
-  const size_t runs = (size_t)m * k / 16;
+  using namespace any4;
+  const size_t pieces = (size_t)m * k / 8;
   int shift = 0;
-  while ((16 << shift) < group) ++shift;
-  const unsigned blocks = (unsigned)((runs + any4::kActThreads - 1) / any4::kActThreads);
-  const cudaError_t e = any4::launch_act(any4::act_unpack_kernel, blocks, (cudaStream_t)stream,
-                                         reinterpret_cast<const uint8_t*>(codes), steps, runs, shift, x);
+  while ((8 << shift) < group) ++shift;
+  const bool many = pieces >= 2 * kActManyRuns;
+  const size_t block = (size_t)(many ? kActItems : 1) * kActThreads;
+  const cudaError_t e = launch_act(many ? act_unpack_kernel<kActItems> : act_unpack_kernel<1>,
+                                   (unsigned)((pieces + block - 1) / block), (cudaStream_t)stream,
+                                   reinterpret_cast<const uint8_t*>(codes), steps, pieces, shift, x);
   return e == cudaSuccess ? ANY4_OK : any4::record_cuda_error(e);
 }
 

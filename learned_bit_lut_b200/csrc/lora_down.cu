@@ -134,7 +134,8 @@ static_assert(sizeof(DownCtl) <= 1024, "control block");
 struct DownParams {
   Adapters ad;
   SlotLists lists;
-  int m, steps, splits;        // a step is `chunks` chunks of the contraction
+  int m, steps, splits;        // a step is `chunks` chunks of the contraction; a split takes every splits-th, so that
+                               // the splits of a tile read neighbouring columns at a time (whole DRAM pages)
   int groups, per_group;       // adapter groups of a tile, adapters per group
   int chunks, stages;          // chunks per stage, stages
   int r16;                     // R rounded up to 16
@@ -192,8 +193,6 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   volatile int* abort_flag = &ctl->abort_flag;
   const int split = blockIdx.x % p.splits, tg = blockIdx.x / p.splits;
   const int group = tg % p.groups, tile = tg / p.groups;
-  const int k0 = (int)((long long)split * p.steps / p.splits);
-  const int k1 = (int)((long long)(split + 1) * p.steps / p.splits);
   const int r16 = p.r16;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
-      for (int k = k0; k < k1 && count > 0; ++k) {
+      for (int k = split; k < p.steps && count > 0; k += p.splits) {
         if (r.wrapped && !gemm_wait(smem_addr(&ctl->empty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
         const uint32_t fb = smem_addr(&ctl->full[r.s]), dst = sbase + (uint32_t)r.s * stage_bytes;
         mbar_arrive_expect_tx(fb, x_bytes);
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   } else if (warp == 6) {
     if (lane == 0) {
       Ring r;
-      for (int k = k0; k < k1 && count > 0; ++k) {
+      for (int k = split; k < p.steps && count > 0; k += p.splits) {
         if (r.wrapped && !gemm_wait(smem_addr(&ctl->empty[r.s]), r.parity ^ 1u, abort_flag, p.status)) break;
         const uint32_t fb = smem_addr(&ctl->full[r.s]);
         uint32_t dst = sbase + (uint32_t)r.s * stage_bytes + x_bytes;
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
     if (lane == 0) {
       Ring r;
       const uint32_t idesc = tc_idesc(count * p.cols, false, BACK);
-      for (int k = k0; k < k1 && count > 0; ++k) {
+      for (int k = split; k < p.steps && count > 0; k += p.splits) {
         if (!gemm_wait(smem_addr(&ctl->full[r.s]), r.parity, abort_flag, p.status)) break;
         tc_fence_after();
         uint32_t xa = sbase + (uint32_t)r.s * stage_bytes, ma = xa + x_bytes;
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
 #pragma unroll
           for (int kk = 0; kk < kChunk / 16; ++kk)
             tc_mma(tmem, ad + 2u * (uint64_t)kk, bd + (BACK ? 128u : 2u) * (uint64_t)kk, idesc,
-                   k > k0 || c > 0 || kk > 0 ? 1u : 0u);
+                   k > split || c > 0 || kk > 0 ? 1u : 0u);
         }
         tc_commit(smem_addr(&ctl->empty[r.s]));
         r.next(p.stages);

@@ -575,11 +575,13 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-// How m tokens, src columns and adapters with z columns `width` wide are cut up.
+// How m tokens, src columns and adapters with z columns `width` wide are cut
+// up. dA and dB share a launch and are cut into as many shares, whichever of
+// them is asked for, so that a sum does not depend on it.
 struct WgradPlan {
   int tiles, chunks, splits, passes, group_cols, per_pass;
 };
-WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
+WgradPlan wgrad_cut(int m, int cols, int adapters, int width) {
   WgradPlan w;
   w.tiles = (cols + kCols - 1) / kCols;
   w.chunks = (m + kTokens - 1) / kTokens;
@@ -587,20 +589,27 @@ WgradPlan wgrad_plan(int m, int cols, int adapters, int width, int num_sms) {
   w.per_pass = kMaxZCols / w.group_cols;
   if (w.per_pass > adapters) w.per_pass = adapters;
   w.passes = (adapters + w.per_pass - 1) / w.per_pass;
-  // shares of the chunks: two blocks per SM, two chunks each at least, and no
-  // more than the last block can add up quickly
-  const int units = w.tiles * w.passes;
-  int s = units < 2 * num_sms ? 2 * num_sms / units : 1;
-  if (s > w.chunks / 2) s = w.chunks / 2;
+  w.splits = 1;
+  return w;
+}
+struct WgradPlans {
+  WgradPlan da, db;
+};
+WgradPlans wgrad_plans(int m, int n, int k, int adapters, int rank, int num_sms) {
+  WgradPlans w = {wgrad_cut(m, k, adapters, 2 * rank16(rank)), wgrad_cut(m, n, adapters, rank16(rank))};
+  // shares of the chunks: two blocks per SM over both sums, two chunks each at
+  // least, and no more than the last block can add up quickly
+  const long long units = (long long)w.da.tiles * w.da.passes + (long long)w.db.tiles * w.db.passes;
+  long long s = 2 * num_sms / units;
+  if (s > w.da.chunks / 2) s = w.da.chunks / 2;
   if (s > kMaxSplits) s = kMaxSplits;
-  w.splits = s < 1 ? 1 : s;
+  w.da.splits = w.db.splits = s < 1 ? 1 : (int)s;
   return w;
 }
 
 // Fills in a job's plan; the shared memory its blocks need.
-size_t plan_job(WgradJob* job, void* space, int num_sms) {
+size_t plan_job(WgradJob* job, const WgradPlan& w, void* space) {
   WgradParams& p = job->p;
-  const WgradPlan w = wgrad_plan(p.m, p.cols, p.ad.count, p.width, num_sms);
   p.chunks = w.chunks;
   p.splits = w.splits;
   p.passes = w.passes;
@@ -627,8 +636,7 @@ size_t plan_job(WgradJob* job, void* space, int num_sms) {
   return (size_t)WgradCfg<false>::kSrcBytes + (size_t)p.z_stages * p.z_stage + info_bytes + kWgradFixed;
 }
 
-size_t job_bytes(int m, int cols, int adapters, int rank, int width, int num_sms) {
-  const WgradPlan w = wgrad_plan(m, cols, adapters, width, num_sms);
+size_t job_bytes(const WgradPlan& w, int rank) {
   if (w.splits == 1) return 0;
   const size_t units = (size_t)w.tiles * w.passes * w.splits;
   return align_up(units * sizeof(unsigned), kAlign) +
@@ -638,14 +646,15 @@ size_t job_bytes(int m, int cols, int adapters, int rank, int width, int num_sms
 }  // namespace
 
 size_t wgrad_partials_bytes(int m, int n, int k, int adapters, int rank, int num_sms) {
-  return job_bytes(m, n, adapters, rank, rank16(rank), num_sms) +
-         job_bytes(m, k, adapters, rank, 2 * rank16(rank), num_sms);
+  const WgradPlans w = wgrad_plans(m, n, k, adapters, rank, num_sms);
+  return job_bytes(w.da, rank) + job_bytes(w.db, rank);
 }
 
 cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t* pairs, const uint16_t* u,
                          const Adapters& ad, const SlotLists& lists, int m, int n, int k, uint16_t* da, uint16_t* db,
                          void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
   WgradJob ja{}, jb{};
+  const WgradPlans plans = wgrad_plans(m, n, k, ad.count, ad.rank, num_sms);
   size_t smem = 0;
   if (db != nullptr) {
     WgradParams& p = jb.p;
@@ -662,7 +671,7 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
     p.status = status;
     if (!encode_bf16_map(&jb.smap, dy, m, n, kTokens) || !encode_bf16_map(&jb.zmap, u, m, ad.rank, kTokens))
       return cudaErrorInvalidValue;
-    smem = plan_job(&jb, space, num_sms);
+    smem = plan_job(&jb, plans.db, space);
     if (jb.p.splits > 1) counters += jb.units / jb.p.splits;
   }
   if (da != nullptr) {
@@ -687,8 +696,8 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
     }
     if (x.codes != nullptr ? !encode_u8_map(&ja.smap, x.codes, m, k, kTokens) : !encode_bf16_map(&ja.smap, x.x, m, k, kTokens))
       return cudaErrorInvalidValue;
-    const size_t db_bytes = db != nullptr ? job_bytes(m, n, ad.count, ad.rank, rank16(ad.rank), num_sms) : 0;
-    const size_t bytes = plan_job(&ja, static_cast<uint8_t*>(space) + db_bytes, num_sms);
+    const size_t db_bytes = db != nullptr ? job_bytes(plans.db, ad.rank) : 0;
+    const size_t bytes = plan_job(&ja, plans.da, static_cast<uint8_t*>(space) + db_bytes);
     if (bytes > smem) smem = bytes;
   }
   cudaError_t e = x.codes != nullptr ? allow_smem<adapter_wgrad_kernel<true>>(kWgradSmem)

@@ -118,3 +118,12 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(c2, -codes) and torch.equal(s2, steps * 2) and torch.equal(b2, back * -2)
+
+
+def test_inputs_at_odd_addresses():
+    """x on a 16-byte but not a 32-byte boundary."""
+    for group, k in ((64, 320), (128, 4096), (1024, 2048)):
+        buf = torch.randn(700 * k + 8, device="cuda").to(torch.bfloat16)
+        x = buf[8:].view(700, k)
+        assert x.data_ptr() % 32 == 16
+        check(x, group)
