@@ -478,7 +478,7 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
     m, dev = x.shape[0], x.device
     ad = _adapters(a, b, scale, ids, m, n, k, dev)
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
         out_p = out.data_ptr()
     else:
         out_p = _typed(out, "out", _BF16, dev, (m, n))
@@ -518,7 +518,7 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
                 raise ValueError(f"{name} was given but is not among the outputs")
             return None, None
         if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            t = torch.empty(*shape, dtype=torch.bfloat16, device=dev)
             return t, t.data_ptr()
         return t, _typed(t, name, _BF16, dev, shape)
 
@@ -559,9 +559,9 @@ def any4_act_pack(x: torch.Tensor, group: int, codes: torch.Tensor | None = None
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
     if codes is None:
-        codes = torch.empty((m, k), dtype=torch.int8, device=dev)
+        codes = torch.empty(m, k, dtype=torch.int8, device=dev)
     if steps is None:
-        steps = torch.empty((m, k // group), dtype=torch.bfloat16, device=dev)
+        steps = torch.empty(m, k // group, dtype=torch.bfloat16, device=dev)
     st = lib.any4_act_pack(_typed(x, "x", _BF16, dev, (m, k)), m, k, group, _typed(codes, "codes", _INT8, dev, (m, k)),
                            _typed(steps, "steps", _BF16, dev, (m, k // group)), _stream(dev))
     if st != ANY4_OK:
@@ -577,7 +577,7 @@ def any4_act_unpack(codes: torch.Tensor, steps: torch.Tensor, group: int,
     if group < 1 or k % group:
         raise Any4Error(ANY4_ESHAPE)
     if out is None:
-        out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(m, k, dtype=torch.bfloat16, device=dev)
     _check(lib.any4_act_unpack(_typed(codes, "codes", _INT8, dev, (m, k)),
                                _typed(steps, "steps", _BF16, dev, (m, k // group)), m, k, group,
                                _typed(out, "out", _BF16, dev, (m, k)), _stream(dev)))

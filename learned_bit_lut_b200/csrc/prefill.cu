@@ -47,6 +47,8 @@ constexpr int kBM = 128;                       // weight rows per tile (MMA M)
 constexpr int kBK = 64;                        // K per stage: one 128-byte swizzle row
 constexpr int kAStageBytes = kBM * kBK * 2;    // 16 KB
 constexpr int kGemmThreads = 192;
+constexpr int kOutWarpBytes = 32 * 64;         // an epilogue warp's 32 rows of 32 tokens, [token][row]
+constexpr int kOutBytes = 4 * kOutWarpBytes;
 constexpr int kPatchThreads = 128;             // with adapters: 4 warps more
 
 // BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
@@ -55,12 +57,12 @@ struct GemmCfg {
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int kStageBytes = kAStageBytes + BN * kBK * 2;
   static constexpr uint32_t kTmem = 2 * BN;                              // two fp32 accumulators
-  static constexpr int kSmem = kStages * kStageBytes + 1024 + 1024;      // stages, control, alignment
+  static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + 1024;   // stages, output, control, alignment
 };
 constexpr int kBN = 256;
 constexpr int kMaxStages = 6;
 
-struct GemmCtl {
+struct alignas(1024) GemmCtl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
   uint64_t acc_full[2];
@@ -73,6 +75,8 @@ struct GemmCtl {
   int spoilt[4];    // tile tcount & 3: an adapter's infinities or NaN were taken out
 };
 
+static_assert(sizeof(GemmCtl) == 1024, "control block");
+
 constexpr int kEpilogueBar = 1;                 // named barrier of the 4 epilogue warps
 constexpr int kPartialFloats = kBM * kBN;       // one split's fp32 tile [token][row] (room for BN = 256)
 constexpr int kMinSplitChunks = 8;              // K per split >= 8 stages (512 columns)
@@ -80,6 +84,75 @@ constexpr int kMaxSplits = 4;                   // the last block reads all spli
 
 __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync %0, 128;" ::"n"(kEpilogueBar) : "memory");
+}
+
+// 32 tokens from m0 on of an epilogue warp's 32 output rows (row0 on): v[i] is
+// token m0 + i of row row0 + lane. Through shared memory, so that a token's 32
+// rows leave as four 16-byte stores instead of 2 bytes a lane (`wide`: y is
+// 16-byte aligned); the warp's own `out` buffer is free before and after.
+__device__ __forceinline__ void store_rows(uint16_t* __restrict__ y, const uint32_t (&v)[32], int m0, int m, int row0,
+                                           int n, uint32_t out, bool wide, int lane) {
+  if (!wide) {
+    if (row0 + lane >= n) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (m0 + i < m) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(v[i]));
+        y[(size_t)(m0 + i) * n + row0 + lane] = *reinterpret_cast<const uint16_t*>(&h);
+      }
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(v[i]));
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + (uint32_t)(i * 64 + lane * 2)),
+                 "h"(*reinterpret_cast<const uint16_t*>(&h))
+                 : "memory");
+  }
+  __syncwarp();
+  const int row = row0 + 8 * (lane & 3);   // N is a multiple of 16
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int t = m0 + 8 * q + (lane >> 2);
+    const uint4 w = lds128(out + (uint32_t)(q * 512 + lane * 16));
+    if (t < m && row < n) *reinterpret_cast<uint4*>(y + (size_t)t * n + row) = w;
+  }
+}
+
+// The last split of a tile to arrive adds the fp32 partials of all of them in
+// split order, with every thread of the block (it has no other tile): four
+// rows of a token a step.
+template <int BN, int THREADS>
+__device__ __forceinline__ void finish_splits(const float* __restrict__ parts, int splits, uint16_t* __restrict__ y,
+                                              int nt, int mt, int m, int n) {
+  const bool pairs = (reinterpret_cast<uintptr_t>(y) & 7) == 0;
+  const int tokens = min(BN, m - mt * BN);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < tokens * (kBM / 4); i += THREADS) {
+    const int t = i / (kBM / 4), row = nt * kBM + i % (kBM / 4) * 4;
+    if (row >= n) continue;   // N is a multiple of 16
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int sp = 0; sp < kMaxSplits; ++sp) {
+      if (sp >= splits) break;
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + (size_t)sp * kPartialFloats) + i);
+      acc.x += p.x;
+      acc.y += p.y;
+      acc.z += p.z;
+      acc.w += p.w;
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    uint32_t* out = reinterpret_cast<uint32_t*>(y + (size_t)(mt * BN + t) * n + row);
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(&lo), b = *reinterpret_cast<const uint32_t*>(&hi);
+    if (pairs) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(a, b);
+    } else {
+      out[0] = a;
+      out[1] = b;
+    }
+  }
 }
 
 // ------------------------------------------------- the adapters' extra stages
@@ -210,15 +283,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
     ctl->abort_flag = 0;
+    ctl->last_split = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&ctl->tmem_base)),
-                 "r"(C::kTmem)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tc_alloc(&ctl->tmem_base, C::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -381,7 +449,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     }
   } else {
     // ---------------------------------------------------------- epilogue
+    const bool wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const int q = warp & 3;   // tensor-memory lane quarter of this warp
+    const uint32_t out = smem_addr(ctl + 1) + (uint32_t)(q * kOutWarpBytes);   // the control block is padded to 1024
     int tcount = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++tcount) {
       const int tile = u / splits;
@@ -412,14 +482,8 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         if (splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) __stcg(part + (32 * j + i) * kBM + r, __uint_as_float(v[i]));
-        } else if (row < n) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (m0 + i < m) {
-              const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(v[i]));
-              y[(size_t)(m0 + i) * n + row] = *reinterpret_cast<const uint16_t*>(&h);
-            }
-          }
+        } else {
+          store_rows(y, v, m0, m, nt * kBM + 32 * q, n, out, wide, lane);
         }
       }
       if constexpr (LORA)
@@ -431,49 +495,23 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       __syncwarp();
       if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
       if (splits > 1) {
-        // publish this split; the last of the tile's splits adds them in order
         __threadfence();
         epilogue_sync();
         if (q == 0 && lane == 0) ctl->last_split = atomicAdd(counters + tile, 1u) == (unsigned)(splits - 1);
         epilogue_sync();
-        if (ctl->last_split) {
-          __threadfence();
-          const float* base = partials + (size_t)tile * splits * kPartialFloats;
-          if (row < n) {
-            // 32 tokens at a time, so 32 loads of each split are in flight together
-#pragma unroll 1
-            for (int j0 = 0; j0 < BN && mt * BN + j0 < m; j0 += 32) {
-              float acc[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
-#pragma unroll 1
-              for (int sp = 0; sp < splits; ++sp) {
-                const float* src = base + (size_t)sp * kPartialFloats + j0 * kBM + r;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] += __ldcg(src + i * kBM);
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int mm = mt * BN + j0 + i;
-                if (mm < m) {
-                  const __nv_bfloat16 h = __float2bfloat16_rn(acc[i]);
-                  y[(size_t)mm * n + row] = *reinterpret_cast<const uint16_t*>(&h);
-                }
-              }
-            }
-          }
-          epilogue_sync();
-          if (q == 0 && lane == 0) counters[tile] = 0u;   // ready for the next call
-        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem)
-                 : "memory");
+  if (warp == 1) tc_free(tmem, C::kTmem);
+  if (splits > 1 && ctl->last_split) {   // one unit per block then
+    __threadfence();
+    const int tile = blockIdx.x / splits;
+    finish_splits<BN, kGemmThreads + (LORA ? kPatchThreads : 0)>(partials + (size_t)tile * splits * kPartialFloats, splits, y, tile / m_tiles, tile % m_tiles, m, n);
+    if (threadIdx.x == 0) counters[tile] = 0u;   // ready for the next call
+  }
 }
 
 // =============================================================================
@@ -503,11 +541,11 @@ struct FusedCfg {
   static constexpr int kBStage = BN * kBK * 2;
   static constexpr int kStage = kAStageBytes + kBStage;
   static constexpr uint32_t kTmem = 2 * BN;   // two accumulators (a power of two >= 32)
-  static constexpr int kSmem = kFusedStages * kStage + 1024 + 1024;
+  static constexpr int kSmem = kFusedStages * kStage + kOutBytes + 1024 + 1024;
   static constexpr uint32_t kIdescN = tc_idesc(BN);
 };
 
-struct FusedCtl {
+struct alignas(1024) FusedCtl {
   uint64_t full[kFusedStages];
   uint64_t empty[kFusedStages];
   uint64_t acc_full[2];
@@ -564,15 +602,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
     ctl->abort_flag = 0;
+    ctl->last_split = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&ctl->tmem_base)),
-                 "r"(C::kTmem)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tc_alloc(&ctl->tmem_base, C::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -795,7 +828,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("griddepcontrol.wait;" ::: "memory");   // y and the workspace are free
+    const bool wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const int q = warp & 3;
+    const uint32_t out = smem_addr(ctl + 1) + (uint32_t)(q * kOutWarpBytes);   // the control block is padded to 1024
     int tcount = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++tcount) {
       const int tile = u / splits;
@@ -826,14 +861,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) __stcg(part + (32 * j + i) * kBM + r, __uint_as_float(v[i]));
-        } else if (row < n) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (m0 + i < m) {
-              const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(v[i]));
-              y[(size_t)(m0 + i) * n + row] = *reinterpret_cast<const uint16_t*>(&h);
-            }
-          }
+        } else {
+          store_rows(y, v, m0, m, nt * kBM + 32 * q, n, out, wide, lane);
         }
       }
       if constexpr (LORA)
@@ -849,42 +878,19 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         epilogue_sync();
         if (q == 0 && lane == 0) ctl->last_split = atomicAdd(counters + tile, 1u) == (unsigned)(splits - 1);
         epilogue_sync();
-        if (ctl->last_split) {
-          __threadfence();
-          const float* base = partials + (size_t)tile * splits * kPartialFloats;
-          if (row < n) {
-#pragma unroll 1
-            for (int j0 = 0; j0 < BN && mt * BN + j0 < m; j0 += 32) {
-              float acc[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
-#pragma unroll 1
-              for (int sp = 0; sp < splits; ++sp) {
-                const float* src = base + (size_t)sp * kPartialFloats + j0 * kBM + r;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] += __ldcg(src + i * kBM);
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int mm = mt * BN + j0 + i;
-                if (mm < m) {
-                  const __nv_bfloat16 h = __float2bfloat16_rn(acc[i]);
-                  y[(size_t)mm * n + row] = *reinterpret_cast<const uint16_t*>(&h);
-                }
-              }
-            }
-          }
-          epilogue_sync();
-          if (q == 0 && lane == 0) counters[tile] = 0u;
-        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+  if (warp == 1) tc_free(tmem, C::kTmem);
+  if (splits > 1 && ctl->last_split) {   // one unit per block then
+    __threadfence();
+    const int tile = blockIdx.x / splits;
+    finish_splits<BN, kFusedThreads>(partials + (size_t)tile * splits * kPartialFloats, splits, y, tile / m_tiles, tile % m_tiles, m, n);
+    if (threadIdx.x == 0) counters[tile] = 0u;   // ready for the next call
+  }
 }
 
 template <auto Kernel>
