@@ -178,9 +178,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 struct LoraSpace {
   size_t delta, pairs, lists, partials, total;
 };
-LoraSpace lora_space(const LinearPlan& plan, int m, int n, int k, int rank, int sms) {
+LoraSpace lora_space(const LinearPlan& plan, const Layout& L, int m, const Adapters& ad, int sms) {
+  const int rank = ad.rank, n = L.n, k = L.k;
   LoraSpace s{};
-  size_t at = align_up(plan.workspace_bytes, kAlign);
+  size_t at = align_up(plan.mode != 3 ? plan.workspace_bytes : prefill_lora_workspace_bytes(L, m, ad, sms), kAlign);
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += align_up(bytes, kAlign);
@@ -217,7 +218,10 @@ ANY4_API size_t any4_lora_workspace_bytes(int bits, int m, int n, int k, int gro
     any4::record_cuda_error(e);
     return 0;
   }
-  return any4::lora_space(any4::plan_linear(m, any4::make_layout(n, k, group, bits), sms), m, n, k, rank, sms).total;
+  const any4::Layout L = any4::make_layout(n, k, group, bits);
+  const int32_t some = 0;   // ids or none: the larger of both needs
+  const any4::Adapters ad = {nullptr, nullptr, nullptr, &some, adapters, rank};
+  return any4::lora_space(any4::plan_linear(m, L, sms), L, m, ad, sms).total;
 }
 
 ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, int m, int n, int k, int group,
@@ -236,9 +240,9 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
   if (e != cudaSuccess) return record_cuda_error(e);
   const Layout L = make_layout(n, k, group, bits);
   const LinearPlan plan = plan_linear(m, L, sms);
-  const LoraSpace space = lora_space(plan, m, n, k, rank, sms);
-  if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
   const Adapters ad = {a, b, scale, ids, adapters, rank};
+  const LoraSpace space = lora_space(plan, L, m, ad, sms);
+  if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = (cudaStream_t)stream;

@@ -98,13 +98,14 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
                          const Adapters& ad, const SlotLists& lists, int m, int n, int k, uint16_t* da, uint16_t* db,
                          void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream);
 
-// y = x . W_hat^T + u . B_l^T for M > 16 (prefill.cu); the workspace is
-// any4_linear's.
+// y = x . W_hat^T + u . B_l^T for M > 16 (prefill.cu); the workspace is laid
+// out as any4_linear's, with room for the adapters' splits.
+size_t prefill_lora_workspace_bytes(const Layout& L, int m, const Adapters& ad, int num_sms);
 cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
                                 void* workspace, int num_sms, const AdapterTerm& term, cudaStream_t stream);
 
 // dx = dy . W_hat + v . A_l for W_hat (N x K) dequantized to bf16.
-size_t dx_partials_bytes(const Layout& L, int m, int num_sms);
+size_t dx_partials_bytes(const Layout& L, int m, const Adapters& ad, int num_sms);
 cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
                       unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream);
 

@@ -29,7 +29,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 struct GradSpace {
   size_t what, pairs, lists, partials, total;
 };
-GradSpace grad_space(const Layout& L, int m, int adapters, int rank, int sms) {
+GradSpace grad_space(const Layout& L, int m, const Adapters& ad, int sms) {
+  const int adapters = ad.count, rank = ad.rank;
   GradSpace s{};
   size_t at = align_up(kHeaderBytes, kAlign);
   auto take = [&](size_t bytes) {
@@ -40,7 +41,7 @@ GradSpace grad_space(const Layout& L, int m, int adapters, int rank, int sms) {
   s.what = take((size_t)L.n * L.k * 2);
   s.pairs = take(pairs_bytes(m, rank));
   s.lists = take(slot_lists_bytes(m));
-  const size_t down = down_partials_bytes(m, L.n, rank, sms), dx = dx_partials_bytes(L, m, sms);
+  const size_t down = down_partials_bytes(m, L.n, rank, sms), dx = dx_partials_bytes(L, m, ad, sms);
   s.partials = take(std::max(std::max(down, dx), wgrad_partials_bytes(m, L.n, L.k, adapters, rank, sms)));
   s.total = at;
   return s;
@@ -64,7 +65,9 @@ ANY4_API size_t any4_lora_grad_workspace_bytes(int bits, int m, int n, int k, in
     any4::record_cuda_error(e);
     return 0;
   }
-  return any4::grad_space(any4::make_layout(n, k, group, bits), m, adapters, rank, sms).total;
+  const int32_t some = 0;   // ids or none: the larger of both needs
+  const any4::Adapters ad = {nullptr, nullptr, nullptr, &some, adapters, rank};
+  return any4::grad_space(any4::make_layout(n, k, group, bits), m, ad, sms).total;
 }
 
 ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t* x, const int8_t* x_codes,
@@ -89,9 +92,9 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
   cudaError_t e = cached_sm_count(&sms);
   if (e != cudaSuccess) return record_cuda_error(e);
   const Layout L = make_layout(n, k, group, bits);
-  const GradSpace space = grad_space(L, m, adapters, rank, sms);
-  if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
   const Adapters ad = {a, b, scale, ids, adapters, rank};
+  const GradSpace space = grad_space(L, m, ad, sms);
+  if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + space.what);
   uint16_t* pairs = reinterpret_cast<uint16_t*>(ws + space.pairs);

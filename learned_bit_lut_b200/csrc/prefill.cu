@@ -49,6 +49,7 @@ constexpr int kAStageBytes = kBM * kBK * 2;    // 16 KB
 constexpr int kGemmThreads = 192;
 constexpr int kOutWarpBytes = 32 * 64;         // an epilogue warp's 32 rows of 32 tokens, [token][row]
 constexpr int kOutBytes = 4 * kOutWarpBytes;
+constexpr int kListBytes = 4352;               // a split's own adapter stages
 constexpr int kPatchThreads = 128;             // with adapters: 4 warps more
 
 // BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
@@ -57,7 +58,7 @@ struct GemmCfg {
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int kStageBytes = kAStageBytes + BN * kBK * 2;
   static constexpr uint32_t kTmem = 2 * BN;                              // two fp32 accumulators
-  static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + 1024;   // stages, output, control, alignment
+  static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kListBytes + 1024 + 1024;   // stages, output, list, control, alignment
 };
 constexpr int kBN = 256;
 constexpr int kMaxStages = 6;
@@ -67,6 +68,7 @@ struct alignas(1024) GemmCtl {
   uint64_t empty[kMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t listed;                // the split's own stages are known
   uint64_t raw[kMaxStages];       // TMA bytes of a stage to be patched
   uint64_t patched[kMaxStages];
   uint32_t tmem_base;
@@ -81,6 +83,7 @@ constexpr int kEpilogueBar = 1;                 // named barrier of the 4 epilog
 constexpr int kPartialFloats = kBM * kBN;       // one split's fp32 tile [token][row] (room for BN = 256)
 constexpr int kMinSplitChunks = 8;              // K per split >= 8 stages (512 columns)
 constexpr int kMaxSplits = 4;                   // the last block reads all splits' partials
+constexpr int kMaxExtraSplits = 8;              // the same where adapters' stages are split
 
 __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync %0, 128;" ::"n"(kEpilogueBar) : "memory");
@@ -135,7 +138,7 @@ __device__ __forceinline__ void finish_splits(const float* __restrict__ parts, i
     if (row >= n) continue;   // N is a multiple of 16
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int sp = 0; sp < kMaxSplits; ++sp) {
+    for (int sp = 0; sp < kMaxExtraSplits; ++sp) {
       if (sp >= splits) break;
       const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + (size_t)sp * kPartialFloats) + i);
       acc.x += p.x;
@@ -163,7 +166,8 @@ __device__ __forceinline__ void finish_splits(const float* __restrict__ parts, i
 // tile where W's goes and z's where x's goes. z is a bf16 pair, leading and
 // trailing part; for R <= 32 both lie in one 64-column row and share a stage,
 // beyond that each 64 rank columns take one stage per part. A tile's K splits
-// share them.
+// share them, by the adapter's number, so that what is added to what does not
+// depend on the order of the tokens.
 //
 // A tile whose tokens do not all have one adapter runs the stages of each of
 // its adapters, with z zeroed in the rows of the other tokens. So that an
@@ -183,9 +187,6 @@ struct LoraArgs {
   int r16;
 };
 
-// This split's share of a tile's `count` extra stages.
-__device__ __forceinline__ int extra_begin(int count, int split, int splits) { return count * split / splits; }
-
 struct Extra {
   int rank0, zcol, steps;   // first rank column, column of the pairs, 16-deep steps
   bool both;                // leading and trailing part in one stage
@@ -195,6 +196,48 @@ __device__ __forceinline__ Extra extra_stage(int r16, int h) {
   if (r16 <= 32) return {0, 0, r16 / 16, true};
   const int rank0 = 64 * (h >> 1);
   return {rank0, (h & 1) * r16 + rank0, min(4, (r16 - rank0) / 16), false};
+}
+
+// The stages of a unit in the order every role takes them: without K splits
+// those of all the tile's adapters, else this split's own (the block has one
+// unit then), which one warp writes into shared memory.
+struct StageList {
+  const SlotLists& lists;
+  const int* own;   // adapter << 2 | stage of the adapter
+  int tile, per, count;
+  SlotHead head;
+  bool split;
+  __device__ __forceinline__ int adapter(int e) const { return split ? own[e] >> 2 : slot_at(lists, tile, head, e / per); }
+  __device__ __forceinline__ int part(int e) const { return split ? own[e] & 3 : e % per; }
+};
+struct OwnStages {
+  int count;
+  int stage[4 * 256];
+};
+static_assert(sizeof(OwnStages) <= kListBytes, "stage list");
+
+__device__ __forceinline__ StageList stage_list(const LoraArgs& la, int tile, bool split, const OwnStages* own) {
+  StageList s = {la.lists, own->stage, tile, extra_stages(la.r16), 0, {0, 0, false}, split};
+  s.head = slot_head(la.lists, tile);
+  s.count = split ? own->count : s.head.count * s.per;
+  return s;
+}
+
+// One warp: the stages of split `sp` of `splits`.
+__device__ __forceinline__ void list_own_stages(const LoraArgs& la, int tile, int sp, int splits, OwnStages* own, int lane) {
+  const SlotHead head = slot_head(la.lists, tile);
+  const int per = extra_stages(la.r16);
+  int n = 0;
+  for (int e0 = 0; e0 < head.count * per; e0 += 32) {
+    const int e = e0 + lane;
+    const int l = e < head.count * per ? slot_at(la.lists, tile, head, e / per) : 0, h = e % per;
+    const bool mine = e < head.count * per && (l * per + h) % splits == sp;
+    const unsigned ballot = __ballot_sync(0xFFFFFFFFu, mine);
+    if (mine) own->stage[n + __popc(ballot & ((1u << lane) - 1u))] = l << 2 | h;
+    n += __popc(ballot);
+  }
+  if (lane == 0) own->count = n;
+  __syncwarp();
 }
 
 // Patches the first `steps` 16-deep steps of M's tile (128 rows x 64 rank
@@ -255,6 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   auto sa = [&](int s) { return sbase + (uint32_t)s * C::kStageBytes; };
   auto sb = [&](int s) { return sbase + (uint32_t)s * C::kStageBytes + kAStageBytes; };
   volatile int* abort_flag = &ctl->abort_flag;
+  [[maybe_unused]] OwnStages* own = reinterpret_cast<OwnStages*>(reinterpret_cast<uint8_t*>(ctl + 1) + kOutBytes);
 
   const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + BN - 1) / BN;
   const int tiles = n_tiles * m_tiles, kch = (k + kBK - 1) / kBK;
@@ -276,6 +320,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       mbar_init(smem_addr(&ctl->acc_empty[b]), 4);   // one arrival per epilogue warp
     }
     if (LORA) {
+      mbar_init(smem_addr(&ctl->listed), 1);
       for (int s = 0; s < kStages; ++s) {
         mbar_init(smem_addr(&ctl->raw[s]), 1);
         mbar_init(smem_addr(&ctl->patched[s]), kPatchThreads / 32);
@@ -319,18 +364,17 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           tma_load_2d(sb(s), &xmap, kc * kBK, mt * BN, fb);
         }
         if constexpr (LORA) {
-          const SlotHead head = slot_head(lora.lists, mt);
-          const bool mixed = head.mixed;
-          const int per = extra_stages(lora.r16), count = head.count * per;
-          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
-          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;   // read one stage ahead
-          for (int e = e0; e < e1; ++e, ++it) {
+          if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
+          const StageList list = stage_list(lora, mt, splits > 1, own);
+          const bool mixed = list.head.mixed;
+          int l_next = list.count > 0 ? list.adapter(0) : 0;   // read one stage ahead
+          for (int e = 0; e < list.count; ++e, ++it) {
             const int s = it % kStages;
             const uint32_t ph = (uint32_t)(it / kStages) & 1u;
             const int l = l_next;
-            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
+            if (e + 1 < list.count) l_next = list.adapter(e + 1);
             if (it >= kStages && !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
-            const Extra ex = extra_stage(lora.r16, e % per);
+            const Extra ex = extra_stage(lora.r16, list.part(e));
             // a stage to be patched lands on a barrier of its own: the patching
             // warps see only those stages, so they cannot count the others
             const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
@@ -354,7 +398,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
-        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);
+        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);   // read ahead of its use
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
@@ -375,9 +419,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           tc_commit(smem_addr(&ctl->empty[s]));   // the stage is free once these MMAs are done
         }
         if constexpr (LORA) {
-          const int per = extra_stages(lora.r16), sp = u % splits;
-          const int e1 = extra_begin(head.count * per, sp + 1, splits);
-          for (int e = extra_begin(head.count * per, sp, splits); e < e1; ++e, ++it) {
+          if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
+          const int per = extra_stages(lora.r16), count = splits > 1 ? own->count : head.count * per;
+          for (int e = 0; e < count; ++e, ++it) {
             const int s = it % kStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kStages) & 1u, abort_flag, status)) break;
             if (head.mixed) {
@@ -385,7 +429,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
               patch_phase ^= 1u << s;
             }
             tc_fence_after();
-            const Extra ex = extra_stage(lora.r16, e % per);
+            const Extra ex = extra_stage(lora.r16, splits > 1 ? own->stage[e] & 3 : e % per);
             const uint64_t ad = TRANS ? sw128_desc_mn(sa(s), kAStageBytes / 2) : sw128_desc(sa(s)), bd = sw128_desc(sb(s));
             for (int kk = 0; kk < ex.steps; ++kk) {
               const uint64_t ak = ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bk = bd + 2u * (uint64_t)kk;
@@ -409,11 +453,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         int kc0, kc1;
         k_range(u, kc0, kc1);
         it += kc1 - kc0;
-        const SlotHead head = slot_head(lora.lists, mt);
-        const bool mixed = head.mixed;
-        const int per = extra_stages(lora.r16), count = head.count * per;
-        const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
-        if (mixed) {
+        if (splits > 1 && !__all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->listed), 0u, abort_flag, status))) break;
+        const StageList list = stage_list(lora, mt, splits > 1, own);
+        if (list.head.mixed) {
           constexpr int kOwn = (BN + kPatchThreads - 1) / kPatchThreads;   // this thread's token rows
           int id[kOwn];
 #pragma unroll
@@ -422,18 +464,18 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             id[i] = row < BN && t < m ? adapter_of(lora.ad, t) : -1;
           }
           bool ok = true;
-          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
-          for (int e = e0; e < e1; ++e) {
-            const int s = (it + e - e0) % kStages;
+          int l_next = list.count > 0 ? list.adapter(0) : 0;
+          for (int e = 0; e < list.count; ++e) {
+            const int s = (it + e) % kStages;
             const int l = l_next;
-            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
+            if (e + 1 < list.count) l_next = list.adapter(e + 1);
             // the first one comes at the end of the tile's main loop
             const uint32_t rb = smem_addr(&ctl->raw[s]), rp = (raw_phase >> s) & 1u;
-            ok = __all_sync(0xFFFFFFFFu, e == e0 ? gemm_wait_idle(rb, rp, abort_flag, status)
+            ok = __all_sync(0xFFFFFFFFu, e == 0 ? gemm_wait_idle(rb, rp, abort_flag, status)
                                                  : gemm_wait(rb, rp, abort_flag, status));
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
-            if (patch_tile<TRANS, kPatchThreads>(sa(s), extra_stage(lora.r16, e % per).steps, thread))
+            if (patch_tile<TRANS, kPatchThreads>(sa(s), extra_stage(lora.r16, list.part(e)).steps, thread))
               *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
@@ -444,11 +486,17 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           }
           if (!ok) break;
         }
-        it += e1 - e0;
+        it += list.count;
       }
     }
   } else {
     // ---------------------------------------------------------- epilogue
+    if constexpr (LORA) {
+      if (splits > 1 && warp == 2) {
+        list_own_stages(lora, (int)blockIdx.x / splits % m_tiles, blockIdx.x % splits, splits, own, lane);
+        if (lane == 0) mbar_arrive_one(smem_addr(&ctl->listed));
+      }
+    }
     const bool wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const int q = warp & 3;   // tensor-memory lane quarter of this warp
     const uint32_t out = smem_addr(ctl + 1) + (uint32_t)(q * kOutWarpBytes);   // the control block is padded to 1024
@@ -541,7 +589,7 @@ struct FusedCfg {
   static constexpr int kBStage = BN * kBK * 2;
   static constexpr int kStage = kAStageBytes + kBStage;
   static constexpr uint32_t kTmem = 2 * BN;   // two accumulators (a power of two >= 32)
-  static constexpr int kSmem = kFusedStages * kStage + kOutBytes + 1024 + 1024;
+  static constexpr int kSmem = kFusedStages * kStage + kOutBytes + kListBytes + 1024 + 1024;
   static constexpr uint32_t kIdescN = tc_idesc(BN);
 };
 
@@ -550,6 +598,7 @@ struct alignas(1024) FusedCtl {
   uint64_t empty[kFusedStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t listed;
   uint64_t patched[kFusedStages];
   uint32_t tmem_base;
   int abort_flag;
@@ -578,6 +627,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
   auto sa = [&](int s) { return sbase + (uint32_t)s * C::kStage; };
   auto sb = [&](int s) { return sbase + (uint32_t)s * C::kStage + kAStageBytes; };
   volatile int* abort_flag = &ctl->abort_flag;
+  [[maybe_unused]] OwnStages* own = reinterpret_cast<OwnStages*>(reinterpret_cast<uint8_t*>(ctl + 1) + kOutBytes);
 
   const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + BN - 1) / BN;
   const int tiles = n_tiles * m_tiles, kch = k / kBK;
@@ -598,6 +648,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       mbar_init(smem_addr(&ctl->acc_empty[b]), 4);
     }
     if (LORA) {
+      mbar_init(smem_addr(&ctl->listed), 1);
       for (int s = 0; s < kFusedStages; ++s) mbar_init(smem_addr(&ctl->patched[s]), kFusedDecoders);
       for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
@@ -705,16 +756,16 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (ok) {
           asm volatile("griddepcontrol.wait;" ::: "memory");   // lists, ids and pairs are ready
           const int mt = (u / splits) % m_tiles, thread = threadIdx.x - 6 * 32;
-          const SlotHead head = slot_head(lora.lists, mt);
-          const bool mixed = head.mixed;
-          const int per = extra_stages(lora.r16), count = head.count * per;
+          ok = splits == 1 || __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status));
+          if (!ok) break;
+          const StageList list = stage_list(lora, mt, splits > 1, own);
+          const bool mixed = list.head.mixed;
           const int t = mt * BN + thread;
           const int id = mixed && thread < BN && t < m ? adapter_of(lora.ad, t) : -1;
-          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
-          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
-          for (int e = e0; e < e1; ++e) {
+          int l_next = list.count > 0 ? list.adapter(0) : 0;
+          for (int e = 0; e < list.count; ++e) {
             const int l = l_next;
-            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
+            if (e + 1 < list.count) l_next = list.adapter(e + 1);
             const int s = it % kFusedStages;
             const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
             ++it;
@@ -725,7 +776,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             if (!mixed) continue;
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
-            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), extra_stage(lora.r16, e % per).steps, thread))
+            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), extra_stage(lora.r16, list.part(e)).steps, thread))
               *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
             if (thread < BN && id != l) zero_row(sb(s), thread);
             fence_proxy_async_smem();
@@ -755,17 +806,16 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         }
         if constexpr (LORA) {
           const int nt = (u / splits) / m_tiles;
-          const SlotHead head = slot_head(lora.lists, mt);
-          const int per = extra_stages(lora.r16), count = head.count * per;
-          const int e0 = extra_begin(count, u % splits, splits), e1 = extra_begin(count, u % splits + 1, splits);
-          int l_next = e0 < e1 ? slot_at(lora.lists, mt, head, e0 / per) : 0;
-          for (int e = e0; e < e1; ++e, ++it) {
+          if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
+          const StageList list = stage_list(lora, mt, splits > 1, own);
+          int l_next = list.count > 0 ? list.adapter(0) : 0;
+          for (int e = 0; e < list.count; ++e, ++it) {
             const int l = l_next;
-            if (e + 1 < e1) l_next = slot_at(lora.lists, mt, head, (e + 1) / per);
+            if (e + 1 < list.count) l_next = list.adapter(e + 1);
             const int s = it % kFusedStages;
             const uint32_t ph = (uint32_t)(it / kFusedStages) & 1u;
             if (it >= kFusedStages && !gemm_wait_idle(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
-            const Extra ex = extra_stage(lora.r16, e % per);
+            const Extra ex = extra_stage(lora.r16, list.part(e));
             const uint32_t fb = smem_addr(&ctl->full[s]);
             mbar_arrive_expect_tx(fb, C::kStage);
             tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, fb);
@@ -782,7 +832,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       if (LORA) asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists are ready
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
-        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);
+        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);   // read ahead of its use
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status)) break;
@@ -802,9 +852,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           tc_commit(smem_addr(&ctl->empty[s]));
         }
         if constexpr (LORA) {
-          const int per = extra_stages(lora.r16), sp = u % splits;
-          const int e1 = extra_begin(head.count * per, sp + 1, splits);
-          for (int e = extra_begin(head.count * per, sp, splits); e < e1; ++e, ++it) {
+          if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
+          const int per = extra_stages(lora.r16), count = splits > 1 ? own->count : head.count * per;
+          for (int e = 0; e < count; ++e, ++it) {
             const int s = it % kFusedStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kFusedStages) & 1u, abort_flag, status)) break;
             if (head.mixed) {
@@ -812,7 +862,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
               patch_phase ^= 1u << s;
             }
             tc_fence_after();
-            const Extra ex = extra_stage(lora.r16, e % per);
+            const Extra ex = extra_stage(lora.r16, splits > 1 ? own->stage[e] & 3 : e % per);
             const uint64_t ad = sw128_desc(sa(s)), bd = sw128_desc(sb(s));
             for (int kk = 0; kk < ex.steps; ++kk) {
               const uint64_t ak = ad + 2u * (uint64_t)kk, bk = bd + 2u * (uint64_t)kk;
@@ -828,6 +878,12 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("griddepcontrol.wait;" ::: "memory");   // y and the workspace are free
+    if constexpr (LORA) {
+      if (splits > 1 && warp == 2) {
+        list_own_stages(lora, (int)blockIdx.x / splits % m_tiles, blockIdx.x % splits, splits, own, lane);
+        if (lane == 0) mbar_arrive_one(smem_addr(&ctl->listed));
+      }
+    }
     const bool wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0;
     const int q = warp & 3;
     const uint32_t out = smem_addr(ctl + 1) + (uint32_t)(q * kOutWarpBytes);   // the control block is padded to 1024
@@ -924,16 +980,36 @@ bool fill_lora(LoraArgs* la, const AdapterTerm* term, const Layout& L, int m, in
 // (larger M loops over 256-token tiles).
 int fused_bn(int m) { return m <= 64 ? 64 : m <= 128 ? 128 : 256; }
 
-int tiles_for(const Layout& L, int m, int bn) { return ((L.n + kBM - 1) / kBM) * ((m + bn - 1) / bn); }
+// Extra stages that a tile of bn tokens may need at most: all adapters that
+// can have a token in it.
+int extra_bound(const Adapters* ad, int m, int bn) {
+  if (ad == nullptr || ad->ids == nullptr) return 0;
+  const int tokens = m < bn ? m : bn, per = rank16(ad->rank) <= 32 ? 1 : (rank16(ad->rank) + 63) / 64 * 2;
+  return (ad->count < tokens ? ad->count : tokens) * per;
+}
 
-int splits_for(const Layout& L, int tiles, int num_sms) {
-  const int kch = L.k / kBK;
-  int s = tiles < num_sms ? num_sms / tiles : 1;
-  const int smax = kch / kMinSplitChunks > 0 ? kch / kMinSplitChunks : 1;
-  if (s > smax) s = smax;
+// K splits for `tiles` output tiles with kch chunks of the contraction and up
+// to `extra` stages of adapters: so many that every SM has a tile's share, of
+// 8 stages at least. Stages of adapters count like chunks (~0.5 us each on
+// B200, where a tile of few columns and many adapters would leave most SMs
+// idle), but a split needs a chunk of its own.
+int splits_of(int tiles, int kch, int extra, int num_sms) {
+  const int want = tiles < num_sms ? num_sms / tiles : 1;
+  int s = kch / kMinSplitChunks;
   if (s > kMaxSplits) s = kMaxSplits;
+  if (extra > 0) {
+    int e = (kch + extra) / kMinSplitChunks;
+    if (e > kMaxExtraSplits) e = kMaxExtraSplits;
+    if (e > kch) e = kch;
+    if (e > s) s = e;
+  }
+  if (s > want) s = want;
   return s < 1 ? 1 : s;
 }
+
+int tiles_for(const Layout& L, int m, int bn) { return ((L.n + kBM - 1) / kBM) * ((m + bn - 1) / bn); }
+
+int splits_for(const Layout& L, int tiles, int extra, int num_sms) { return splits_of(tiles, L.k / kBK, extra, num_sms); }
 
 // any4 prefill up to 512 tokens decodes into the GEMM's shared memory: it
 // reads each packed weight once instead of writing and re-reading a bf16 copy
@@ -953,7 +1029,7 @@ cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout&
   X lora;
   if (!encode_bf16_map(&xmap, x, m, L.k, BN) || !fill_lora(&lora, term, L, m, BN, false)) return cudaErrorInvalidValue;
   const int tiles = tiles_for(L, m, BN);
-  const int splits = splits_for(L, tiles, num_sms);
+  const int splits = splits_for(L, tiles, extra_bound(term != nullptr ? &term->ad : nullptr, m, BN), num_sms);
   const int units = tiles * splits;
   const int grid = units < num_sms ? units : num_sms;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
@@ -1017,32 +1093,27 @@ bool prefill_fused(const Layout& L, int m) { return fused_path(L, m); }
 
 // K splits of a GEMM with `rows` output rows, a contraction of `cols` and bn
 // tokens per tile.
-static int gemm_splits(int rows, int cols, int m, int bn, int num_sms) {
+static int gemm_splits(int rows, int cols, int m, int bn, const Adapters* ad, int num_sms) {
   const int tiles = ((rows + kBM - 1) / kBM) * ((m + bn - 1) / bn);
-  const int kch = cols / kBK;
-  int s = tiles < num_sms ? num_sms / tiles : 1;
-  const int smax = kch / kMinSplitChunks > 0 ? kch / kMinSplitChunks : 1;
-  if (s > smax) s = smax;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : s;
+  return splits_of(tiles, cols / kBK, extra_bound(ad, m, bn), num_sms);
 }
-
-int prefill_splits(const Layout& L, int m, int num_sms) { return gemm_splits(L.n, L.k, m, kBN, num_sms); }
 
 size_t prefill_partials_offset(const Layout& L) {
   return kHeaderBytes + align_up((size_t)L.n * L.k * 2, kAlign);
 }
 
-size_t prefill_workspace_bytes(const Layout& L, int m, int num_sms) {
-  if (fused_path(L, m)) {
-    const int tiles = tiles_for(L, m, fused_bn(m));
-    const int splits = splits_for(L, tiles, num_sms);
-    return kHeaderBytes + (splits > 1 ? (size_t)tiles * splits * kPartialFloats * sizeof(float) : 0);
-  }
-  const int splits = prefill_splits(L, m, num_sms);
-  const int tiles = ((L.n + kBM - 1) / kBM) * ((m + kBN - 1) / kBN);
+static size_t workspace_bytes(const Layout& L, int m, const Adapters* ad, int num_sms) {
+  const bool fused = fused_path(L, m);
+  const int bn = fused ? fused_bn(m) : kBN, tiles = tiles_for(L, m, bn);
+  const int splits = splits_for(L, tiles, extra_bound(ad, m, bn), num_sms);
   const size_t partials = splits > 1 ? (size_t)tiles * splits * kPartialFloats * sizeof(float) : 0;
-  return prefill_partials_offset(L) + partials;
+  return (fused ? kHeaderBytes : prefill_partials_offset(L)) + partials;
+}
+
+size_t prefill_workspace_bytes(const Layout& L, int m, int num_sms) { return workspace_bytes(L, m, nullptr, num_sms); }
+
+size_t prefill_lora_workspace_bytes(const Layout& L, int m, const Adapters& ad, int num_sms) {
+  return workspace_bytes(L, m, &ad, num_sms);
 }
 
 template <typename X>
@@ -1059,7 +1130,7 @@ static cudaError_t launch_prefill_any(const uint16_t* x, const uint8_t* packed, 
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + prefill_scratch_offset());
   const cudaError_t e = launch_dequant(packed, L, what, stream);   // bf16 W_hat, N x K
   if (e != cudaSuccess) return e;
-  return launch_gemm<kBN, false, X>(x, what, L, m, y, prefill_splits(L, m, num_sms),
+  return launch_gemm<kBN, false, X>(x, what, L, m, y, gemm_splits(L.n, L.k, m, kBN, term != nullptr ? &term->ad : nullptr, num_sms),
                                reinterpret_cast<float*>(ws + prefill_partials_offset(L)), reinterpret_cast<unsigned*>(ws),
                                reinterpret_cast<unsigned*>(ws + kCountersBytes), num_sms, term, stream);
 }
@@ -1076,15 +1147,15 @@ cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const 
 
 // dx takes the fused path's token tiles: 64 or 128 for few tokens (B200,
 // 4096 x 4096, M = 64: DXB us against DXA us in a 256-token tile).
-size_t dx_partials_bytes(const Layout& L, int m, int num_sms) {
-  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, num_sms);
+size_t dx_partials_bytes(const Layout& L, int m, const Adapters& ad, int num_sms) {
+  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, &ad, num_sms);
   const int tiles = ((L.k + kBM - 1) / kBM) * ((m + bn - 1) / bn);
   return splits > 1 ? align_up((size_t)tiles * splits * kPartialFloats * sizeof(float), kAlign) : 0;
 }
 
 cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
                       unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream) {
-  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, num_sms);
+  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, &term.ad, num_sms);
   switch (bn) {
     case 64:
       return launch_gemm<64, true, LoraArgs>(dy, what, L, m, dx, splits, partials, counters, status, num_sms, &term, stream);
