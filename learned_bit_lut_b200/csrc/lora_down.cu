@@ -119,6 +119,7 @@ constexpr int kMaxDownStages = 8;
 constexpr int kDownTcThreads = 224;
 constexpr int kMaxProductCols = 256;                // adapter columns of one instruction
 constexpr int kDownBar = 1;
+constexpr int kMaxDownSplits = 16;
 constexpr int kStageBudget = 104 * 1024;         // a block's stages: two blocks share an SM
 
 struct DownCtl {
@@ -156,16 +157,20 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two values as bf16 pairs: the leading parts, and in lo the trailing ones. An
+// infinity or NaN goes into both: the sum of their products is that of the one.
+__device__ __forceinline__ uint32_t split_pair(float a, float b, uint32_t& lo) {
+  const uint32_t hi = bf16x2_of(a, b);
+  const float h0 = bf16_bits_to_float(hi & 0xFFFFu), h1 = __uint_as_float(hi & 0xFFFF0000u);
+  lo = bf16x2_of(isfinite(h0) ? a - h0 : h0, isfinite(h1) ? b - h1 : h1);
+  return hi;
+}
+
 // z (16 values from r0 on) of token t: the bf16 pair, and z rounded to bf16.
 __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, const float (&z)[16]) {
   uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = bf16x2_of(z[2 * i], z[2 * i + 1]);
-    const float h0 = bf16_bits_to_float(hi[i] & 0xFFFFu), h1 = __uint_as_float(hi[i] & 0xFFFF0000u);
-    // an infinity or NaN goes into both parts: the sum of their products is that of the one
-    lo[i] = bf16x2_of(isfinite(h0) ? z[2 * i] - h0 : h0, isfinite(h1) ? z[2 * i + 1] - h1 : h1);
-  }
+  for (int i = 0; i < 8; ++i) hi[i] = split_pair(z[2 * i], z[2 * i + 1], lo[i]);
   uint4* row = reinterpret_cast<uint4*>(p.pairs + (size_t)t * 2 * p.r16 + r0);
   row[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   row[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -208,6 +213,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
     }
     mbar_init(smem_addr(&ctl->acc_full), 1);
     ctl->abort_flag = 0;
+    ctl->last = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
@@ -311,44 +317,9 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
         __threadfence();
         down_epilogue_sync();
         if (row == 0) ctl->last = atomicAdd(p.counters + tg, 1u) == (unsigned)(p.splits - 1);
-        down_epilogue_sync();
-      }
-      if (p.splits == 1) {
-        if (group == 0 && t < p.m && mine < 0) {
-          const float zero[16] = {};
-          for (int r0 = 0; r0 < r16; r0 += 16) store_inner(p, t, r0, zero);
-        }
-      } else if (ctl->last) {
-        __threadfence();
-        const int parts = r16 / 16;
-        for (int e = row; e < kTileTokens * parts; e += 128) {
-          const int tr = e / parts, r0 = e % parts * 16, tt = tile * kTileTokens + tr;
-          if (tt >= p.m) break;
-          const int l = adapter_of(p.ad, tt);
-          bool own = l < 0 && group == 0;   // the token is this group's to write
-          for (int j = 0; j < count; ++j) own |= l >= 0 && ctl->slots[j] == l;
-          if (!own) continue;
-          float z[16] = {};
-          if (l >= 0) {
-            const float* src = p.partials + ((size_t)tile * p.splits * kTileTokens + tr) * r16 + r0;
-#pragma unroll 4
-            for (int sp = 0; sp < p.splits; ++sp, src += (size_t)kTileTokens * r16) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldcg(reinterpret_cast<const float4*>(src) + i);
-                z[4 * i] += f.x;
-                z[4 * i + 1] += f.y;
-                z[4 * i + 2] += f.z;
-                z[4 * i + 3] += f.w;
-              }
-            }
-            const float sc = __ldcg(p.ad.scale + l);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] *= sc;
-          }
-          store_inner(p, tt, r0, z);
-        }
-        if (row == 0) p.counters[tg] = 0u;   // ready for the next call
+      } else if (group == 0 && t < p.m && mine < 0) {
+        const float zero[16] = {};
+        for (int r0 = 0; r0 < r16; r0 += 16) store_inner(p, t, r0, zero);
       }
     }
   }
@@ -356,6 +327,50 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tc_free(tmem, p.tmem_cols);
+  if (!ctl->last) return;
+  // the last split adds them all in order, four ranks of a token a step
+  __threadfence();
+  const int quads = r16 / 4, tokens = min(kTileTokens, p.m - tile * kTileTokens);
+  const float* parts = p.partials + (size_t)tile * p.splits * kTileTokens * r16;
+  for (int i = threadIdx.x; i < tokens * quads; i += kDownTcThreads) {
+    const int tr = i / quads, r0 = (i - tr * quads) * 4, tt = tile * kTileTokens + tr;
+    const int l = adapter_of(p.ad, tt);
+    bool own = l < 0 && group == 0;   // the token is this group's to write
+    for (int j = 0; j < count; ++j) own |= l >= 0 && ctl->slots[j] == l;
+    if (!own) continue;
+    float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (l >= 0) {
+      const float4* src = reinterpret_cast<const float4*>(parts) + i;
+#pragma unroll
+      for (int s0 = 0; s0 < kMaxDownSplits; s0 += 8) {   // eight loads in flight
+        float4 f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (s0 + q < p.splits) f[q] = __ldcg(src + (size_t)(s0 + q) * kTileTokens * quads);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (s0 + q >= p.splits) break;
+          z.x += f[q].x;
+          z.y += f[q].y;
+          z.z += f[q].z;
+          z.w += f[q].w;
+        }
+      }
+      const float sc = __ldcg(p.ad.scale + l);
+      z.x *= sc;
+      z.y *= sc;
+      z.z *= sc;
+      z.w *= sc;
+    }
+    uint32_t lo0, lo1;
+    const uint32_t hi0 = split_pair(z.x, z.y, lo0), hi1 = split_pair(z.z, z.w, lo1);
+    uint16_t* row = p.pairs + (size_t)tt * 2 * r16 + r0;
+    *reinterpret_cast<uint2*>(row) = make_uint2(hi0, hi1);
+    *reinterpret_cast<uint2*>(row + r16) = make_uint2(lo0, lo1);
+    if (p.rounded != nullptr && r0 < p.ad.rank)
+      *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) = make_uint2(hi0, hi1);
+  }
+  if (threadIdx.x == 0) p.counters[tg] = 0u;   // ready for the next call
 }
 
 template <bool BACK>
@@ -373,11 +388,15 @@ cudaError_t allow_down_smem(int bytes) {
 
 constexpr int kDownSmem = kStageBudget + 1024 + 1024;   // stages, control, alignment
 
-int down_splits(int m, int cols, int num_sms) {
+// Splits of the contraction: two blocks per SM, two chunks a block at least,
+// and no more than the last block adds in the time they save: on B200 a chunk
+// takes ~0.6 us and 64 ranks of one more split ~0.5 us.
+int down_splits(int m, int cols, int rank, int num_sms) {
   const int tiles = (m + kTileTokens - 1) / kTileTokens, chunks = (cols + kChunk - 1) / kChunk;
-  int s = 2 * num_sms / tiles;          // two blocks per SM
-  if (s > chunks / 2) s = chunks / 2;   // two chunks a block at least
-  if (s > 16) s = 16;                   // the last block reads all partials
+  int s = 2 * num_sms / tiles;
+  if (s > chunks / 2) s = chunks / 2;
+  if (s > kMaxDownSplits) s = kMaxDownSplits;
+  while (s > 1 && s * s * rank16(rank) > 77 * chunks) --s;
   return s < 1 ? 1 : s;
 }
 
@@ -408,7 +427,7 @@ cudaError_t launch_slot_lists(const Adapters& ad, int m, void* space, cudaStream
 }
 
 size_t down_partials_bytes(int m, int cols, int rank, int num_sms) {
-  const int tiles = (m + kTileTokens - 1) / kTileTokens, splits = down_splits(m, cols, num_sms);
+  const int tiles = (m + kTileTokens - 1) / kTileTokens, splits = down_splits(m, cols, rank, num_sms);
   return splits > 1 ? align_up((size_t)tiles * splits * kTileTokens * rank16(rank) * sizeof(float), kAlign) : 0;
 }
 
@@ -421,7 +440,7 @@ cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, c
   p.ad = ad;
   p.lists = lists;
   p.m = m;
-  p.splits = down_splits(m, cols, num_sms);
+  p.splits = down_splits(m, cols, ad.rank, num_sms);
   p.r16 = rank16(ad.rank);
   p.cols = backward ? (p.r16 + 63) / 64 * 64 : p.r16;
   p.m_bytes = p.cols * 128;

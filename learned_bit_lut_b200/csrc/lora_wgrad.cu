@@ -30,6 +30,7 @@
 // 14 = TMA of z.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "act8.cuh"
@@ -47,25 +48,18 @@ constexpr int kRawBytes = kTokens * kCols;       // the same in codes
 constexpr int kWorkers = 8;
 constexpr int kWorkThreads = kWorkers * 32;
 constexpr int kWgradThreads = 192 + kWorkThreads + 32;
-constexpr int kZBudget = 132 * 1024;             // z stages and chunk masks, one block per SM
-constexpr int kZBudgetTwo = 44 * 1024;           // the same for two blocks per SM
 constexpr int kMaxZStages = 8;
 constexpr int kWgradBar = 1;
 constexpr int kMaxZCols = 256;                   // z columns of one instruction:
 constexpr int kMaxPass = kMaxZCols / 32;         // at most so many adapters per block
 
-template <bool CODES>
-struct WgradCfg {
-  static constexpr int kAStages = CODES ? 2 : 4;
-  static constexpr int kRawStages = CODES ? 4 : 0;
-  static constexpr int kSrcBytes = kAStages * kABytes + kRawStages * kRawBytes;   // 64 KB both
-};
-constexpr int kMaxAStages = 4, kMaxRawStages = 4;
+constexpr int kMaxAStages = 4, kMaxRawStages = 4;   // stages of src in bf16 and in codes
+constexpr int kTwoBlocks = 110 * 1024;              // shared memory of a block where two share an SM
 constexpr int kMaxSplits = 16;
 constexpr int kWgradFixed = 1024 + 1024;         // control, alignment
-constexpr int kWgradSmem = WgradCfg<false>::kSrcBytes + kZBudget + kWgradFixed;
-// a block's chunk masks share the z stages' budget: all of 2^20 tokens leave one stage of the widest
-static_assert(kMaxTokens / kTokens * 4 + 4 * 8192 <= kZBudget, "masks and a z stage");
+constexpr int kWgradSmem = 200 * 1024;
+// the masks of all 2^20 tokens leave two stages of src and of the widest z
+static_assert(kMaxTokens / kTokens * 4 + 2 * (kABytes + 4 * 8192) + 2 * kRawBytes + kWgradFixed <= kWgradSmem, "stages");
 
 constexpr unsigned kMixed = 1u << 31;
 
@@ -92,6 +86,7 @@ struct WgradParams {
   int width;                  // z columns of one instruction: 2 R16 (pairs) or R16
   int r16;
   int group_cols, per_pass;   // tensor-memory columns per adapter, adapters per block
+  int a_stages, raw_stages;
   int z_bytes, z_stage, z_stages;   // an adapter's z tile, a stage (that or all adapters'), stages
   uint32_t idesc, idesc_all, tmem_cols;
   const uint16_t* src;        // bf16 src, or
@@ -173,12 +168,12 @@ __device__ __forceinline__ void store_grad(const WgradParams& p, int l, int col,
 template <bool PAIRS, bool CODES>
 __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUtensorMap& zmap, const WgradParams& p,
                                             const int unit) {
-  using C = WgradCfg<CODES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
-  const uint32_t rbase = sbase + C::kAStages * kABytes, zbase = sbase + C::kSrcBytes;
+  const int a_stages = p.a_stages, raw_stages = p.raw_stages;
+  const uint32_t rbase = sbase + (uint32_t)(a_stages * kABytes), zbase = rbase + (uint32_t)(raw_stages * kRawBytes);
   WgradCtl* ctl = reinterpret_cast<WgradCtl*>(smem_raw + (zbase - raw) + (size_t)p.z_stages * p.z_stage);
   // chunk c0 + i: bit g is adapter l_lo + g, kMixed: its tokens do not all have one adapter
   unsigned* info = reinterpret_cast<unsigned*>(ctl + 1);
@@ -190,13 +185,13 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
   const int l_lo = pass * p.per_pass, l_hi = min(p.ad.count, l_lo + p.per_pass);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kAStages; ++s) {
+    for (int s = 0; s < a_stages; ++s) {
       mbar_init(smem_addr(&ctl->a_full[s]), 1);
       mbar_init(smem_addr(&ctl->a_empty[s]), 1);
       mbar_init(smem_addr(&ctl->a_raw[s]), 1);
       mbar_init(smem_addr(&ctl->a_ready[s]), kWorkers);
     }
-    for (int s = 0; s < C::kRawStages; ++s) {
+    for (int s = 0; s < raw_stages; ++s) {
       mbar_init(smem_addr(&ctl->code_full[s]), 1);
       mbar_init(smem_addr(&ctl->code_empty[s]), kWorkers);
     }
@@ -239,7 +234,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
   tc_fence_after();
 
   // Every role walks the chunks alike; each takes one stage of src and one of z.
-  constexpr int kSrcStages = CODES ? C::kRawStages : C::kAStages;
+  const int src_stages = CODES ? raw_stages : a_stages;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA of src
     if (lane == 0) {
@@ -263,7 +258,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
           tma_load_2d(sbase + (uint32_t)s * kABytes, &smap, ct * kCols, c * kTokens, fb);
           tma_load_2d(sbase + (uint32_t)s * kABytes + kABytes / 2, &smap, ct * kCols + 64, c * kTokens, fb);
         }
-        r.next(kSrcStages);
+        r.next(src_stages);
       }
     }
   } else if (warp == 14) {
@@ -315,7 +310,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
           if (!gemm_wait(smem_addr(&ctl->z_ready[zs]), (z_phase >> zs) & 1u, abort_flag, p.status)) break;
           z_phase ^= 1u << zs;
         }
-        ra.next(C::kAStages);
+        ra.next(a_stages);
         rz.next(z_stages);
         tc_fence_after();
         const uint64_t ad = sw128_desc_mn(sbase + (uint32_t)s * kABytes, kABytes / 2);
@@ -353,12 +348,42 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
       return two;
     };
     uint32_t step_next = steps_of(c0);
+    // a mixed chunk's z tile: four threads a token, which take its 8-column
+    // pieces in turn; the token's adapter is read a chunk ahead
+    const int zt = thread >> 2;
+    auto adapter_at = [&](int c) {
+      const int t = c * kTokens + zt;
+      return c < c1 && (info[c - c0] & kMixed) && t < p.m ? adapter_of(p.ad, t) : -1;
+    };
+    int mine_next = adapter_at(c0);
     for (int c = c0; c < c1 && ok; ++c) {
       const unsigned in = info[c - c0];
       const bool mixed = in & kMixed;
       const uint32_t step = step_next;
+      const int mine = mine_next;
       step_next = steps_of(c + 1);
+      mine_next = adapter_at(c + 1);
       if (in == 0) continue;
+      const int zs = rz.s;
+      rz.next(z_stages);
+      if (mixed) {   // its copies run while src is waited for
+        ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        z_phase ^= 1u << zs;
+        const int first = mine >= l_lo && mine < l_hi ? (mine - l_lo) * p.group_cols : -p.width;   // its own columns
+        const int have = min(p.width, p.z_stride);   // u has R columns, which may be fewer than R16
+        const uint16_t* zrow = p.z + (size_t)(c * kTokens + zt) * p.z_stride;
+        const uint32_t ztile = zbase + (uint32_t)(zs * p.z_stage + zt * 128);
+        const int all_cols = (l_hi - l_lo) * p.group_cols;
+        for (int col = 8 * (thread & 3); col < all_cols; col += 32) {
+          const bool its = col >= first && col < first + have;
+          const uint32_t dst = ztile + (uint32_t)((col >> 6) * 8192 + ((((col >> 3) & 7) ^ (zt & 7)) << 4));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(its ? zrow + (col - first) : p.z),
+                       "r"(its ? 16 : 0)
+                       : "memory");   // 0 bytes: zeros
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
       const int s = ra.s;
       const uint32_t abase = sbase + (uint32_t)s * kABytes;
       if (CODES) {
@@ -369,7 +394,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
           ok = warp_wait(smem_addr(&ctl->a_empty[s]), ra.parity ^ 1u, abort_flag, p.status);
           if (!ok) break;
         }
-        rc.next(kSrcStages);
+        rc.next(src_stages);
         bool bad = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -408,27 +433,9 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         __syncwarp();
         if (lane == 0) mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
       }
-      ra.next(C::kAStages);
-      const int zs = rz.s;
-      rz.next(z_stages);
+      ra.next(a_stages);
       if (!mixed) continue;
-      // z's tile: four threads a token, which take its 8-column pieces in turn
-      const int zt = thread >> 2, t = c * kTokens + zt;
-      const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
-      const int first = mine >= l_lo && mine < l_hi ? (mine - l_lo) * p.group_cols : -p.width;   // its own columns
-      const int have = min(p.width, p.z_stride);   // u has R columns, which may be fewer than R16
-      const uint16_t* zrow = p.z + (size_t)t * p.z_stride;
-      ok = warp_wait(smem_addr(&ctl->z_raw[zs]), (z_phase >> zs) & 1u, abort_flag, p.status);
-      if (!ok) break;
-      z_phase ^= 1u << zs;
-      const uint32_t ztile = zbase + (uint32_t)(zs * p.z_stage + zt * 128);
-      const int all_cols = (l_hi - l_lo) * p.group_cols;
-#pragma unroll 4
-      for (int col = 8 * (thread & 3); col < all_cols; col += 32) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (col >= first && col < first + have) v = __ldcg(reinterpret_cast<const uint4*>(zrow + (col - first)));
-        sts128(ztile + (uint32_t)((col >> 6) * 8192 + ((((col >> 3) & 7) ^ (zt & 7)) << 4)), v.x, v.y, v.z, v.w);
-      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_one(smem_addr(&ctl->z_ready[zs]));
@@ -621,11 +628,15 @@ size_t plan_job(WgradJob* job, const WgradPlan& w, void* space) {
   p.z_stage = p.ad.ids == nullptr ? p.z_bytes : (all_cols + 63) / 64 * 8192;
   const int info_words = (w.chunks + w.splits - 1) / w.splits;
   const int info_bytes = (int)align_up((size_t)(info_words > kMaxPass ? info_words : kMaxPass) * sizeof(unsigned), 16);
-  // two blocks per SM where two z stages fit: the issuing threads bound a
-  // block, at ~1000 cycles a chunk
-  int stages = (kZBudgetTwo - info_bytes) / p.z_stage;
-  if (stages < 2) stages = (kZBudget - info_bytes) / p.z_stage;
-  p.z_stages = stages < kMaxZStages ? stages : kMaxZStages;
+  // two blocks per SM where two stages of z and enough of src fit: the issuing
+  // threads bound a block, at ~1000 cycles a chunk
+  const bool coded = p.codes != nullptr;
+  const int fixed = info_bytes + kWgradFixed, src = coded ? 2 * kABytes + 2 * kRawBytes : 2 * kABytes;
+  const int room = (fixed + src + 2 * p.z_stage <= kTwoBlocks ? kTwoBlocks : kWgradSmem) - fixed - 2 * p.z_stage;
+  p.a_stages = coded ? 2 : std::min(kMaxAStages, room / kABytes);
+  p.raw_stages = coded ? std::min(kMaxRawStages, (room - 2 * kABytes) / kRawBytes) : 0;
+  const int left = room - p.a_stages * kABytes - p.raw_stages * kRawBytes;
+  p.z_stages = std::min(kMaxZStages, 2 + left / p.z_stage);
   p.idesc = tc_idesc(p.width, true, true);
   p.idesc_all = tc_idesc(all_cols, true, true);
   p.tmem_cols = 32;
@@ -633,7 +644,7 @@ size_t plan_job(WgradJob* job, const WgradPlan& w, void* space) {
   job->units = w.tiles * w.passes * w.splits;
   p.masks = static_cast<unsigned*>(space);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(space) + align_up((size_t)job->units * sizeof(unsigned), kAlign));
-  return (size_t)WgradCfg<false>::kSrcBytes + (size_t)p.z_stages * p.z_stage + info_bytes + kWgradFixed;
+  return (size_t)fixed + p.a_stages * kABytes + p.raw_stages * kRawBytes + p.z_stages * p.z_stage;
 }
 
 size_t job_bytes(const WgradPlan& w, int rank) {

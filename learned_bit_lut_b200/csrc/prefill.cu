@@ -50,7 +50,7 @@ constexpr int kGemmThreads = 192;
 constexpr int kOutWarpBytes = 32 * 64;         // an epilogue warp's 32 rows of 32 tokens, [token][row]
 constexpr int kOutBytes = 4 * kOutWarpBytes;
 constexpr int kListBytes = 4352;               // a split's own adapter stages
-constexpr int kPatchThreads = 128;             // with adapters: 4 warps more
+constexpr int kPatchThreads = 256;             // with adapters: 8 warps more
 
 // BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
 template <int BN>
