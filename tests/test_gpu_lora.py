@@ -113,6 +113,30 @@ def test_gradients(shape, kept):
             assert torch.equal(one.view(torch.int16), two.view(torch.int16))
 
 
+@pytest.mark.parametrize("shape", [(1300, 1024, 8192, 128, 4, 1, 16, "null"), (5000, 2048, 4096, 128, 4, 2, 24, "holes"),
+                                   (5000, 4096, 2048, 256, 4, 1, 64, "null"), (2300, 2064, 4160, 64, 3, 1, 40, "holes")],
+                         ids=str)
+def test_longer_steps(shape):
+    """More tiles than SMs, several shares of every sum, ragged last waves."""
+    c = Case(*shape, seed=14)
+    u = torch.empty(c.m, c.rank, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(a4.any4_lora_workspace_bytes(c.m, *c.shape(), c.adapters, c.rank, bits=c.bits),
+                     dtype=torch.uint8, device="cuda")
+    y = forward(c, u=u, workspace=ws)
+    check(u, *c.u_ref(), "u")
+    check(y, *c.y_ref(), "y")
+    assert not bool(ws[:a4.lib.any4_lora_header_bytes()].any())
+    del ws
+    ws = torch.zeros(a4.any4_lora_grad_workspace_bytes(c.m, *c.shape(), c.adapters, c.rank, bits=c.bits),
+                     dtype=torch.uint8, device="cuda")
+    got = grads(c, u=u, workspace=ws)
+    for name, g, ref in zip(("dx", "da", "db"), got, c.grad_ref(c.x, u)):
+        check(g, *ref, name)
+    assert not bool(ws[:a4.lib.any4_lora_header_bytes()].any())
+    again = forward(c, u=u), *grads(c, u=u)
+    assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip((y, *got), again))
+
+
 @pytest.mark.parametrize("outputs", [("dx",), ("da",), ("db",), ("da", "db"), ("dx", "db")])
 def test_some_outputs_equal_all(outputs):
     c = Case(77, 272, 320, 64, 4, 3, 24, "holes")
