@@ -336,33 +336,32 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
     bool ok = true;
     // codes: this thread's two runs of 16 columns (run, run + 4) of one token
     const int token = thread & 63, run = thread >> 6;
-    auto steps_of = [&](int c) {
-      uint32_t two = 0;
+    // read a chunk ahead; nothing is computed of the values before their use,
+    // which would wait for the loads (half the time of a chunk)
+    const size_t step_col = (size_t)((ct * kCols + 16 * run) >> p.step_shift);
+    const size_t step_col2 = (size_t)((ct * kCols + 64 + 16 * run) >> p.step_shift);
+    const bool has_col = ct * kCols + 16 * run < p.cols, has_col2 = ct * kCols + 64 + 16 * run < p.cols;
+    auto step_of = [&](int c, size_t col, bool has) -> uint32_t {
       const int t = c * kTokens + token;
-      if (CODES && c < c1 && t < p.m) {
-        const uint16_t* row = p.steps + (size_t)t * p.step_cols;
-        const int col = ct * kCols + 16 * run;
-        if (col < p.cols) two = ld_nc_u16(row + (col >> p.step_shift));
-        if (col + 64 < p.cols) two |= ld_nc_u16(row + ((col + 64) >> p.step_shift)) << 16;
-      }
-      return two;
+      return CODES && has && c < c1 && t < p.m ? ld_nc_u16(p.steps + (size_t)t * p.step_cols + col) : 0u;
     };
-    uint32_t step_next = steps_of(c0);
+    uint32_t step_next = step_of(c0, step_col, has_col), step_next2 = step_of(c0, step_col2, has_col2);
     // a mixed chunk's z tile: four threads a token, which take its 8-column
     // pieces in turn; the token's adapter is read a chunk ahead
     const int zt = thread >> 2;
-    auto adapter_at = [&](int c) {
+    auto id_at = [&](int c) {
       const int t = c * kTokens + zt;
-      return c < c1 && (info[c - c0] & kMixed) && t < p.m ? adapter_of(p.ad, t) : -1;
+      return c < c1 && (info[c - c0] & kMixed) && t < p.m ? __ldcg(p.ad.ids + t) : -1;
     };
-    int mine_next = adapter_at(c0);
+    int id_next = id_at(c0);
     for (int c = c0; c < c1 && ok; ++c) {
       const unsigned in = info[c - c0];
       const bool mixed = in & kMixed;
-      const uint32_t step = step_next;
-      const int mine = mine_next;
-      step_next = steps_of(c + 1);
-      mine_next = adapter_at(c + 1);
+      const uint32_t step = step_next, step2nd = step_next2;
+      const int mine = id_next;
+      step_next = step_of(c + 1, step_col, has_col);
+      step_next2 = step_of(c + 1, step_col2, has_col2);
+      id_next = id_at(c + 1);
       if (in == 0) continue;
       const int zs = rz.s;
       rz.next(z_stages);
@@ -398,7 +397,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         bool bad = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t st = half ? step >> 16 : step & 0xFFFFu;
+          uint32_t st = half ? step2nd : step;
           if (mixed && (st & 0x7F80u) == 0x7F80u) {   // a group that reads back as NaN
             st = 0;
             bad = true;
