@@ -127,3 +127,15 @@ def test_inputs_at_odd_addresses():
         x = buf[8:].view(700, k)
         assert x.data_ptr() % 32 == 16
         check(x, group)
+
+
+def test_every_code_at_every_magnitude_of_step():
+    """Reading back: all codes, -128 among them, against every kind of step."""
+    steps = torch.tensor([0x0000, 0x0001, 0x0007, 0x007F, 0x0080, 0x0133, 0x3F80, 0x3FFF, 0x7AFF, 0x7B00, 0x7BFF, 0x7F7F,
+                          0x7F80, 0x7FC0], dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    codes = torch.arange(-128, 128, dtype=torch.int8, device="cuda").repeat(len(steps), 1).contiguous()
+    got = a4.any4_act_unpack(codes, steps.view(-1, 1).repeat(1, 4).contiguous(), 64)
+    want = (codes.to(F64) * steps.to(F64)[:, None]).to(torch.bfloat16)
+    assert torch.equal(got.isnan(), want.isnan())
+    fine = ~want.isnan()
+    assert torch.equal(got[fine].to(F64), want[fine].to(F64))   # values; a zero's sign is not the format's
