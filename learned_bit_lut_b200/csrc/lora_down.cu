@@ -148,6 +148,7 @@ struct DownParams {
   float* partials;             // [tile][split][token][R16]
   unsigned* counters;          // [tile][group]
   unsigned* status;
+  bool beside;                 // runs beside the kernel launched before it
 };
 
 __device__ __forceinline__ void down_epilogue_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kDownBar) : "memory"); }
@@ -200,11 +201,18 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   const int group = tg % p.groups, tile = tg / p.groups;
   const int r16 = p.r16;
 
+  // the lists and `in` are ready, the outputs are free: once the kernel before
+  // has ended, or, beside it, already. Then the last block ends after it, so
+  // that whatever waits for this kernel has waited for both.
+  const bool outlasts = p.beside && blockIdx.x == gridDim.x - 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists and `in` are ready, the outputs are free
+  if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   const SlotHead head = slot_head(p.lists, tile);
   const int j0 = group * p.per_group, count = min(head.count - j0, p.per_group);
-  if (group > 0 && count <= 0) return;   // group 0 also clears the tokens without an adapter
+  if (group > 0 && count <= 0) {   // group 0 also clears the tokens without an adapter
+    if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -327,7 +335,10 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tc_free(tmem, p.tmem_cols);
-  if (!ctl->last) return;
+  if (!ctl->last) {
+    if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   // the last split adds them all in order, four ranks of a token a step
   __threadfence();
   const int quads = r16 / 4, tokens = min(kTileTokens, p.m - tile * kTileTokens);
@@ -371,6 +382,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
       *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) = make_uint2(hi0, hi1);
   }
   if (threadIdx.x == 0) p.counters[tg] = 0u;   // ready for the next call
+  if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <bool BACK>
@@ -433,7 +445,7 @@ size_t down_partials_bytes(int m, int cols, int rank, int num_sms) {
 
 cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, const SlotLists& lists, int m, int n, int k,
                         uint16_t* pairs, uint16_t* rounded, float* partials, unsigned* counters, unsigned* status,
-                        int num_sms, cudaStream_t stream) {
+                        int num_sms, bool beside, cudaStream_t stream) {
   const int cols = backward ? n : k;
   const int tiles = (m + kTileTokens - 1) / kTileTokens;
   DownParams p{};
@@ -462,6 +474,7 @@ cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, c
   p.partials = partials;
   p.counters = counters;
   p.status = status;
+  p.beside = beside;
   CUtensorMap xmap, wmap;
   if (!encode_bf16_map(&xmap, in, m, cols, kTileTokens)) return cudaErrorInvalidValue;
   if (backward ? !encode_bf16_map3(&wmap, ad.b, ad.count, n, ad.rank, 64)

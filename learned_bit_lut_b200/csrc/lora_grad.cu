@@ -24,10 +24,11 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The workspace: any4_linear's header, W_hat in bf16, v as a bf16 pair, the
-// adapters of each token tile, then the partial sums of v, of dx and of
-// dA and dB (which follow each other).
+// adapters of each token tile, then the partial sums of v and of dx (which
+// follow each other) and those of dA and dB (which run beside dx, with the
+// other half of the header's counters).
 struct GradSpace {
-  size_t what, pairs, lists, partials, total;
+  size_t what, pairs, lists, partials, wgrad, total;
 };
 GradSpace grad_space(const Layout& L, int m, const Adapters& ad, int sms) {
   const int adapters = ad.count, rank = ad.rank;
@@ -42,7 +43,8 @@ GradSpace grad_space(const Layout& L, int m, const Adapters& ad, int sms) {
   s.pairs = take(pairs_bytes(m, rank));
   s.lists = take(slot_lists_bytes(m));
   const size_t down = down_partials_bytes(m, L.n, rank, sms), dx = dx_partials_bytes(L, m, ad, sms);
-  s.partials = take(std::max(std::max(down, dx), wgrad_partials_bytes(m, L.n, L.k, adapters, rank, sms)));
+  s.partials = take(std::max(down, dx));
+  s.wgrad = take(wgrad_partials_bytes(m, L.n, L.k, adapters, rank, sms));
   s.total = at;
   return s;
 }
@@ -105,17 +107,19 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
   AdapterTerm term{};
   term.ad = ad;
   term.pairs = pairs;
-  if (dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st);
   if (e == cudaSuccess && ids != nullptr) {
     for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
     e = launch_slot_lists(ad, m, ws + space.lists, st);
   }
+  if (e == cudaSuccess && dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st);
   if (e == cudaSuccess && (dx || da))
-    e = launch_down(true, dy, ad, term.lists[1], m, n, k, pairs, nullptr, partials, counters, status, sms, st);
+    e = launch_down(true, dy, ad, term.lists[1], m, n, k, pairs, nullptr, partials, counters, status, sms, dx != nullptr,
+                    st);
   if (e == cudaSuccess && dx) e = launch_dx(dy, what, L, m, dx, partials, counters, status, sms, term, st);
   if (e == cudaSuccess && (da || db)) {
     const KeptInput kept = {kept8 ? nullptr : x, x_codes, x_steps, x_group};
-    e = launch_wgrad(dy, kept, pairs, u, ad, term.lists[0], m, n, k, da, db, partials, counters, status, sms, st);
+    e = launch_wgrad(dy, kept, pairs, u, ad, term.lists[0], m, n, k, da, db, ws + space.wgrad, counters + kMaxTiles / 2,
+                     status, sms, dx != nullptr, st);
   }
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);
 }

@@ -100,6 +100,7 @@ struct WgradParams {
   unsigned* masks;            // [unit]: adapters with a product
   unsigned* counters;
   unsigned* status;
+  bool beside;                 // runs beside the kernel launched before it
 };
 
 __device__ __forceinline__ void wgrad_epilogue_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kWgradBar) : "memory"); }
@@ -218,7 +219,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
     tc_wait_st();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int c = c0 + threadIdx.x; c < c1; c += kWgradThreads) {
     const SlotHead h = slot_head(p.lists, c);
     unsigned mask = 0;
@@ -557,15 +558,18 @@ struct WgradJob {
   int units;
 };
 
-// The blocks of dB, then those of dA (either may have none).
+// The blocks of dB, then those of dA (either may have none). Beside the kernel
+// launched before it, the last block ends after that one: whatever waits for
+// this kernel has waited for both.
 template <bool CODES>
 __global__ void __launch_bounds__(kWgradThreads, 2)
-    adapter_wgrad_kernel(const __grid_constant__ WgradJob db, const __grid_constant__ WgradJob da) {
+    adapter_wgrad_kernel(const __grid_constant__ WgradJob db, const __grid_constant__ WgradJob da, bool beside) {
   const int unit = blockIdx.x;
   if (unit < db.units)
     wgrad_block<false, false>(db.smap, db.zmap, db.p, unit);
   else
     wgrad_block<true, CODES>(da.smap, da.zmap, da.p, unit - db.units);
+  if (beside && unit == (int)gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <auto Kernel>
@@ -662,7 +666,8 @@ size_t wgrad_partials_bytes(int m, int n, int k, int adapters, int rank, int num
 
 cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t* pairs, const uint16_t* u,
                          const Adapters& ad, const SlotLists& lists, int m, int n, int k, uint16_t* da, uint16_t* db,
-                         void* space, unsigned* counters, unsigned* status, int num_sms, cudaStream_t stream) {
+                         void* space, unsigned* counters, unsigned* status, int num_sms, bool beside,
+                         cudaStream_t stream) {
   WgradJob ja{}, jb{};
   const WgradPlans plans = wgrad_plans(m, n, k, ad.count, ad.rank, num_sms);
   size_t smem = 0;
@@ -679,6 +684,7 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
     p.out = db;
     p.counters = counters;
     p.status = status;
+    p.beside = beside;
     if (!encode_bf16_map(&jb.smap, dy, m, n, kTokens) || !encode_bf16_map(&jb.zmap, u, m, ad.rank, kTokens))
       return cudaErrorInvalidValue;
     smem = plan_job(&jb, plans.db, space);
@@ -699,6 +705,7 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
     p.out = da;
     p.counters = counters;
     p.status = status;
+    p.beside = beside;
     if (!encode_bf16_map(&ja.zmap, pairs, m, p.width, kTokens)) return cudaErrorInvalidValue;
     if (x.codes != nullptr) {
       while ((1 << p.step_shift) < x.group) ++p.step_shift;
@@ -723,8 +730,8 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return x.codes != nullptr ? cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<true>, jb, ja)
-                            : cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<false>, jb, ja);
+  return x.codes != nullptr ? cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<true>, jb, ja, beside)
+                            : cudaLaunchKernelEx(&cfg, adapter_wgrad_kernel<false>, jb, ja, beside);
 }
 
 }  // namespace any4

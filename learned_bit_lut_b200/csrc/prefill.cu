@@ -337,6 +337,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // x (and the dequantized W) are ready
+  // dA and dB need nothing of dx: their blocks take the SMs of the last, partial
+  // wave of tiles (all of v is ready, here and so there)
+  if (LORA && TRANS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
@@ -1127,16 +1130,24 @@ static cudaError_t launch_prefill_any(const uint16_t* x, const uint8_t* packed, 
     }
   }
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
-  uint16_t* what = reinterpret_cast<uint16_t*>(ws + prefill_scratch_offset());
-  const cudaError_t e = launch_dequant(packed, L, what, stream);   // bf16 W_hat, N x K
-  if (e != cudaSuccess) return e;
+  const uint16_t* what = reinterpret_cast<const uint16_t*>(ws + prefill_scratch_offset());
   return launch_gemm<kBN, false, X>(x, what, L, m, y, gemm_splits(L.n, L.k, m, kBN, term != nullptr ? &term->ad : nullptr, num_sms),
                                reinterpret_cast<float*>(ws + prefill_partials_offset(L)), reinterpret_cast<unsigned*>(ws),
                                reinterpret_cast<unsigned*>(ws + kCountersBytes), num_sms, term, stream);
 }
 
+// bf16 W_hat, N x K
+cudaError_t launch_prefill_dequant(const uint8_t* packed, const Layout& L, void* workspace, cudaStream_t stream) {
+  uint16_t* what = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + prefill_scratch_offset());
+  return launch_dequant(packed, L, what, stream);
+}
+
 cudaError_t launch_prefill(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
                            void* workspace, int num_sms, cudaStream_t stream) {
+  if (!fused_path(L, m)) {
+    const cudaError_t e = launch_prefill_dequant(packed, L, workspace, stream);
+    if (e != cudaSuccess) return e;
+  }
   return launch_prefill_any<NoLora>(x, packed, L, m, y, workspace, num_sms, nullptr, stream);
 }
 
@@ -1146,7 +1157,8 @@ cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const 
 }
 
 // dx takes the fused path's token tiles: 64 or 128 for few tokens (B200,
-// 4096 x 4096, M = 64: DXB us against DXA us in a 256-token tile).
+// 4096 x 4096, M = 64: dx with the dequantized weight 33.9 us, 36.2 us in a
+// 256-token tile; 14336 x 4096: 77.7 and 86.3 us).
 size_t dx_partials_bytes(const Layout& L, int m, const Adapters& ad, int num_sms) {
   const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, &ad, num_sms);
   const int tiles = ((L.k + kBM - 1) / kBM) * ((m + bn - 1) / bn);
