@@ -33,8 +33,9 @@ cudaError_t cached_sm_count(int* sms);
 // The 16 bf16 values of a fixed-table format (any4_format); false if unknown.
 bool format_table(int format, uint16_t (&lut)[16]);
 
-cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w,
-                           cudaStream_t stream);
+// beside: beside the kernel launched before it (lora.cuh)
+cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream,
+                           bool beside = false);
 
 // The workspace of any4_linear starts with a fixed header of arrival
 // counters (one per possible 32-row panel, so the counters of every shape live

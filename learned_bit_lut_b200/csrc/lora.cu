@@ -260,10 +260,11 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
       e = launch_slot_lists(ad, m, ws + space.lists, st);
     }
     const bool fused = prefill_fused(L, m);
-    if (e == cudaSuccess && !fused) e = launch_prefill_dequant(w, L, workspace, st);
+    if (e == cudaSuccess && !fused) e = launch_prefill_dequant(w, L, workspace, ids != nullptr, st);
     if (e == cudaSuccess)
-      e = launch_down(false, x, ad, term.lists[1], m, n, k, pairs, u, reinterpret_cast<float*>(ws + space.partials),
-                      reinterpret_cast<unsigned*>(ws), reinterpret_cast<unsigned*>(ws + kCountersBytes), sms, !fused, st);
+      e = launch_down(false, x, ad, m, n, k, pairs, u, reinterpret_cast<float*>(ws + space.partials),
+                      reinterpret_cast<unsigned*>(ws), reinterpret_cast<unsigned*>(ws + kCountersBytes), sms,
+                      ids != nullptr || !fused, st);
     if (e == cudaSuccess) e = launch_prefill_lora(x, w, L, m, y, workspace, sms, term, st);
   }
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);

@@ -73,11 +73,12 @@ inline size_t pairs_bytes(int m, int rank) { return (size_t)m * rank16(rank) * 4
 // A launch `beside` the one before it reads nothing that one writes and leaves
 // its outputs alone: it starts as soon as that kernel has blocks to spare,
 // where it would have to wait for its end. The kernel before is one that waits
-// for its own predecessors before it lets this one start (dequant, dx).
+// for its own predecessors before it lets this one start (the lists, dx), or
+// itself runs beside such a one (dequant beside the lists).
 size_t down_partials_bytes(int m, int cols, int rank, int num_sms);
-cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, const SlotLists& lists, int m, int n, int k,
-                        uint16_t* pairs, uint16_t* rounded, float* partials, unsigned* counters, unsigned* status,
-                        int num_sms, bool beside, cudaStream_t stream);
+cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, int m, int n, int k, uint16_t* pairs,
+                        uint16_t* rounded, float* partials, unsigned* counters, unsigned* status, int num_sms,
+                        bool beside, cudaStream_t stream);
 
 // What a GEMM adds to its sums: z[t] . M_l for z as above, M_l = B_l^T
 // (forward) or A_l (backward), in the accumulators of the main product.
@@ -108,7 +109,8 @@ cudaError_t launch_wgrad(const uint16_t* dy, const KeptInput& x, const uint16_t*
 // out as any4_linear's, with room for the adapters' splits. Unless
 // prefill_fused(L, m), W_hat is dequantized into it beforehand.
 size_t prefill_lora_workspace_bytes(const Layout& L, int m, const Adapters& ad, int num_sms);
-cudaError_t launch_prefill_dequant(const uint8_t* packed, const Layout& L, void* workspace, cudaStream_t stream);
+cudaError_t launch_prefill_dequant(const uint8_t* packed, const Layout& L, void* workspace, bool beside,
+                                   cudaStream_t stream);
 cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
                                 void* workspace, int num_sms, const AdapterTerm& term, cudaStream_t stream);
 

@@ -51,35 +51,38 @@ ListSpace list_space(void* space, int m) {
   return s;
 }
 
+// The nearest token before i of the same adapter, or -1: within the warp, or
+// the first token of the nearest earlier warp that has one (tiles start at
+// warps). id[] holds the adapters of the tokens, 16-byte aligned.
+__device__ __forceinline__ int token_before(const int* id, int i, int mine) {
+  const unsigned same = __match_any_sync(0xFFFFFFFFu, mine) & ((1u << (i & 31)) - 1u);
+  if (same != 0) return (i & ~31) + 31 - __clz(same);
+  if (mine < 0) return -1;
+  for (int w = (i >> 5) - 1; w >= 0; --w) {
+    const int4* ids = reinterpret_cast<const int4*>(id + 32 * w);
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int4 q = ids[c];
+      found |= q.x == mine || q.y == mine || q.z == mine || q.w == mine;
+    }
+    if (found) return 32 * w;
+  }
+  return -1;
+}
+
 __global__ void __launch_bounds__(kListTile) slot_lists_kernel(const Adapters ad, int m, ListSpace out) {
   __shared__ __align__(16) int id[kListTile];
   __shared__ int warp_first[3][kListTile / 32];
   __shared__ int warp_none[kListTile / 32];
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   const int t = blockIdx.x * kListTile + i;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int mine = t < m ? adapter_of(ad, t) : -1;
   id[i] = mine;
   __syncthreads();
-  // the nearest earlier token of the same adapter: within the warp, or the
-  // first token of the nearest earlier warp that has one (tiles start at warps)
-  int before = -1;
-  const unsigned same = __match_any_sync(0xFFFFFFFFu, mine) & ((1u << lane) - 1u);
-  if (same != 0) {
-    before = (i & ~31) + 31 - __clz(same);
-  } else if (mine >= 0) {
-    for (int w = warp - 1; w >= 0 && before < 0; --w) {
-      const int4* ids = reinterpret_cast<const int4*>(id + 32 * w);
-      bool found = false;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int4 q = ids[c];
-        found |= q.x == mine || q.y == mine || q.z == mine || q.w == mine;
-      }
-      if (found) before = 32 * w;
-    }
-  }
+  const int before = token_before(id, i, mine);
   const unsigned none = __ballot_sync(0xFFFFFFFFu, t < m && mine < 0);
   if (lane == 0) warp_none[warp] = none != 0;
   unsigned first[3];
@@ -128,13 +131,14 @@ struct DownCtl {
   uint32_t tmem_base;
   int abort_flag;
   int leave, last;   // the epilogue's own agreements
-  int slots[kMaxProductCols / 16];
+  int slots[kMaxProductCols / 16];           // the group's adapters
+  alignas(16) int id[kTileTokens];           // the tokens' adapters
+  int firsts[kTileTokens / 32];              // adapters whose first token is in a warp's 32
 };
 static_assert(sizeof(DownCtl) <= 1024, "control block");
 
 struct DownParams {
   Adapters ad;
-  SlotLists lists;
   int m, steps, splits;        // a step is `chunks` chunks of the contraction; a split takes every splits-th, so that
                                // the splits of a tile read neighbouring columns at a time (whole DRAM pages)
   int groups, per_group;       // adapter groups of a tile, adapters per group
@@ -185,6 +189,33 @@ __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, 
   }
 }
 
+// Lists the tile's adapters in the order of their first tokens (as the lists
+// that the GEMMs read, which this kernel need not wait for); those of the
+// group go to slots[] (readable after the next barrier). Their number.
+__device__ __forceinline__ int group_slots(const DownParams& p, int tile, int group, DownCtl* ctl) {
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31, j0 = group * p.per_group;
+  int mine = -1;
+  unsigned first = 0;
+  if (i < kTileTokens) {
+    if (tile * kTileTokens + i < p.m) mine = adapter_of(p.ad, tile * kTileTokens + i);
+    ctl->id[i] = mine;
+  }
+  __syncthreads();
+  if (i < kTileTokens) {
+    const int before = token_before(ctl->id, i, mine);
+    first = __ballot_sync(0xFFFFFFFFu, mine >= 0 && before < 0);
+    if (lane == 0) ctl->firsts[warp] = __popc(first);
+  }
+  __syncthreads();
+  int at = __popc(first & ((1u << lane) - 1u)) - j0, listed = 0;
+  for (int w = 0; w < kTileTokens / 32; ++w) {
+    if (w < warp) at += ctl->firsts[w];
+    listed += ctl->firsts[w];
+  }
+  if (first >> lane & 1u && at >= 0 && at < p.per_group) ctl->slots[at] = mine;
+  return min(listed - j0, p.per_group);
+}
+
 template <bool BACK>
 __global__ void __launch_bounds__(kDownTcThreads, 2)
     adapter_down_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
@@ -201,14 +232,13 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   const int group = tg % p.groups, tile = tg / p.groups;
   const int r16 = p.r16;
 
-  // the lists and `in` are ready, the outputs are free: once the kernel before
+  // ids and `in` are ready, the outputs are free: once the kernel before
   // has ended, or, beside it, already. Then the last block ends after it, so
   // that whatever waits for this kernel has waited for both.
   const bool outlasts = p.beside && blockIdx.x == gridDim.x - 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const SlotHead head = slot_head(p.lists, tile);
-  const int j0 = group * p.per_group, count = min(head.count - j0, p.per_group);
+  const int count = group_slots(p, tile, group, ctl);
   if (group > 0 && count <= 0) {   // group 0 also clears the tokens without an adapter
     if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -225,7 +255,6 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
     fence_mbar_init();
   }
   if (warp == 1) tc_alloc(&ctl->tmem_base, p.tmem_cols);
-  if ((int)threadIdx.x < count) ctl->slots[threadIdx.x] = slot_at(p.lists, tile, head, j0 + threadIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -443,14 +472,13 @@ size_t down_partials_bytes(int m, int cols, int rank, int num_sms) {
   return splits > 1 ? align_up((size_t)tiles * splits * kTileTokens * rank16(rank) * sizeof(float), kAlign) : 0;
 }
 
-cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, const SlotLists& lists, int m, int n, int k,
-                        uint16_t* pairs, uint16_t* rounded, float* partials, unsigned* counters, unsigned* status,
-                        int num_sms, bool beside, cudaStream_t stream) {
+cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, int m, int n, int k, uint16_t* pairs,
+                        uint16_t* rounded, float* partials, unsigned* counters, unsigned* status, int num_sms,
+                        bool beside, cudaStream_t stream) {
   const int cols = backward ? n : k;
   const int tiles = (m + kTileTokens - 1) / kTileTokens;
   DownParams p{};
   p.ad = ad;
-  p.lists = lists;
   p.m = m;
   p.splits = down_splits(m, cols, ad.rank, num_sms);
   p.r16 = rank16(ad.rank);

@@ -258,7 +258,7 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t pair, float a, float c) 
 
 template <int BITS, bool WIDE>
 __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8_t* __restrict__ packed, Layout L,
-                                                                     uint16_t* __restrict__ w) {
+                                                                     uint16_t* __restrict__ w, bool beside) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int P = blockIdx.y, c0 = (blockIdx.x * kDqWarps + warp) * kDqChunks;
   const uint4* lsec = reinterpret_cast<const uint4*>(packed + L.lut_off) + (size_t)P * kPanelRows * 2;
@@ -267,8 +267,9 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8
   Planes T[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) T[r] = to_planes(ld_nc_v4(lsec + (g + 8 * r) * 2), ld_nc_v4(lsec + (g + 8 * r) * 2 + 1));
-  // the packed weight is immutable; w is free, and a dependent may launch, from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the packed weight is immutable; w is free, and a dependent may launch, from
+  // here on. Beside the kernel launched before it, the last block ends after it.
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 2
   for (int c = c0; c < min(c0 + kDqChunks, L.kchunks); ++c) {
@@ -320,6 +321,8 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8
       }
     }
   }
+  if (beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 static int grid_for(size_t work, int threads) {
@@ -367,7 +370,8 @@ cudaError_t launch_pack_fixed(const uint8_t* idx_nib, const uint16_t (&lut)[16],
 }
 
 template <int BITS>
-static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream) {
+static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, bool beside,
+                                       cudaStream_t stream) {
   const int per_block = kDqWarps * kDqChunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((L.kchunks + per_block - 1) / per_block, L.panels);
@@ -379,23 +383,22 @@ static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, u
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return (reinterpret_cast<uintptr_t>(w) & 31) == 0
-             ? cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, true>, packed, L, w)
-             : cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, false>, packed, L, w);
+             ? cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, true>, packed, L, w, beside)
+             : cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, false>, packed, L, w, beside);
 }
 
-cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w,
-                           cudaStream_t stream) {
+cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream, bool beside) {
   const int th = 256;
   const size_t lanes = (size_t)L.panels * L.kchunks * 32;
   const bool runs = (reinterpret_cast<uintptr_t>(w) & 15) == 0;   // else w is only 4-byte aligned
   if (L.bits == 3) {
-    if (runs) return launch_dequant_rows<3>(packed, L, w, stream);
+    if (runs) return launch_dequant_rows<3>(packed, L, w, beside, stream);
     dequant_bits_kernel<3><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else if (L.bits == 2) {
-    if (runs) return launch_dequant_rows<2>(packed, L, w, stream);
+    if (runs) return launch_dequant_rows<2>(packed, L, w, beside, stream);
     dequant_bits_kernel<2><<<grid_for(lanes, th), th, 0, stream>>>(packed, L, w);
   } else {
-    if (runs) return launch_dequant_rows<4>(packed, L, w, stream);
+    if (runs) return launch_dequant_rows<4>(packed, L, w, beside, stream);
     dequant_kernel<<<grid_for((size_t)L.n_pad * L.k / 8, th), th, 0, stream>>>(packed, L, w);
   }
   return cudaGetLastError();

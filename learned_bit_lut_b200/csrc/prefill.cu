@@ -1137,15 +1137,16 @@ static cudaError_t launch_prefill_any(const uint16_t* x, const uint8_t* packed, 
 }
 
 // bf16 W_hat, N x K
-cudaError_t launch_prefill_dequant(const uint8_t* packed, const Layout& L, void* workspace, cudaStream_t stream) {
+cudaError_t launch_prefill_dequant(const uint8_t* packed, const Layout& L, void* workspace, bool beside,
+                                   cudaStream_t stream) {
   uint16_t* what = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + prefill_scratch_offset());
-  return launch_dequant(packed, L, what, stream);
+  return launch_dequant(packed, L, what, stream, beside);
 }
 
 cudaError_t launch_prefill(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
                            void* workspace, int num_sms, cudaStream_t stream) {
   if (!fused_path(L, m)) {
-    const cudaError_t e = launch_prefill_dequant(packed, L, workspace, stream);
+    const cudaError_t e = launch_prefill_dequant(packed, L, workspace, false, stream);
     if (e != cudaSuccess) return e;
   }
   return launch_prefill_any<NoLora>(x, packed, L, m, y, workspace, num_sms, nullptr, stream);
