@@ -24,6 +24,12 @@
 //    TMA (tiles of 128 rows x 256 tokens). The decode then runs once per
 //    call instead of once per 256-token tile.
 //
+//    With more than one wave of tiles, pairs of blocks on neighbouring SMs share
+//    tiles of 256 x 256 (cta_group::2): each brings in its 128 rows and half of
+//    the tokens and keeps the sums of its rows, and one of them issues the
+//    products of both. The GPU is at its power limit in such products, and a
+//    pair moves a third less from L2 and through shared memory per product.
+//
 // Warps of prefill_gemm_kernel: 0 = TMA producer, 1 = MMA issuer (and
 // tensor-memory owner), 2-5 = epilogue (warp w reads tensor-memory lanes
 // 32*(w%4) .. +31). Every mbarrier wait is bounded (~2 s); a timeout sets the
@@ -53,10 +59,12 @@ constexpr int kListBytes = 4352;               // a split's own adapter stages
 constexpr int kPatchThreads = 256;             // with adapters: 8 warps more
 
 // BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
-template <int BN>
+// PAIR: two blocks share a tile of 256 rows, each with half of its tokens.
+template <int BN, bool PAIR>
 struct GemmCfg {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kStageBytes = kAStageBytes + BN * kBK * 2;
+  static constexpr int kBTokens = PAIR ? BN / 2 : BN;
+  static constexpr int kStages = kBTokens == 256 ? 4 : 6;
+  static constexpr int kStageBytes = kAStageBytes + kBTokens * kBK * 2;
   static constexpr uint32_t kTmem = 2 * BN;                              // two fp32 accumulators
   static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kListBytes + 1024 + 1024;   // stages, output, list, control, alignment
 };
@@ -282,14 +290,15 @@ __device__ __noinline__ float spoilt_term(const LoraArgs& la, int t, int row, in
 // of `k`: W K-major (N x K), or with TRANS the K axis down W's rows (dx: row =
 // input column, contraction over the N outputs; a last chunk past `k` reads
 // zeros). X: NoLora, or LoraArgs for the adapters' term.
-template <int BN, bool TRANS, typename X>
+// PAIR: see the top of this file; there are no K splits then.
+template <int BN, bool TRANS, bool PAIR, typename X>
 __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0), 1)
     prefill_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         uint16_t* __restrict__ y, int m, int n, int k, int splits, float* __restrict__ partials,
                         unsigned* counters, unsigned* status, const __grid_constant__ X lora) {
   constexpr bool LORA = std::is_same<X, LoraArgs>::value;
-  using C = GemmCfg<BN>;
-  constexpr int kStages = C::kStages;
+  using C = GemmCfg<BN, PAIR>;
+  constexpr int kStages = C::kStages, kBTokens = C::kBTokens, kPeers = PAIR ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
@@ -300,16 +309,40 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   volatile int* abort_flag = &ctl->abort_flag;
   [[maybe_unused]] OwnStages* own = reinterpret_cast<OwnStages*>(reinterpret_cast<uint8_t*>(ctl + 1) + kOutBytes);
 
-  const int n_tiles = (n + kBM - 1) / kBM, m_tiles = (m + BN - 1) / BN;
+  const int n_tiles = (n + kBM * kPeers - 1) / (kBM * kPeers), m_tiles = (m + BN - 1) / BN;
   const int tiles = n_tiles * m_tiles, kch = (k + kBK - 1) / kBK;
   const int units = tiles * splits;   // unit u: tile u / splits, K split u % splits
+  const int peer = PAIR ? (int)cluster_rank() : 0;   // this block's 128 rows of a tile, and its tokens
+  const int u_first = (int)blockIdx.x / kPeers, u_step = (int)gridDim.x / kPeers;
   auto k_range = [&](int u, int& kc0, int& kc1) {
     const int sp = u % splits;
     kc0 = (int)((long long)sp * kch / splits);
     kc1 = (int)((long long)(sp + 1) * kch / splits);
   };
 
-  constexpr uint32_t idesc = tc_idesc(BN, TRANS);
+  constexpr uint32_t idesc = tc_idesc(BN, TRANS, false, kBM * kPeers);
+  auto mma = [&](uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
+    if (PAIR)
+      tc_mma_pair(d, a_desc, b_desc, idesc, accumulate);
+    else
+      tc_mma(d, a_desc, b_desc, idesc, accumulate);
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (PAIR)
+      tc_commit_pair(smem_addr(bar));
+    else
+      tc_commit(smem_addr(bar));
+  };
+  auto wait_both = [&](uint64_t* bar, uint32_t parity) {   // for arrivals from both blocks
+    return PAIR ? gemm_wait_cluster(smem_addr(bar), parity, abort_flag, status)
+                : gemm_wait(smem_addr(bar), parity, abort_flag, status);
+  };
+  auto block_sync = [&]() {
+    if (PAIR)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);    // TMA expect_tx arrival + bytes
@@ -317,13 +350,13 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&ctl->acc_full[b]), 1);    // tcgen05.commit
-      mbar_init(smem_addr(&ctl->acc_empty[b]), 4);   // one arrival per epilogue warp
+      mbar_init(smem_addr(&ctl->acc_empty[b]), 4 * kPeers);   // one arrival per epilogue warp
     }
     if (LORA) {
       mbar_init(smem_addr(&ctl->listed), 1);
       for (int s = 0; s < kStages; ++s) {
         mbar_init(smem_addr(&ctl->raw[s]), 1);
-        mbar_init(smem_addr(&ctl->patched[s]), kPatchThreads / 32);
+        mbar_init(smem_addr(&ctl->patched[s]), kPatchThreads / 32 + (PAIR && peer == 0));
       }
       for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
@@ -331,9 +364,14 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     ctl->last_split = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tc_alloc(&ctl->tmem_base, C::kTmem);
+  if (warp == 1) {
+    if (PAIR)
+      tc_alloc_pair(&ctl->tmem_base, C::kTmem);
+    else
+      tc_alloc(&ctl->tmem_base, C::kTmem);
+  }
   tc_fence_before();
-  __syncthreads();
+  block_sync();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // x (and the dequantized W) are ready
@@ -344,10 +382,17 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
+      // the bytes of both blocks of a pair count on the leader's barrier
+      auto load_2d = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+        if (PAIR)
+          tma_load_2d_pair(dst, map, c0, c1, bar);
+        else
+          tma_load_2d(dst, map, c0, c1, bar);
+      };
       int it = 0;
-      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
+      for (int u = u_first; u < units && !*abort_flag; u += u_step) {
         const int tile = u / splits;
-        const int nt = tile / m_tiles, mt = tile % m_tiles;
+        const int nt = tile / m_tiles * kPeers + peer, mt = tile % m_tiles, m0 = mt * BN + peer * kBTokens;
         int kc0, kc1;
         k_range(u, kc0, kc1);
         for (int kc = kc0; kc < kc1; ++kc, ++it) {
@@ -356,15 +401,15 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           if (it >= kStages &&
               !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status))
             break;
-          const uint32_t fb = smem_addr(&ctl->full[s]);
-          mbar_arrive_expect_tx(fb, C::kStageBytes);
+          const uint32_t own_fb = smem_addr(&ctl->full[s]), fb = PAIR ? leader_addr(own_fb) : own_fb;
+          if (peer == 0) mbar_arrive_expect_tx(own_fb, C::kStageBytes * kPeers);
           if (TRANS) {
-            tma_load_2d(sa(s), &wmap, nt * kBM, kc * kBK, fb);
-            tma_load_2d(sa(s) + kAStageBytes / 2, &wmap, nt * kBM + 64, kc * kBK, fb);
+            load_2d(sa(s), &wmap, nt * kBM, kc * kBK, fb);
+            load_2d(sa(s) + kAStageBytes / 2, &wmap, nt * kBM + 64, kc * kBK, fb);
           } else {
-            tma_load_2d(sa(s), &wmap, kc * kBK, nt * kBM, fb);
+            load_2d(sa(s), &wmap, kc * kBK, nt * kBM, fb);
           }
-          tma_load_2d(sb(s), &xmap, kc * kBK, mt * BN, fb);
+          load_2d(sb(s), &xmap, kc * kBK, m0, fb);
         }
         if constexpr (LORA) {
           if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
@@ -378,34 +423,55 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             if (e + 1 < list.count) l_next = list.adapter(e + 1);
             if (it >= kStages && !gemm_wait(smem_addr(&ctl->empty[s]), ph ^ 1u, abort_flag, status)) break;
             const Extra ex = extra_stage(lora.r16, list.part(e));
-            // a stage to be patched lands on a barrier of its own: the patching
-            // warps see only those stages, so they cannot count the others
-            const uint32_t fb = smem_addr(mixed ? &ctl->raw[s] : &ctl->full[s]);
-            mbar_arrive_expect_tx(fb, C::kStageBytes);
-            if (mixed) mbar_arrive_one(smem_addr(&ctl->full[s]));
-            if (TRANS) {
-              tma_load_3d(sa(s), &lora.mmap, nt * kBM, ex.rank0, l, fb);
-              tma_load_3d(sa(s) + kAStageBytes / 2, &lora.mmap, nt * kBM + 64, ex.rank0, l, fb);
-            } else {
-              tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, fb);
+            // a stage to be patched lands on a barrier of its own, in each block: the
+            // patching warps see only those stages, so they cannot count the others
+            const uint32_t own_fb = smem_addr(&ctl->full[s]);
+            if (mixed) {
+              const uint32_t rb = smem_addr(&ctl->raw[s]);
+              mbar_arrive_expect_tx(rb, C::kStageBytes);
+              if (peer == 0) mbar_arrive_one(own_fb);
+              if (TRANS) {
+                tma_load_3d(sa(s), &lora.mmap, nt * kBM, ex.rank0, l, rb);
+                tma_load_3d(sa(s) + kAStageBytes / 2, &lora.mmap, nt * kBM + 64, ex.rank0, l, rb);
+              } else {
+                tma_load_3d(sa(s), &lora.mmap, ex.rank0, nt * kBM, l, rb);
+              }
+              tma_load_2d(sb(s), &lora.zmap, ex.zcol, m0, rb);
+              continue;
             }
-            tma_load_2d(sb(s), &lora.zmap, ex.zcol, mt * BN, fb);
+            auto load_3d = [&](uint32_t dst, int c0, int c1, uint32_t bar) {
+              if (PAIR)
+                tma_load_3d_pair(dst, &lora.mmap, c0, c1, l, bar);
+              else
+                tma_load_3d(dst, &lora.mmap, c0, c1, l, bar);
+            };
+            const uint32_t fb = PAIR ? leader_addr(own_fb) : own_fb;
+            if (peer == 0) mbar_arrive_expect_tx(own_fb, C::kStageBytes * kPeers);
+            if (TRANS) {
+              load_3d(sa(s), nt * kBM, ex.rank0, fb);
+              load_3d(sa(s) + kAStageBytes / 2, nt * kBM + 64, ex.rank0, fb);
+            } else {
+              load_3d(sa(s), ex.rank0, nt * kBM, fb);
+            }
+            load_2d(sb(s), &lora.zmap, ex.zcol, m0, fb);
           }
         }
       }
+      if (PAIR)   // the last stages' releases come from the leader: not after this block has left
+        for (int i = it < kStages ? 0 : it - kStages; i < it; ++i)
+          if (!gemm_wait(smem_addr(&ctl->empty[i % kStages]), (uint32_t)(i / kStages) & 1u, abort_flag, status)) break;
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && peer == 0) {
       int it = 0, tcount = 0;
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
-      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
+      for (int u = u_first; u < units && !*abort_flag; u += u_step, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
         if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);   // read ahead of its use
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
-        if (tcount >= 2 && !gemm_wait(smem_addr(&ctl->acc_empty[b]), aph ^ 1u, abort_flag, status))
-          break;
+        if (tcount >= 2 && !wait_both(&ctl->acc_empty[b], aph ^ 1u)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)b * BN;
         int kc0, kc1;
@@ -418,8 +484,8 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           const uint64_t ad = TRANS ? sw128_desc_mn(sa(s), kAStageBytes / 2) : sw128_desc(sa(s)), bd = sw128_desc(sb(s));
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)   // 16 columns = 32 bytes = 2 descriptor units
-            tc_mma(d, ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bd + 2u * (uint64_t)kk, idesc, (kc > kc0 || kk > 0) ? 1u : 0u);
-          tc_commit(smem_addr(&ctl->empty[s]));   // the stage is free once these MMAs are done
+            mma(d, ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bd + 2u * (uint64_t)kk, (kc > kc0 || kk > 0) ? 1u : 0u);
+          commit(&ctl->empty[s]);   // the stage is free once these MMAs are done
         }
         if constexpr (LORA) {
           if (splits > 1 && !gemm_wait(smem_addr(&ctl->listed), 0u, abort_flag, status)) break;
@@ -428,7 +494,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             const int s = it % kStages;
             if (!gemm_wait(smem_addr(&ctl->full[s]), (uint32_t)(it / kStages) & 1u, abort_flag, status)) break;
             if (head.mixed) {
-              if (!gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)) break;
+              if (!wait_both(&ctl->patched[s], (patch_phase >> s) & 1u)) break;
               patch_phase ^= 1u << s;
             }
             tc_fence_after();
@@ -436,13 +502,33 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             const uint64_t ad = TRANS ? sw128_desc_mn(sa(s), kAStageBytes / 2) : sw128_desc(sa(s)), bd = sw128_desc(sb(s));
             for (int kk = 0; kk < ex.steps; ++kk) {
               const uint64_t ak = ad + (TRANS ? 128u : 2u) * (uint64_t)kk, bk = bd + 2u * (uint64_t)kk;
-              tc_mma(d, ak, bk, idesc, 1u);
-              if (ex.both) tc_mma(d, ak, bk + (uint64_t)(lora.r16 / 8), idesc, 1u);   // R16 columns on
+              mma(d, ak, bk, 1u);
+              if (ex.both) mma(d, ak, bk + (uint64_t)(lora.r16 / 8), 1u);   // R16 columns on
             }
-            tc_commit(smem_addr(&ctl->empty[s]));
+            commit(&ctl->empty[s]);
           }
         }
-        tc_commit(smem_addr(&ctl->acc_full[b]));
+        commit(&ctl->acc_full[b]);
+      }
+    }
+    if constexpr (PAIR && LORA) {
+      if (lane == 0 && peer == 1) {   // nothing to issue here: tells the leader of this block's patched stages
+        int it = 0;
+        uint32_t patch_phase = 0;
+        for (int u = u_first; u < units && !*abort_flag; u += u_step) {
+          const SlotHead head = slot_head(lora.lists, u % m_tiles);
+          const int count = head.count * extra_stages(lora.r16);
+          it += kch;
+          for (int e = 0; head.mixed && e < count; ++e) {
+            const int s = (it + e) % kStages;
+            if (!(e == 0 ? gemm_wait_idle(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)
+                         : gemm_wait(smem_addr(&ctl->patched[s]), (patch_phase >> s) & 1u, abort_flag, status)))
+              break;
+            patch_phase ^= 1u << s;
+            mbar_arrive_leader(smem_addr(&ctl->patched[s]));
+          }
+          it += count;
+        }
       }
     }
   } else if (LORA && warp >= 6) {
@@ -451,20 +537,20 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       const int thread = threadIdx.x - kGemmThreads;
       int it = 0, tcount = 0;
       uint32_t raw_phase = 0;
-      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x, ++tcount) {
-        const int mt = (u / splits) % m_tiles;
+      for (int u = u_first; u < units && !*abort_flag; u += u_step, ++tcount) {
+        const int mt = (u / splits) % m_tiles, m0 = mt * BN + peer * kBTokens;
         int kc0, kc1;
         k_range(u, kc0, kc1);
         it += kc1 - kc0;
         if (splits > 1 && !__all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->listed), 0u, abort_flag, status))) break;
         const StageList list = stage_list(lora, mt, splits > 1, own);
         if (list.head.mixed) {
-          constexpr int kOwn = (BN + kPatchThreads - 1) / kPatchThreads;   // this thread's token rows
+          constexpr int kOwn = (kBTokens + kPatchThreads - 1) / kPatchThreads;   // this thread's token rows
           int id[kOwn];
 #pragma unroll
           for (int i = 0; i < kOwn; ++i) {
-            const int row = thread + i * kPatchThreads, t = mt * BN + row;
-            id[i] = row < BN && t < m ? adapter_of(lora.ad, t) : -1;
+            const int row = thread + i * kPatchThreads, t = m0 + row;
+            id[i] = row < kBTokens && t < m ? adapter_of(lora.ad, t) : -1;
           }
           bool ok = true;
           int l_next = list.count > 0 ? list.adapter(0) : 0;
@@ -482,7 +568,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
               *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
-              if (thread + i * kPatchThreads < BN && id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
+              if (thread + i * kPatchThreads < kBTokens && id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
@@ -504,9 +590,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     const int q = warp & 3;   // tensor-memory lane quarter of this warp
     const uint32_t out = smem_addr(ctl + 1) + (uint32_t)(q * kOutWarpBytes);   // the control block is padded to 1024
     int tcount = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++tcount) {
+    for (int u = u_first; u < units; u += u_step, ++tcount) {
       const int tile = u / splits;
-      const int nt = tile / m_tiles, mt = tile % m_tiles;
+      const int nt = tile / m_tiles * kPeers + peer, mt = tile % m_tiles;
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
       gemm_wait(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
@@ -544,7 +630,12 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_leader(smem_addr(&ctl->acc_empty[b]));
+        else
+          mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
+      }
       if (splits > 1) {
         __threadfence();
         epilogue_sync();
@@ -554,9 +645,14 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     }
   }
   tc_fence_before();
-  __syncthreads();
+  block_sync();   // no block of a pair leaves while the other may still arrive here or multiply from here
   tc_fence_after();
-  if (warp == 1) tc_free(tmem, C::kTmem);
+  if (warp == 1) {
+    if (PAIR)
+      tc_free_pair(tmem, C::kTmem);
+    else
+      tc_free(tmem, C::kTmem);
+  }
   if (splits > 1 && ctl->last_split) {   // one unit per block then
     __threadfence();
     const int tile = blockIdx.x / splits;
@@ -965,16 +1061,16 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-// The adapter arguments of a kernel with `tokens` per tile and `rows` output
-// rows; false if a tensor map cannot be encoded.
-bool fill_lora(NoLora*, const AdapterTerm*, const Layout&, int, int, bool) { return true; }
-bool fill_lora(LoraArgs* la, const AdapterTerm* term, const Layout& L, int m, int tokens, bool trans) {
+// The adapter arguments of a kernel with `tokens` per tile, `box` of them in
+// a block; false if a tensor map cannot be encoded.
+bool fill_lora(NoLora*, const AdapterTerm*, const Layout&, int, int, int, bool) { return true; }
+bool fill_lora(LoraArgs* la, const AdapterTerm* term, const Layout& L, int m, int tokens, int box, bool trans) {
   const Adapters& ad = term->ad;
   la->ad = ad;
   la->lists = term->lists[tokens == 64 ? 0 : tokens == 128 ? 1 : 2];
   la->pairs = term->pairs;
   la->r16 = rank16(ad.rank);
-  return encode_bf16_map(&la->zmap, term->pairs, m, 2 * la->r16, tokens) &&
+  return encode_bf16_map(&la->zmap, term->pairs, m, 2 * la->r16, box) &&
          (trans ? encode_bf16_map3(&la->mmap, ad.a, ad.count, ad.rank, L.k, 64)
                 : encode_bf16_map3(&la->mmap, ad.b, ad.count, L.n, ad.rank, kBM));
 }
@@ -1030,7 +1126,7 @@ cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout&
   if (e != cudaSuccess) return e;
   CUtensorMap xmap;
   X lora;
-  if (!encode_bf16_map(&xmap, x, m, L.k, BN) || !fill_lora(&lora, term, L, m, BN, false)) return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&xmap, x, m, L.k, BN) || !fill_lora(&lora, term, L, m, BN, BN, false)) return cudaErrorInvalidValue;
   const int tiles = tiles_for(L, m, BN);
   const int splits = splits_for(L, tiles, extra_bound(term != nullptr ? &term->ad : nullptr, m, BN), num_sms);
   const int units = tiles * splits;
@@ -1059,33 +1155,56 @@ cudaError_t launch_fused(const uint16_t* x, const uint8_t* packed, const Layout&
 
 // The GEMM over `rows` output rows and a contraction of `cols`, from W_hat in
 // bf16 (N x K; TRANS: rows = K, cols = N).
-template <int BN, bool TRANS, typename X>
-cudaError_t launch_gemm(const uint16_t* in, const uint16_t* what, const Layout& L, int m, uint16_t* out, int splits,
+template <int BN, bool TRANS, bool PAIR, typename X>
+cudaError_t launch_gemm_as(const uint16_t* in, const uint16_t* what, const Layout& L, int m, uint16_t* out, int splits,
                         float* partials, unsigned* counters, unsigned* status, int num_sms, const AdapterTerm* term,
                         cudaStream_t stream) {
-  using C = GemmCfg<BN>;
-  cudaError_t e = allow_smem<prefill_gemm_kernel<BN, TRANS, X>>(C::kSmem);
+  using C = GemmCfg<BN, PAIR>;
+  cudaError_t e = allow_smem<prefill_gemm_kernel<BN, TRANS, PAIR, X>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const int rows = TRANS ? L.k : L.n, cols = TRANS ? L.n : L.k;
   CUtensorMap wmap, xmap;
   X lora;
-  if (!encode_bf16_map(&wmap, what, L.n, L.k, TRANS ? kBK : kBM) || !encode_bf16_map(&xmap, in, m, cols, BN) ||
-      !fill_lora(&lora, term, L, m, BN, TRANS))
+  if (!encode_bf16_map(&wmap, what, L.n, L.k, TRANS ? kBK : kBM) || !encode_bf16_map(&xmap, in, m, cols, C::kBTokens) ||
+      !fill_lora(&lora, term, L, m, BN, C::kBTokens, TRANS))
     return cudaErrorInvalidValue;
-  const int tiles = ((rows + kBM - 1) / kBM) * ((m + BN - 1) / BN);
-  const int units = tiles * splits;
+  constexpr int kPeers = PAIR ? 2 : 1;
+  const int tiles = ((rows + kBM * kPeers - 1) / (kBM * kPeers)) * ((m + BN - 1) / BN);
+  const int units = tiles * splits, at_once = num_sms / kPeers;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units < num_sms ? units : num_sms);
+  cfg.gridDim = dim3((unsigned)((units < at_once ? units : at_once) * kPeers));
   cfg.blockDim = dim3(kGemmThreads + (std::is_same<X, LoraArgs>::value ? kPatchThreads : 0));
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPeers;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel<BN, TRANS, X>, wmap, xmap, out, m, rows, cols, splits, partials,
-                            counters, status, lora);
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, prefill_gemm_kernel<BN, TRANS, PAIR, X>, wmap, xmap, out, m, rows, cols, splits,
+                            partials, counters, status, lora);
+}
+
+// Pairs of blocks where there is more than a wave of tiles of 256 tokens, and
+// pairing the row tiles costs no wave (an odd number of them leaves half a
+// pair idle). B200: dx of 8192 x 14336 x 4096 935 -> 847 us
+// with its dequantization and dA, dB, the forward of 4096 x 4096 x 14336 464 ->
+// 416 us; in a single wave (700 tokens, 4096 x 4096) 50.2 -> 52.5 us.
+template <int BN, bool TRANS, typename X>
+cudaError_t launch_gemm(const uint16_t* in, const uint16_t* what, const Layout& L, int m, uint16_t* out, int splits,
+                        float* partials, unsigned* counters, unsigned* status, int num_sms, const AdapterTerm* term,
+                        cudaStream_t stream) {
+  if constexpr (BN == 256) {
+    const int row_tiles = ((TRANS ? L.k : L.n) + kBM - 1) / kBM, m_tiles = (m + BN - 1) / BN, pairs = num_sms / 2;
+    const int waves = (row_tiles * m_tiles + num_sms - 1) / num_sms;
+    if (waves > 1 && pairs > 0 && ((row_tiles + 1) / 2 * m_tiles + pairs - 1) / pairs <= waves)
+      return launch_gemm_as<BN, TRANS, true, X>(in, what, L, m, out, 1, partials, counters, status, num_sms, term, stream);
+  }
+  return launch_gemm_as<BN, TRANS, false, X>(in, what, L, m, out, splits, partials, counters, status, num_sms, term, stream);
 }
 
 }  // namespace
