@@ -70,6 +70,7 @@ struct GemmCfg {
 };
 constexpr int kBN = 256;
 constexpr int kMaxStages = 6;
+constexpr int kBand = 8;   // token tiles side by side, pairs of blocks
 
 struct alignas(1024) GemmCtl {
   uint64_t full[kMaxStages];
@@ -314,6 +315,19 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   const int units = tiles * splits;   // unit u: tile u / splits, K split u % splits
   const int peer = PAIR ? (int)cluster_rank() : 0;   // this block's 128 rows of a tile, and its tokens
   const int u_first = (int)blockIdx.x / kPeers, u_step = (int)gridDim.x / kPeers;
+  // Pairs take the tiles in bands of 8 token tiles, so that those at work at a
+  // time (74 on B200) read about as many rows of W as of `in`.
+  auto place = [&](int tile, int& nt, int& mt) {
+    if (PAIR) {
+      const int band = tile / (kBand * n_tiles), r = tile - band * kBand * n_tiles;
+      const int width = min(kBand, m_tiles - band * kBand);
+      nt = r / width;
+      mt = band * kBand + r - nt * width;
+    } else {
+      nt = tile / m_tiles;
+      mt = tile - nt * m_tiles;
+    }
+  };
   auto k_range = [&](int u, int& kc0, int& kc1) {
     const int sp = u % splits;
     kc0 = (int)((long long)sp * kch / splits);
@@ -391,8 +405,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       };
       int it = 0;
       for (int u = u_first; u < units && !*abort_flag; u += u_step) {
-        const int tile = u / splits;
-        const int nt = tile / m_tiles * kPeers + peer, mt = tile % m_tiles, m0 = mt * BN + peer * kBTokens;
+        int nt, mt;
+        place(u / splits, nt, mt);
+        nt = nt * kPeers + peer;
+        const int m0 = mt * BN + peer * kBTokens;
         int kc0, kc1;
         k_range(u, kc0, kc1);
         for (int kc = kc0; kc < kc1; ++kc, ++it) {
@@ -468,7 +484,11 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       [[maybe_unused]] uint32_t patch_phase = 0;   // bit s: parity of stage s's next patch
       for (int u = u_first; u < units && !*abort_flag; u += u_step, ++tcount) {
         [[maybe_unused]] SlotHead head{0, 0, false};
-        if constexpr (LORA) head = slot_head(lora.lists, (u / splits) % m_tiles);   // read ahead of its use
+        if constexpr (LORA) {   // read ahead of its use
+          int nt, mt;
+          place(u / splits, nt, mt);
+          head = slot_head(lora.lists, mt);
+        }
         const int b = tcount & 1;
         const uint32_t aph = (uint32_t)(tcount >> 1) & 1u;
         if (tcount >= 2 && !wait_both(&ctl->acc_empty[b], aph ^ 1u)) break;
@@ -516,7 +536,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         int it = 0;
         uint32_t patch_phase = 0;
         for (int u = u_first; u < units && !*abort_flag; u += u_step) {
-          const SlotHead head = slot_head(lora.lists, u % m_tiles);
+          int nt, mt;
+          place(u, nt, mt);
+          const SlotHead head = slot_head(lora.lists, mt);
           const int count = head.count * extra_stages(lora.r16);
           it += kch;
           for (int e = 0; head.mixed && e < count; ++e) {
@@ -538,7 +560,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       int it = 0, tcount = 0;
       uint32_t raw_phase = 0;
       for (int u = u_first; u < units && !*abort_flag; u += u_step, ++tcount) {
-        const int mt = (u / splits) % m_tiles, m0 = mt * BN + peer * kBTokens;
+        int nt, mt;
+        place(u / splits, nt, mt);
+        const int m0 = mt * BN + peer * kBTokens;
         int kc0, kc1;
         k_range(u, kc0, kc1);
         it += kc1 - kc0;
@@ -592,7 +616,9 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
     int tcount = 0;
     for (int u = u_first; u < units; u += u_step, ++tcount) {
       const int tile = u / splits;
-      const int nt = tile / m_tiles * kPeers + peer, mt = tile % m_tiles;
+      int nt, mt;
+      place(tile, nt, mt);
+      nt = nt * kPeers + peer;
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
       gemm_wait(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
