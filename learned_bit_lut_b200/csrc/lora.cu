@@ -259,12 +259,11 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
       for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
       e = launch_slot_lists(ad, m, ws + space.lists, st);
     }
-    const bool fused = prefill_fused(L, m);
-    if (e == cudaSuccess && !fused) e = launch_prefill_dequant(w, L, workspace, ids != nullptr, st);
     if (e == cudaSuccess)
       e = launch_down(false, x, ad, m, n, k, pairs, u, reinterpret_cast<float*>(ws + space.partials),
                       reinterpret_cast<unsigned*>(ws), reinterpret_cast<unsigned*>(ws + kCountersBytes), sms,
-                      ids != nullptr || !fused, st);
+                      ids != nullptr, st);
+    if (e == cudaSuccess && !prefill_fused(L, m)) e = launch_prefill_dequant(w, L, workspace, true, st);
     if (e == cudaSuccess) e = launch_prefill_lora(x, w, L, m, y, workspace, sms, term, st);
   }
   return e == cudaSuccess ? ANY4_OK : record_cuda_error(e);

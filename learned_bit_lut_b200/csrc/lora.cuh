@@ -73,8 +73,9 @@ inline size_t pairs_bytes(int m, int rank) { return (size_t)m * rank16(rank) * 4
 // A launch `beside` the one before it reads nothing that one writes and leaves
 // its outputs alone: it starts as soon as that kernel has blocks to spare,
 // where it would have to wait for its end. The kernel before is one that waits
-// for its own predecessors before it lets this one start (the lists, dx), or
-// itself runs beside such a one (dequant beside the lists).
+// for its own predecessors before it lets this one start (the lists, dx; the
+// inner values without lists), or itself runs beside such a one (dequant beside
+// the inner values beside the lists).
 size_t down_partials_bytes(int m, int cols, int rank, int num_sms);
 cudaError_t launch_down(bool backward, const uint16_t* in, const Adapters& ad, int m, int n, int k, uint16_t* pairs,
                         uint16_t* rounded, float* partials, unsigned* counters, unsigned* status, int num_sms,

@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
   // has ended, or, beside it, already. Then the last block ends after it, so
   // that whatever waits for this kernel has waited for both.
   const bool outlasts = p.beside && blockIdx.x == gridDim.x - 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int count = group_slots(p, tile, group, ctl);
   if (group > 0 && count <= 0) {   // group 0 also clears the tokens without an adapter
     if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -111,9 +111,9 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
     for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
     e = launch_slot_lists(ad, m, ws + space.lists, st);
   }
-  if (e == cudaSuccess && dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st, ids != nullptr);
   if (e == cudaSuccess && (dx || da))
-    e = launch_down(true, dy, ad, m, n, k, pairs, nullptr, partials, counters, status, sms, ids != nullptr || dx, st);
+    e = launch_down(true, dy, ad, m, n, k, pairs, nullptr, partials, counters, status, sms, ids != nullptr, st);
+  if (e == cudaSuccess && dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st, true);
   if (e == cudaSuccess && dx) e = launch_dx(dy, what, L, m, dx, partials, counters, status, sms, term, st);
   if (e == cudaSuccess && (da || db)) {
     const KeptInput kept = {kept8 ? nullptr : x, x_codes, x_steps, x_group};
