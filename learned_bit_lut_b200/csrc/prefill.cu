@@ -1115,15 +1115,15 @@ int extra_bound(const Adapters* ad, int m, int bn) {
 
 // K splits for `tiles` output tiles with kch chunks of the contraction and up
 // to `extra` stages of adapters: so many that every SM has a tile's share, of
-// 8 stages at least. Stages of adapters count like chunks (~0.5 us each on
+// `least` stages at least. Stages of adapters count like chunks (~0.5 us each on
 // B200, where a tile of few columns and many adapters would leave most SMs
 // idle), but a split needs a chunk of its own.
-int splits_of(int tiles, int kch, int extra, int num_sms) {
+int splits_of(int tiles, int kch, int extra, int num_sms, int least = kMinSplitChunks) {
   const int want = tiles < num_sms ? num_sms / tiles : 1;
-  int s = kch / kMinSplitChunks;
+  int s = kch / least;
   if (s > kMaxSplits) s = kMaxSplits;
   if (extra > 0) {
-    int e = (kch + extra) / kMinSplitChunks;
+    int e = (kch + extra) / least;
     if (e > kMaxExtraSplits) e = kMaxExtraSplits;
     if (e > kch) e = kch;
     if (e > s) s = e;
@@ -1241,9 +1241,9 @@ bool prefill_fused(const Layout& L, int m) { return fused_path(L, m); }
 
 // K splits of a GEMM with `rows` output rows, a contraction of `cols` and bn
 // tokens per tile.
-static int gemm_splits(int rows, int cols, int m, int bn, const Adapters* ad, int num_sms) {
+static int gemm_splits(int rows, int cols, int m, int bn, const Adapters* ad, int num_sms, int least = kMinSplitChunks) {
   const int tiles = ((rows + kBM - 1) / kBM) * ((m + bn - 1) / bn);
-  return splits_of(tiles, cols / kBK, extra_bound(ad, m, bn), num_sms);
+  return splits_of(tiles, cols / kBK, extra_bound(ad, m, bn), num_sms, least);
 }
 
 size_t prefill_partials_offset(const Layout& L) {
@@ -1305,15 +1305,25 @@ cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const 
 // dx takes the fused path's token tiles: 64 or 128 for few tokens (B200,
 // 4096 x 4096, M = 64: dx with the dequantized weight 33.9 us, 36.2 us in a
 // 256-token tile; 14336 x 4096: 77.7 and 86.3 us).
+//
+// Its K splits are longer for more tokens: one block adds up a tile's partial
+// sums, which for 256 tokens takes as long as ~16 chunks (B200, gradients of
+// 300 tokens, 4096 x 1024: 59 us with 8 chunks a split at least, 41 with 24;
+// of 64 tokens, 4096 x 4096: 30.0 and 31.4). The forward keeps the splits of
+// the layer without adapters, and so its sums' order.
+static int dx_splits(const Layout& L, int m, int bn, const Adapters& ad, int num_sms) {
+  return gemm_splits(L.k, L.n, m, bn, &ad, num_sms, kMinSplitChunks + 16 * (m < bn ? m : bn) / 256);
+}
+
 size_t dx_partials_bytes(const Layout& L, int m, const Adapters& ad, int num_sms) {
-  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, &ad, num_sms);
+  const int bn = fused_bn(m), splits = dx_splits(L, m, bn, ad, num_sms);
   const int tiles = ((L.k + kBM - 1) / kBM) * ((m + bn - 1) / bn);
   return splits > 1 ? align_up((size_t)tiles * splits * kPartialFloats * sizeof(float), kAlign) : 0;
 }
 
 cudaError_t launch_dx(const uint16_t* dy, const uint16_t* what, const Layout& L, int m, uint16_t* dx, float* partials,
                       unsigned* counters, unsigned* status, int num_sms, const AdapterTerm& term, cudaStream_t stream) {
-  const int bn = fused_bn(m), splits = gemm_splits(L.k, L.n, m, bn, &term.ad, num_sms);
+  const int bn = fused_bn(m), splits = dx_splits(L, m, bn, term.ad, num_sms);
   switch (bn) {
     case 64:
       return launch_gemm<64, true, LoraArgs>(dy, what, L, m, dx, splits, partials, counters, status, num_sms, &term, stream);
