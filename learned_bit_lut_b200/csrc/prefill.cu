@@ -135,34 +135,45 @@ __device__ __forceinline__ void store_rows(uint16_t* __restrict__ y, const uint3
 
 // The last split of a tile to arrive adds the fp32 partials of all of them in
 // split order, with every thread of the block (it has no other tile): four
-// rows of a token a step.
+// rows of a token a step, the loads of two steps ahead of their sums (up to 16
+// in flight; B200, 300 tokens, 8 splits of 4096 -> 1024: the layer with adapters
+// 57 us with a step's loads one after the other, 38 us so).
 template <int BN, int THREADS>
 __device__ __forceinline__ void finish_splits(const float* __restrict__ parts, int splits, uint16_t* __restrict__ y,
                                               int nt, int mt, int m, int n) {
   const bool pairs = (reinterpret_cast<uintptr_t>(y) & 7) == 0;
-  const int tokens = min(BN, m - mt * BN);
-#pragma unroll 2
-  for (int i = threadIdx.x; i < tokens * (kBM / 4); i += THREADS) {
-    const int t = i / (kBM / 4), row = nt * kBM + i % (kBM / 4) * 4;
-    if (row >= n) continue;   // N is a multiple of 16
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int items = min(BN, m - mt * BN) * (kBM / 4);
+  for (int i0 = threadIdx.x; i0 < items; i0 += 2 * THREADS) {
+    float4 p[2][kMaxExtraSplits];
 #pragma unroll
-    for (int sp = 0; sp < kMaxExtraSplits; ++sp) {
-      if (sp >= splits) break;
-      const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + (size_t)sp * kPartialFloats) + i);
-      acc.x += p.x;
-      acc.y += p.y;
-      acc.z += p.z;
-      acc.w += p.w;
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * THREADS;
+#pragma unroll
+      for (int sp = 0; sp < kMaxExtraSplits; ++sp)
+        if (i < items && sp < splits) p[h][sp] = __ldcg(reinterpret_cast<const float4*>(parts + (size_t)sp * kPartialFloats) + i);
     }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    uint32_t* out = reinterpret_cast<uint32_t*>(y + (size_t)(mt * BN + t) * n + row);
-    const uint32_t a = *reinterpret_cast<const uint32_t*>(&lo), b = *reinterpret_cast<const uint32_t*>(&hi);
-    if (pairs) {
-      *reinterpret_cast<uint2*>(out) = make_uint2(a, b);
-    } else {
-      out[0] = a;
-      out[1] = b;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * THREADS, t = i / (kBM / 4), row = nt * kBM + i % (kBM / 4) * 4;
+      if (i >= items || row >= n) continue;   // N is a multiple of 16
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int sp = 0; sp < kMaxExtraSplits; ++sp) {
+        if (sp >= splits) break;
+        acc.x += p[h][sp].x;
+        acc.y += p[h][sp].y;
+        acc.z += p[h][sp].z;
+        acc.w += p[h][sp].w;
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+      uint32_t* out = reinterpret_cast<uint32_t*>(y + (size_t)(mt * BN + t) * n + row);
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(&lo), b = *reinterpret_cast<const uint32_t*>(&hi);
+      if (pairs) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(a, b);
+      } else {
+        out[0] = a;
+        out[1] = b;
+      }
     }
   }
 }
@@ -1306,13 +1317,14 @@ cudaError_t launch_prefill_lora(const uint16_t* x, const uint8_t* packed, const 
 // 4096 x 4096, M = 64: dx with the dequantized weight 33.9 us, 36.2 us in a
 // 256-token tile; 14336 x 4096: 77.7 and 86.3 us).
 //
-// Its K splits are longer for more tokens: one block adds up a tile's partial
-// sums, which for 256 tokens takes as long as ~16 chunks (B200, gradients of
-// 300 tokens, 4096 x 1024: 59 us with 8 chunks a split at least, 41 with 24;
-// of 64 tokens, 4096 x 4096: 30.0 and 31.4). The forward keeps the splits of
-// the layer without adapters, and so its sums' order.
+// Its K splits are longer for more tokens, whose partial sums take longer to
+// exchange, and SMs without one are the adapters' gradients' meanwhile (B200,
+// with those: 300 tokens, 4096 x 1024, 41.1 us with 8 chunks a split at least,
+// 36.7 with 16, 39.1 with 24; 333 tokens, 1024 x 4096, 41.9, 34.2 and 34.3).
+// The forward keeps the splits of the layer without adapters, and so its
+// sums' order.
 static int dx_splits(const Layout& L, int m, int bn, const Adapters& ad, int num_sms) {
-  return gemm_splits(L.k, L.n, m, bn, &ad, num_sms, kMinSplitChunks + 16 * (m < bn ? m : bn) / 256);
+  return gemm_splits(L.k, L.n, m, bn, &ad, num_sms, kMinSplitChunks + 8 * (m < bn ? m : bn) / 256);
 }
 
 size_t dx_partials_bytes(const Layout& L, int m, const Adapters& ad, int num_sms) {
