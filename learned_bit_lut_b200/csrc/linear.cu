@@ -236,14 +236,14 @@ __device__ __forceinline__ void out_pos(int ln, int i, int& token, int& row) {
   }
 }
 
-template <int MODE>
+template <int MODE, bool DELTA>
 __device__ __forceinline__ void store_out(const Params& p, int P, int o, float v) {
   constexpr int NF = Cfg<MODE>::kNF;
   int token, row;
   out_pos<MODE>(o / NF, o % NF, token, row);
   const int n = P * kPanelRows + row;
   if (token < p.m && n < p.n) {
-    if (p.delta != nullptr) v += __ldcg(p.delta + (size_t)token * p.n + n);
+    if (DELTA) v += __ldcg(p.delta + (size_t)token * p.n + n);
     const __nv_bfloat16 hv = __float2bfloat16_rn(v);
     p.y[(size_t)token * p.n + n] = *reinterpret_cast<const uint16_t*>(&hv);
   }
@@ -266,7 +266,9 @@ __device__ __forceinline__ uint32_t pair_addr(const uint32_t (&w)[8], int f, uin
   return (x & (((1u << (2 * BITS)) - 1u) << 8)) | base;
 }
 
-template <int MODE, int BITS, bool XV8>
+// DELTA: p.delta is added to the sums (a test of the pointer there cost the
+// layer without it 4 %).
+template <int MODE, int BITS, bool XV8, bool DELTA>
 __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Params p) {
   using C = Cfg<MODE>;
   constexpr int kCB = kChunkBytes * BITS / 4;   // bytes per chunk: 1024, 768, 512
@@ -517,8 +519,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
             }
           }
         }
-      #pragma unroll
-        for (int i = 0; i < NF; ++i) store_out<MODE>(p, P, lane * NF + i, v[i] + other[i]);
+#pragma unroll
+        for (int i = 0; i < NF; ++i) store_out<MODE, DELTA>(p, P, lane * NF + i, v[i] + other[i]);
         if (split && !clustered && lane == 0) p.counters[P] = 0u;   // ready for the next call
       } else if (clustered) {   // send this block's partial to rank 0
         const uint32_t bar0 = cluster_map(recv_bar, 0u);
@@ -752,21 +754,24 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
   if (tid == 0 && *abort) atomicOr(p.status, kStatusWaitTimeout);
 }
 
-template <int MODE, int BITS>
+template <int MODE, int BITS, bool DELTA>
 cudaError_t allow_smem_mode() {
-  cudaError_t e = cudaFuncSetAttribute(linear_kernel<MODE, BITS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<MODE>::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(linear_kernel<MODE, BITS, false, DELTA>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MODE>::kSmemBytes);
   if (e == cudaSuccess && MODE >= 1)
-    e = cudaFuncSetAttribute(linear_kernel<MODE, BITS, MODE >= 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(linear_kernel<MODE, BITS, MODE >= 1, DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg<MODE>::kSmemBytes);
   return e;
 }
 
 template <int BITS>
 cudaError_t allow_smem_bits() {
-  cudaError_t e = allow_smem_mode<0, BITS>();
-  if (e == cudaSuccess) e = allow_smem_mode<1, BITS>();
-  if (e == cudaSuccess) e = allow_smem_mode<2, BITS>();
+  cudaError_t e = allow_smem_mode<0, BITS, false>();
+  if (e == cudaSuccess) e = allow_smem_mode<1, BITS, false>();
+  if (e == cudaSuccess) e = allow_smem_mode<2, BITS, false>();
+  if (e == cudaSuccess) e = allow_smem_mode<0, BITS, true>();
+  if (e == cudaSuccess) e = allow_smem_mode<1, BITS, true>();
+  if (e == cudaSuccess) e = allow_smem_mode<2, BITS, true>();
   return e;
 }
 
@@ -804,11 +809,14 @@ cudaError_t launch_mode(const Params& p, const LinearPlan& plan, cudaStream_t st
   cfg.numAttrs = plan.cluster > 1 ? 2 : 1;
   // 256-bit activation loads: measured faster at M = 5..16 (M = 8 down
   // 4096 x 14336: 14.3 -> 13.9 us), no gain at M <= 4
-  if (MODE >= 1 && p.x_vec32) return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, MODE >= 1>, p);
-  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, false>, p);
+  if (p.delta != nullptr)
+    return MODE >= 1 && p.x_vec32 ? cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, MODE >= 1, true>, p)
+                                  : cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, false, true>, p);
+  if (MODE >= 1 && p.x_vec32) return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, MODE >= 1, false>, p);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, BITS, false, false>, p);
 }
 
-// How many clusters of `s` blocks of linear_kernel<MODE, BITS, false> the current
+// How many clusters of `s` blocks of linear_kernel<MODE, BITS, false, false> the current
 // device holds at once (0 if the query fails).
 template <int MODE, int BITS>
 int active_clusters(int s) {
@@ -825,7 +833,7 @@ int active_clusters(int s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<MODE, BITS, false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<MODE, BITS, false, false>, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }

@@ -59,7 +59,7 @@ struct RegtParams {
   size_t w_off, lut_off, ab_off;
 };
 
-template <int NT8>
+template <int NT8, bool DELTA>   // DELTA: p.delta is added
 __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(const RegtParams p) {
   using C = RegtCfg<NT8>;
   constexpr int NW = C::kWarps;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(
         const int row = P * kPanelRows + 16 * u + g + 8 * (q >> 1);
         const int tok = 8 * h + 2 * t + (q & 1);
         if (row < p.n && tok < p.m) {
-          if (p.delta != nullptr) v[u][h][q] += __ldcg(p.delta + (size_t)tok * p.n + row);
+          if (DELTA) v[u][h][q] += __ldcg(p.delta + (size_t)tok * p.n + row);
           const __nv_bfloat16 hv = __float2bfloat16_rn(v[u][h][q]);
           p.y[(size_t)tok * p.n + row] = *reinterpret_cast<const uint16_t*>(&hv);
         }
@@ -248,7 +248,10 @@ __global__ void __launch_bounds__(RegtCfg<NT8>::kThreads, 1) linear_regt_kernel(
 
 template <int NT8>
 cudaError_t regt_allow_smem() {
-  return cudaFuncSetAttribute(linear_regt_kernel<NT8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(linear_regt_kernel<NT8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             RegtCfg<NT8>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(linear_regt_kernel<NT8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               RegtCfg<NT8>::kSmem);
 }
 
@@ -259,7 +262,7 @@ int regt_max_cluster() { return kRegtMaxCluster; }
 
 cudaError_t launch_linear_regt(const uint16_t* x, const uint8_t* packed, const Layout& L, int m, uint16_t* y,
                                void* workspace, int cluster, cudaStream_t stream,
-                                const float* delta) {
+                               const float* delta) {
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -297,7 +300,11 @@ cudaError_t launch_linear_regt(const uint16_t* x, const uint8_t* packed, const L
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return m <= 8 ? cudaLaunchKernelEx(&cfg, linear_regt_kernel<1>, p) : cudaLaunchKernelEx(&cfg, linear_regt_kernel<2>, p);
+  if (delta != nullptr)
+    return m <= 8 ? cudaLaunchKernelEx(&cfg, linear_regt_kernel<1, true>, p)
+                  : cudaLaunchKernelEx(&cfg, linear_regt_kernel<2, true>, p);
+  return m <= 8 ? cudaLaunchKernelEx(&cfg, linear_regt_kernel<1, false>, p)
+                : cudaLaunchKernelEx(&cfg, linear_regt_kernel<2, false>, p);
 }
 
 }  // namespace any4

@@ -60,7 +60,7 @@ struct SmallParams {
   size_t w_off, lut_off, ab_off;
 };
 
-template <int MODE>
+template <int MODE, bool DELTA>   // DELTA: p.delta is added
 __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kernel(const SmallParams p) {
   using C = SmallCfg<MODE>;
   constexpr int NW = C::kNW, NF = C::kNF, NX = C::kNX, NCT = NW * 32;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kern
     }
     const int nrow = P * kPanelRows + row;
     if (token < p.m && nrow < p.n) {
-      if (p.delta != nullptr) v[i] += __ldcg(p.delta + (size_t)token * p.n + nrow);
+      if (DELTA) v[i] += __ldcg(p.delta + (size_t)token * p.n + nrow);
       const __nv_bfloat16 hv = __float2bfloat16_rn(v[i]);
       p.y[(size_t)token * p.n + nrow] = *reinterpret_cast<const uint16_t*>(&hv);
     }
@@ -309,7 +309,10 @@ __global__ void __launch_bounds__(SmallCfg<MODE>::kThreads, 1) linear_small_kern
 
 template <int MODE>
 cudaError_t small_allow_smem() {
-  return cudaFuncSetAttribute(linear_small_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(linear_small_kernel<MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(linear_small_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
 }
 
 template <int MODE>
@@ -328,7 +331,8 @@ cudaError_t small_launch(const SmallParams& p, int blocks, int cluster, cudaStre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_small_kernel<MODE>, p);
+  return p.delta != nullptr ? cudaLaunchKernelEx(&cfg, linear_small_kernel<MODE, true>, p)
+                            : cudaLaunchKernelEx(&cfg, linear_small_kernel<MODE, false>, p);
 }
 
 }  // namespace
