@@ -227,11 +227,14 @@ __global__ void dequant_bits_kernel(const uint8_t* __restrict__ packed, Layout L
 // one 32-byte run: the 4 lanes of a row write a 128-byte line. Codes of 3 and
 // 2 bits are first spread to the 4-bit words of the same steps. Same fp32 fma
 // and nearest-even rounding as dequant_kernel, so the same bits.
-// B200, 14336 x 4096: 38.4 us any4, 39.4 us any3, 38.9 us any2, the rate at
-// which 117 MB can be written; by look-ups in shared memory any4 took 38.8
+// B200, 14336 x 4096: 34.9 us any4, 37 us any3, 36 us any2, about the rate at
+// which 117 MB can be written (3.4 TB/s); by look-ups in shared memory any4 took 38.8
 // us, in global memory any3 took 4096 x 4096 in 93 us.
 constexpr int kDqWarps = 8;
 constexpr int kDqChunks = 4;   // chunks of a warp in a row: the tables are loaded once
+// With fewer blocks than this a warp takes one chunk (B200, any4: 1024 x 4096
+// 2.8 us, with four 5.6; 2048 x 4096 5.3 and 5.8; 4096 x 4096 is beyond it, 8.8).
+constexpr int kDqFewBlocks = 256;
 
 // The 4-bit word of step s (a row-pair code per byte) from the lane's packed bits.
 template <int BITS>
@@ -258,9 +261,9 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t pair, float a, float c) 
 
 template <int BITS, bool WIDE>
 __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8_t* __restrict__ packed, Layout L,
-                                                                     uint16_t* __restrict__ w, bool beside) {
+                                                                     uint16_t* __restrict__ w, int chunks, bool beside) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int P = blockIdx.y, c0 = (blockIdx.x * kDqWarps + warp) * kDqChunks;
+  const int P = blockIdx.y, c0 = (blockIdx.x * kDqWarps + warp) * chunks;
   const uint4* lsec = reinterpret_cast<const uint4*>(packed + L.lut_off) + (size_t)P * kPanelRows * 2;
   const uint4* asec = reinterpret_cast<const uint4*>(packed + L.ab_off) + (size_t)P * L.groups * 8 + g;
   const int gshift = __ffs(L.g) - 1;   // G is a power of two
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8
   if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 2
-  for (int c = c0; c < min(c0 + kDqChunks, L.kchunks); ++c) {
+  for (int c = c0; c < min(c0 + chunks, L.kchunks); ++c) {
     const uint8_t* chunk = packed + L.w_off + ((size_t)P * L.kchunks + c) * L.chunk_bytes;
     uint32_t wd[8] = {};
     const uint4 lo = ld_stream_v4(chunk + lane * 16);
@@ -372,7 +375,8 @@ cudaError_t launch_pack_fixed(const uint8_t* idx_nib, const uint16_t (&lut)[16],
 template <int BITS>
 static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, uint16_t* w, bool beside,
                                        cudaStream_t stream) {
-  const int per_block = kDqWarps * kDqChunks;
+  const int most = kDqWarps * kDqChunks;
+  const int chunks = (L.kchunks + most - 1) / most * L.panels < kDqFewBlocks ? 1 : kDqChunks, per_block = kDqWarps * chunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((L.kchunks + per_block - 1) / per_block, L.panels);
   cfg.blockDim = dim3(kDqWarps * 32);
@@ -383,8 +387,8 @@ static cudaError_t launch_dequant_rows(const uint8_t* packed, const Layout& L, u
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return (reinterpret_cast<uintptr_t>(w) & 31) == 0
-             ? cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, true>, packed, L, w, beside)
-             : cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, false>, packed, L, w, beside);
+             ? cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, true>, packed, L, w, chunks, beside)
+             : cudaLaunchKernelEx(&cfg, dequant_rows_kernel<BITS, false>, packed, L, w, chunks, beside);
 }
 
 cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream, bool beside) {
