@@ -369,3 +369,73 @@ def test_decode_reads_what_the_kernel_before_it_wrote(m, n, k):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, want[j % 8]) for j, o in enumerate(outs))
+
+
+# more than 148 tiles of 128 x 256, so two blocks share each: an odd number of
+# row tiles forward (19) and backward (17), a last tile whose second block has
+# no tokens (2600 = 10 x 256 + 40) and one whose second block has no rows
+@pytest.mark.parametrize("shape", [(2600, 2320, 2112, 64, 4, 5, 24, "holes"), (2600, 2320, 2112, 64, 3, 3, 72, "runs"),
+                                   (2600, 2320, 2112, 64, 4, 1, 128, "null"), (5200, 1040, 1088, 64, 2, 40, 16, "mixed")],
+                         ids=["holes", "runs", "null", "many"])
+def test_tiles_shared_by_two_blocks(shape):
+    c = Case(*shape, seed=21)
+    if c.adapters == 5:   # spoilt adapters must not reach the tokens that share their tiles
+        c.a[1, 3, 17] = float("nan")
+        c.b[2, 5, 7] = float("inf")
+        c.b[2, 2319, 1] = float("-inf")
+        c.a[3, 0, 2111] = float("inf")
+    y, y_ok = guarded((c.m, c.n))
+    forward(c, out=y)
+    check(y, *c.y_ref(), "y")
+    u = inner(c)
+    dx, dx_ok = guarded((c.m, c.k))
+    got = grads(c, u=u, dx=dx)
+    for name, g, ref in zip(("dx", "da", "db"), got, c.grad_ref(c.x, u)):
+        check(g, *ref, name)
+    assert y_ok() and dx_ok()
+    if c.adapters == 5:
+        clean = ~torch.isin(c.ids, torch.tensor([1, 2, 3], device="cuda", dtype=torch.int32))
+        assert bool(torch.isfinite(y[clean].float()).all()) and bool(torch.isfinite(dx[clean].float()).all())
+
+
+@pytest.mark.parametrize("m,n,k,bits", [(2600, 2320, 2112, 4), (5200, 1040, 1088, 3)])
+def test_plain_tiles_shared_by_two_blocks(m, n, k, bits):
+    """any4_linear itself: with B = 0 the reference is its own, and so are the bits."""
+    c = Case(m, n, k, 64, bits, 2, 16, "mixed", seed=22)
+    c.b.zero_()
+    y, y_ok = guarded((m, n))
+    a4.any4_linear_bits(bits, c.x, c.packed(), n, k, 64, out=y)
+    check(y, *c.y_ref(), "y")
+    assert y_ok() and bool((forward(c) == y).all())
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Kernels of one call run beside each other; calls still follow each other:
+    every order of short and long calls, forward and backward, on one stream
+    and one workspace, gives what each gives alone."""
+    cases = [Case(40, 272, 512, 128, 4, 3, 16, "mixed", seed=31), Case(700, 1040, 1088, 64, 3, 6, 40, "holes", seed=32),
+             Case(333, 1024, 2048, 128, 4, 5, 8, "mixed", seed=33), Case(2011, 2112, 1024, 64, 4, 1, 16, "null", seed=34),
+             Case(3, 528, 1024, 128, 4, 2, 24, "mixed", seed=35)]
+    packed, us = [c.packed() for c in cases], [inner(c) for c in cases]
+
+    def step(i, ws):
+        c = cases[i]
+        args = (packed[i], *c.shape(), c.a, c.b, c.scale, c.ids)
+        y = a4.any4_linear_lora(c.x, *args, bits=c.bits, workspace=ws)
+        return y, *a4.any4_linear_lora_grad(c.dy, c.x, us[i], *args, bits=c.bits, workspace=ws)
+
+    def space(c, size):
+        return size(c.m, *c.shape(), c.adapters, c.rank, bits=c.bits)
+
+    need = max(max(space(c, a4.any4_lora_workspace_bytes), space(c, a4.any4_lora_grad_workspace_bytes)) for c in cases)
+    alone = []
+    for i in range(len(cases)):
+        alone.append(step(i, torch.zeros(need, dtype=torch.uint8, device="cuda")))
+        torch.cuda.synchronize()
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    order = [i for a in range(len(cases)) for b in range(len(cases)) for i in (a, b)]
+    outs = [step(i, ws) for i in order]
+    torch.cuda.synchronize()
+    for i, out in zip(order, outs):
+        assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(out, alone[i]))
+    assert not bool(ws[:a4.lib.any4_lora_header_bytes()].any())
