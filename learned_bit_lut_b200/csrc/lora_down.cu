@@ -123,6 +123,7 @@ constexpr int kDownTcThreads = 224;
 constexpr int kMaxProductCols = 256;                // adapter columns of one instruction
 constexpr int kDownBar = 1;
 constexpr int kMaxDownSplits = 16;
+constexpr int kNotOwn = -2;                      // instead of an adapter: a token that another group writes
 constexpr int kStageBudget = 104 * 1024;         // a block's stages: two blocks share an SM
 
 struct DownCtl {
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
     }
   } else {
     const int q = warp & 3, row = 32 * q + lane, t = tile * kTileTokens + row;
-    const int mine = t < p.m ? adapter_of(p.ad, t) : -1;
+    const int mine = ctl->id[row];
     const float scale = mine >= 0 ? __ldcg(p.ad.scale + mine) : 0.0f;
     float* part = p.partials + ((size_t)(tile * p.splits + split) * kTileTokens + row) * r16;
     gemm_wait_idle(smem_addr(&ctl->acc_full), 0u, abort_flag, p.status);
@@ -368,47 +369,64 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
     if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  // the last split adds them all in order, four ranks of a token a step
+  // The last split adds them all in order, four ranks of a token a step, two
+  // steps at a time with eight loads each in flight. id[] keeps the adapters of
+  // the tokens that are this group's to write; their scales lie in a stage.
   __threadfence();
-  const int quads = r16 / 4, tokens = min(kTileTokens, p.m - tile * kTileTokens);
-  const float* parts = p.partials + (size_t)tile * p.splits * kTileTokens * r16;
-  for (int i = threadIdx.x; i < tokens * quads; i += kDownTcThreads) {
-    const int tr = i / quads, r0 = (i - tr * quads) * 4, tt = tile * kTileTokens + tr;
-    const int l = adapter_of(p.ad, tt);
-    bool own = l < 0 && group == 0;   // the token is this group's to write
-    for (int j = 0; j < count; ++j) own |= l >= 0 && ctl->slots[j] == l;
-    if (!own) continue;
-    float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (l >= 0) {
-      const float4* src = reinterpret_cast<const float4*>(parts) + i;
+  float* scales = reinterpret_cast<float*>(smem_raw + (sbase - raw));
+  if (threadIdx.x < kTileTokens) {
+    const int l = ctl->id[threadIdx.x];
+    bool own = l < 0 && group == 0;
+    for (int g = 0; g < count; ++g) own |= l >= 0 && ctl->slots[g] == l;
+    ctl->id[threadIdx.x] = own ? l : kNotOwn;
+    scales[threadIdx.x] = own && l >= 0 ? __ldcg(p.ad.scale + l) : 0.0f;
+  }
+  __syncthreads();
+  const int quads = r16 / 4, items = min(kTileTokens, p.m - tile * kTileTokens) * quads;
+  const float4* parts = reinterpret_cast<const float4*>(p.partials + (size_t)tile * p.splits * kTileTokens * r16);
+  for (int i0 = threadIdx.x; i0 < items; i0 += 2 * kDownTcThreads) {
+    int l[2];
+    float4 z[2];
 #pragma unroll
-      for (int s0 = 0; s0 < kMaxDownSplits; s0 += 8) {   // eight loads in flight
-        float4 f[8];
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * kDownTcThreads;
+      l[h] = i < items ? ctl->id[i / quads] : kNotOwn;
+      z[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int s0 = 0; s0 < kMaxDownSplits; s0 += 8) {
+      if (s0 >= p.splits) break;
+      float4 f[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (s0 + q < p.splits) f[q] = __ldcg(src + (size_t)(s0 + q) * kTileTokens * quads);
+          if (l[h] >= 0 && s0 + q < p.splits)
+            f[h][q] = __ldcg(parts + (size_t)(s0 + q) * kTileTokens * quads + i0 + h * kDownTcThreads);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (s0 + q >= p.splits) break;
-          z.x += f[q].x;
-          z.y += f[q].y;
-          z.z += f[q].z;
-          z.w += f[q].w;
-        }
-      }
-      const float sc = __ldcg(p.ad.scale + l);
-      z.x *= sc;
-      z.y *= sc;
-      z.z *= sc;
-      z.w *= sc;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (l[h] >= 0 && s0 + q < p.splits) {
+            z[h].x += f[h][q].x;
+            z[h].y += f[h][q].y;
+            z[h].z += f[h][q].z;
+            z[h].w += f[h][q].w;
+          }
     }
-    uint32_t lo0, lo1;
-    const uint32_t hi0 = split_pair(z.x, z.y, lo0), hi1 = split_pair(z.z, z.w, lo1);
-    uint16_t* row = p.pairs + (size_t)tt * 2 * r16 + r0;
-    *reinterpret_cast<uint2*>(row) = make_uint2(hi0, hi1);
-    *reinterpret_cast<uint2*>(row + r16) = make_uint2(lo0, lo1);
-    if (p.rounded != nullptr && r0 < p.ad.rank)
-      *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) = make_uint2(hi0, hi1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (l[h] == kNotOwn) continue;
+      const int i = i0 + h * kDownTcThreads, tr = i / quads, r0 = (i - tr * quads) * 4, tt = tile * kTileTokens + tr;
+      const float sc = scales[tr];
+      uint32_t lo0, lo1;
+      const uint32_t hi0 = split_pair(z[h].x * sc, z[h].y * sc, lo0), hi1 = split_pair(z[h].z * sc, z[h].w * sc, lo1);
+      uint16_t* row = p.pairs + (size_t)tt * 2 * r16 + r0;
+      *reinterpret_cast<uint2*>(row) = make_uint2(hi0, hi1);
+      *reinterpret_cast<uint2*>(row + r16) = make_uint2(lo0, lo1);
+      if (p.rounded != nullptr && r0 < p.ad.rank)
+        *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) = make_uint2(hi0, hi1);
+    }
   }
   if (threadIdx.x == 0) p.counters[tg] = 0u;   // ready for the next call
   if (outlasts) asm volatile("griddepcontrol.wait;" ::: "memory");
