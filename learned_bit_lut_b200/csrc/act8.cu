@@ -16,8 +16,8 @@
 // NaN and reads back as NaN, so neither is lost in the codes.
 //
 // Both move 3 bytes per value and are bound by HBM, which writes at about half
-// the rate it reads: unpacking 8192 x 14336 (235 MB written) takes 54 us on
-// B200, packing it (235 MB read) 57 us, where a plain copy of as many bytes
+// the rate it reads: unpacking 8192 x 14336 (235 MB written) takes 51 us on
+// B200, packing it (235 MB read) 55 us, where a plain copy of as many bytes
 // takes 56 us; the pack's instructions per value come next, so a lane packs 16
 // values and the group's arithmetic is one multiply and one reciprocal.
 // Groups divide the rows, so the tensor is one flat run of groups. Loads and

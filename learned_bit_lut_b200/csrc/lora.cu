@@ -13,12 +13,19 @@
 // shared memory and share the output rows. The decode kernel is its
 // programmatic dependent, but one of its blocks fills an SM, so it follows
 // rather than overlaps (waiting for the term only before its stores measured
-// the same).
+// the same). B200: 1024 x 4096, one token, rank 16: both kernels 6.7 us back to
+// back (the layer alone 3.1); 4096 x 4096, 16 tokens, rank 16: 14.6 us (the
+// term 6.6); 14336 x 4096, 7 tokens, rank 64: 31 us (the term 12, 9.5 MB of A
+// and B).
 //
 // M > 16: the lists of the adapters in each token tile and u = s x . A^T on
 // the tensor cores (lora_down.cu), then the prefill GEMM with u . B^T as R
 // more columns of its contraction (prefill.cu): y is written once and the
-// term costs R / K of the GEMM and no pass over y of its own.
+// term costs R / K of the GEMM and no pass over y of its own. Lists, u and,
+// where the GEMM reads a dequantized weight, its dequantization run beside each
+// other. B200, any4_linear with and without: 4096 x 4096, 190 tokens, 24
+// adapters of rank 32, 44 and 24 us; 4096 x 14336, 4096 tokens, rank 64, 408
+// and 365 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -16,7 +16,9 @@
 // contraction is split and the last block of a tile's group to arrive adds
 // the others' fp32 partials in order (deterministic). Waiting and issuing
 // cost a block's threads ~1000 cycles a stage, so a stage holds two chunks
-// where it can and two blocks share an SM.
+// where it can and two blocks share an SM. B200: 8192 x 14336 (235 MB), rank 64,
+// 59 us, 4.0 TB/s; 2011 x 4096, rank 16, 17 us, of which launching, the split's
+// partial sums and their join are more than the reading.
 //
 // Warps: 0 = TMA of `in`, 1 = MMA, 2-5 = epilogue, 6 = TMA of the adapters.
 #include <cuda_bf16.h>

@@ -13,6 +13,10 @@
 // src is read once and bounds the work (R <= 64; the rest is small and comes
 // from L2), so x kept in 8 bits halves it: 8 warps turn the codes into the
 // bf16 values they stand for (act8.cuh) on their way into the operand tile.
+// B200: dB of 8192 x 14336 (235 MB), rank 64, 57 us, 4.1 TB/s, and as long
+// without its products or without z: the loads of src bound it; with dA of
+// 8192 x 4096 from codes 74 us; both of 2011 x 4096, rank 16, 20 us, which pass
+// beside dx.
 //
 // For a chunk whose tokens do not all have one adapter the same warps build
 // z's tile: each token's values in the columns of its own adapter, zeros in
