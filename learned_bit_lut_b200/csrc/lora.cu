@@ -14,7 +14,7 @@
 // programmatic dependent, but one of its blocks fills an SM, so it follows
 // rather than overlaps (waiting for the term only before its stores measured
 // the same). B200: 1024 x 4096, one token, rank 16: both kernels 6.7 us back to
-// back (the layer alone 3.1); 4096 x 4096, 16 tokens, rank 16: 14.6 us (the
+// back (the layer alone 3.0); 4096 x 4096, 16 tokens, rank 16: 14.6 us (the
 // term 6.6); 14336 x 4096, 7 tokens, rank 64: 31 us (the term 12, 9.5 MB of A
 // and B).
 //
@@ -25,7 +25,7 @@
 // where the GEMM reads a dequantized weight, its dequantization run beside each
 // other. B200, any4_linear with and without: 4096 x 4096, 190 tokens, 24
 // adapters of rank 32, 44 and 24 us; 4096 x 14336, 4096 tokens, rank 64, 408
-// and 365 us.
+// and 372 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

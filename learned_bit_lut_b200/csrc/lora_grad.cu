@@ -13,7 +13,7 @@
 // (lora_wgrad.cu). Only dx waits, for all before it; the others start beside
 // the one before. Nothing is kept from dx but dx: dA and dB read v, x, dy and
 // u. The product of dx bounds long steps (B200, 8192 tokens, 4096 -> 14336,
-// rank 64: 633 of 795 us, 1.5 PFLOP/s; the GPU is at its power limit), the
+// rank 64: 633 of 816 us, 1.5 PFLOP/s; the GPU is at its power limit), the
 // chain of kernels short ones (333 tokens, 4096 -> 1024: 34 us).
 #include <cuda_runtime.h>
 

@@ -32,7 +32,7 @@
 //
 // Warps of prefill_gemm_kernel: 0 = TMA producer, 1 = MMA issuer (and
 // tensor-memory owner), 2-5 = epilogue (warp w reads tensor-memory lanes
-// 32*(w%4) .. +31). Every mbarrier wait is bounded (~2 s); a timeout sets the
+// 32*(w%4) .. +31), with adapters 6-13 = patching. Every mbarrier wait is bounded (~2 s); a timeout sets the
 // workspace status word and the block winds down.
 #include <cuda.h>
 #include <cuda_bf16.h>
