@@ -301,11 +301,12 @@ def noalloc_status(device: torch.device | None = None) -> int:
     """The status word of any4_linear_noalloc on ``device`` (0: the last call
     completed normally). Synchronizes that device before reading it."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    ptr = _p()
-    _check(lib.any4_noalloc_status_word(ctypes.byref(ptr)))
-    torch.cuda.synchronize(dev)
-    word = torch.as_tensor(_DeviceWord(ptr.value), device=dev)
-    return int(word.view(torch.int32).item()) & 0xFFFFFFFF
+    with torch.cuda.device(dev):
+        ptr = _p()
+        _check(lib.any4_noalloc_status_word(ctypes.byref(ptr)))
+        torch.cuda.synchronize(dev)
+        word = torch.as_tensor(_DeviceWord(ptr.value), device=dev)
+        return int(word.view(torch.int32).item()) & 0xFFFFFFFF
 
 
 def any4_quantize(w: torch.Tensor, ex: torch.Tensor, group: int, bits: int = 4,
