@@ -349,6 +349,8 @@ ANY4_API int any4_pack_format(int format, const uint8_t* idx_nib, const uint16_t
  *
  * u is held in more than bf16 on its way into y (fp32, or a bf16 pair of its
  * leading and trailing part) and y is rounded once from its fp32 sum.
+ * Outputs and the workspace overlap nothing else that the call reads or
+ * writes (ANY4_EINVAL), here and in any4_linear_lora_grad.
  * Results do not depend on how ids order the tokens, and repeat bit for bit.
  */
 ANY4_API size_t any4_lora_header_bytes(void);
@@ -403,6 +405,7 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
  *
  *   x      [M][K] bf16; codes [M][K]; both 16-byte aligned.
  *   steps  [M][K/G] bf16.
+ * Outputs overlap neither the input nor each other (ANY4_EINVAL).
  */
 ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* codes, uint16_t* steps,
                            any4_stream_t stream);

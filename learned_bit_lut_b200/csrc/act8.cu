@@ -213,7 +213,10 @@ ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* c
   if (!any4::act_shape_ok(m, k, group)) return ANY4_ESHAPE;
   if (!any4::aligned16(x) || !any4::aligned16(codes) || (reinterpret_cast<uintptr_t>(steps) & 1)) return ANY4_EALIGN;
   using namespace any4;
-  const size_t runs = (size_t)m * k / 16;
+  const size_t values = (size_t)m * k;
+  const Range ranges[] = {{codes, values}, {steps, values / group * 2}, {x, values * 2}};
+  if (!disjoint(ranges, 2, 3)) return ANY4_EINVAL;
+  const size_t runs = values / 16;
   uint8_t* c = reinterpret_cast<uint8_t*>(codes);
   const cudaError_t e = (reinterpret_cast<uintptr_t>(x) & 31) == 0
                             ? launch_act_pack<true>(x, runs, group, c, steps, (cudaStream_t)stream)
@@ -227,7 +230,10 @@ ANY4_API int any4_act_unpack(const int8_t* codes, const uint16_t* steps, int m, 
   if (!any4::act_shape_ok(m, k, group)) return ANY4_ESHAPE;
   if (!any4::aligned16(x) || !any4::aligned16(codes) || (reinterpret_cast<uintptr_t>(steps) & 1)) return ANY4_EALIGN;
   using namespace any4;
-  const size_t pieces = (size_t)m * k / 8;
+  const size_t values = (size_t)m * k;
+  const Range ranges[] = {{x, values * 2}, {codes, values}, {steps, values / group * 2}};
+  if (!disjoint(ranges, 1, 3)) return ANY4_EINVAL;
+  const size_t pieces = values / 8;
   int shift = 0;
   while ((8 << shift) < group) ++shift;
   const bool many = pieces >= 2 * kActManyRuns;

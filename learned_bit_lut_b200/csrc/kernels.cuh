@@ -37,6 +37,24 @@ bool format_table(int format, uint16_t (&lut)[16]);
 cudaError_t launch_dequant(const uint8_t* packed, const Layout& L, uint16_t* w, cudaStream_t stream,
                            bool beside = false);
 
+// Whether the first `outputs` of `count` ranges overlap no other of them (null
+// ones do not count): an output is written while inputs are still being read.
+struct Range {
+  const void* at;
+  size_t bytes;
+};
+inline bool disjoint(const Range* r, int outputs, int count) {
+  for (int i = 0; i < outputs; ++i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(r[i].at);
+    if (p == 0) continue;
+    for (int j = i + 1; j < count; ++j) {
+      const uintptr_t q = reinterpret_cast<uintptr_t>(r[j].at);
+      if (q != 0 && p < q + r[j].bytes && q < p + r[i].bytes) return false;
+    }
+  }
+  return true;
+}
+
 // The workspace of any4_linear starts with a fixed header of arrival
 // counters (one per possible 32-row panel, so the counters of every shape live
 // in the same zero-filled header whatever the shape of earlier calls; sized for

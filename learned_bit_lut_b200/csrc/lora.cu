@@ -250,6 +250,11 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
   const Adapters ad = {a, b, scale, ids, adapters, rank};
   const LoraSpace space = lora_space(plan, L, m, ad, sms);
   if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
+  const size_t ab = (size_t)adapters * rank * 2;
+  const Range ranges[] = {{y, (size_t)m * n * 2}, {u, (size_t)m * rank * 2}, {workspace, space.total},
+                          {x, (size_t)m * k * 2}, {packed, L.total},         {a, ab * k},
+                          {b, ab * n},            {scale, adapters * sizeof(float)}, {ids, m * sizeof(int32_t)}};
+  if (!disjoint(ranges, 3, sizeof(ranges) / sizeof(ranges[0]))) return ANY4_EINVAL;
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = (cudaStream_t)stream;

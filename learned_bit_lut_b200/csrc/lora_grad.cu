@@ -105,6 +105,22 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
   const Adapters ad = {a, b, scale, ids, adapters, rank};
   const GradSpace space = grad_space(L, m, ad, sms);
   if (workspace_bytes < space.total) return ANY4_EWORKSPACE;
+  const size_t ab = (size_t)adapters * rank * 2, mk = (size_t)m * k;
+  const Range ranges[] = {{dx, mk * 2},
+                          {da, ab * k},
+                          {db, ab * n},
+                          {workspace, space.total},
+                          {dy, (size_t)m * n * 2},
+                          {da ? x : nullptr, mk * 2},
+                          {da ? x_codes : nullptr, mk},
+                          {da && kept8 ? x_steps : nullptr, da && kept8 ? mk / x_group * 2 : 0},
+                          {db ? u : nullptr, (size_t)m * rank * 2},
+                          {dx ? packed : nullptr, L.total},
+                          {dx ? a : nullptr, ab * k},
+                          {b, ab * n},
+                          {scale, adapters * sizeof(float)},
+                          {ids, m * sizeof(int32_t)}};
+  if (!disjoint(ranges, 4, sizeof(ranges) / sizeof(ranges[0]))) return ANY4_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* what = reinterpret_cast<uint16_t*>(ws + space.what);
   uint16_t* pairs = reinterpret_cast<uint16_t*>(ws + space.pairs);

@@ -439,3 +439,65 @@ def test_calls_in_a_row_share_a_workspace():
     for i, out in zip(order, outs):
         assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(out, alone[i]))
     assert not bool(ws[:a4.lib.any4_lora_header_bytes()].any())
+
+
+@pytest.mark.parametrize("shape", [(7, 272, 1024, 128, 4, 3, 64, "mixed"), (190, 1040, 1024, 128, 4, 24, 32, "mixed"),
+                                   (700, 1040, 1088, 64, 3, 6, 40, "holes"), (2011, 2112, 2048, 128, 4, 1, 16, "null"),
+                                   (333, 1024, 4096, 128, 4, 5, 8, "mixed")], ids=str)
+def test_what_follows_on_the_stream_may_overwrite_everything(shape):
+    """The kernels of a call run beside each other, and the call is over for
+    whatever follows it on its stream: inputs, weight and workspace change
+    right behind it, and the results are those of the inputs before."""
+    c = Case(*shape, seed=41)
+    packed, u = c.packed(), inner(c)
+    args = (packed, *c.shape(), c.a, c.b, c.scale, c.ids)
+    need = max(f(c.m, *c.shape(), c.adapters, c.rank, bits=c.bits)
+               for f in (a4.any4_lora_workspace_bytes, a4.any4_lora_grad_workspace_bytes))
+    header = a4.lib.any4_lora_header_bytes()
+    want = (forward(c), *grads(c, u=u))
+    inputs = [t for t in (c.x, c.dy, u, packed, c.a, c.b, c.scale, c.ids) if t is not None]
+    kept = [t.clone() for t in inputs]
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def spoil():
+        for t in inputs:
+            t.view(torch.uint8).fill_(0xFF)
+        ws[header:] = 0xFF
+
+    torch.cuda.synchronize()
+    for _ in range(4):
+        y = a4.any4_linear_lora(c.x, *args, bits=c.bits, workspace=ws)
+        spoil()
+        for t, k in zip(inputs, kept):
+            t.copy_(k)
+        got = a4.any4_linear_lora_grad(c.dy, c.x, u, *args, bits=c.bits, workspace=ws)
+        spoil()
+        for t, k in zip(inputs, kept):
+            t.copy_(k)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip((y, *got), want))
+
+
+def test_overlapping_buffers_are_refused():
+    c = Case(40, 128, 128, 64, 4, 2, 16, "mixed", seed=42)   # N = K: dx fits where dy lies
+    u = inner(c)
+    ws = torch.zeros(a4.any4_lora_grad_workspace_bytes(c.m, *c.shape(), c.adapters, c.rank), dtype=torch.uint8,
+                     device="cuda")
+
+    def refused(call):
+        with pytest.raises(a4.Any4Error) as e:
+            call()
+        assert e.value.status == a4.ANY4_EINVAL
+
+    inside = ws[-2 * c.m * c.n:].view(torch.bfloat16).view(c.m, c.n)   # in the workspace
+    for bad in (dict(dx=c.dy), dict(dx=c.x), dict(da=c.a), dict(db=c.b), dict(dx=inside)):
+        refused(lambda: grads(c, u=u, workspace=ws, **bad))
+    refused(lambda: forward(c, out=c.x))
+    own = torch.zeros(a4.any4_lora_workspace_bytes(c.m, *c.shape(), c.adapters, c.rank), dtype=torch.uint8, device="cuda")
+    refused(lambda: forward(c, out=own[-2 * c.m * c.n:].view(torch.bfloat16).view(c.m, c.n), workspace=own))
+    refused(lambda: forward(c, u=c.x[:, :16].contiguous(), out=c.x))
+    # what the call does not read may be written: x without dA
+    want = grads(c, u=u)
+    x = c.x.clone()
+    dx, da, db = grads(c, kept=x, u=u, dx=x, outputs=("dx", "db"))
+    assert da is None and torch.equal(dx, want[0]) and torch.equal(db, want[2])

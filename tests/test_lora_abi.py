@@ -80,6 +80,15 @@ def test_checkpoint_refusals():
     assert unpack(P, ctypes.c_void_p(4097), 4, 128, 64, P, None) == a4.ANY4_EALIGN
 
 
+def test_checkpoint_refuses_overlapping_buffers():
+    x, codes, steps, near = (ctypes.c_void_p(v) for v in (1 << 20, 2 << 20, 3 << 20, (1 << 20) + 4 * 128 * 2 - 16))
+    pack, unpack = a4.lib.any4_act_pack, a4.lib.any4_act_unpack
+    for c, s in ((x, steps), (near, steps), (codes, near), (codes, codes)):
+        assert pack(x, 4, 128, 64, c, s, None) == a4.ANY4_EINVAL
+    for c, s in ((x, steps), (near, steps), (codes, near)):
+        assert unpack(c, s, 4, 128, 64, x, None) == a4.ANY4_EINVAL
+
+
 def test_binding_refuses_tensors_of_the_host():
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
