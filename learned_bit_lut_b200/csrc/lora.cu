@@ -15,7 +15,7 @@
 // rather than overlaps (waiting for the term only before its stores measured
 // the same). B200: 1024 x 4096, one token, rank 16: both kernels 6.7 us back to
 // back (the layer alone 3.0); 4096 x 4096, 16 tokens, rank 16: 14.6 us (the
-// term 6.6); 14336 x 4096, 7 tokens, rank 64: 31 us (the term 12, 9.5 MB of A
+// term 6.6); 14336 x 4096, 7 tokens, rank 64: 28 us (the term 9, 9.5 MB of A
 // and B).
 //
 // M > 16: the lists of the adapters in each token tile and u = s x . A^T on
@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/any4.h"
@@ -64,9 +65,18 @@ __device__ __forceinline__ uint16_t bf16_of(float v) {
 // delta[t][n] = sum_r u[r] B_l[n][r], R / 8 lanes per output row, 16 bytes
 // each: a warp reads consecutive rows whole (a thread per row took 3 times as
 // long over a kernel's 4 KB strides of 16-byte pieces).
-__global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint16_t* __restrict__ x, const Adapters ad,
-                                                                      int n, int k, float* __restrict__ delta,
-                                                                      uint16_t* __restrict__ u) {
+//
+// AHEAD: the next steps' rows of B are under way while the ones before are
+// summed, the first from the start; with the registers that takes, a block has
+// an SM to itself. For as many clusters as the GPU then holds at once (B200:
+// 14336 x 4096, 7 tokens, rank 64, 14 clusters, with the layer 28.2 us against
+// 31.0); more of them share SMs (4096 x 4096, 16 tokens, 16 clusters, 14.6 us
+// against 15.4).
+template <bool AHEAD>
+__global__ void __launch_bounds__(kDeltaThreads, AHEAD ? 1 : 0) adapter_delta_kernel(const uint16_t* __restrict__ x,
+                                                                                     const Adapters ad, int n, int k,
+                                                                                     float* __restrict__ delta,
+                                                                                     uint16_t* __restrict__ u) {
   __shared__ float part[kDeltaWarps][kMaxRank / kDeltaCluster];
   __shared__ __align__(16) float us[kMaxRank];
   const int rank = blockIdx.x, t = blockIdx.y, slice = blockIdx.z;
@@ -81,13 +91,25 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
   const int first = ((slice * kDeltaCluster + rank) * kDeltaWarps + warp) * per_warp + lane / parts;
   const bool works = lane < per_warp * parts;
   const uint16_t* brow = ad.b + ((size_t)(l < 0 ? 0 : l) * n + first) * ad.rank + 8 * part_of;
-  const size_t b_step = (size_t)warps * per_warp * ad.rank;
+  const int row_step = warps * per_warp;
+  const size_t b_step = (size_t)row_step * ad.rank;
+  auto load_b = [&](uint4 (&q)[4], const uint16_t* b, int row) {   // four steps' loads in flight
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (l >= 0 && works && row + i * row_step < n) q[i] = __ldcg(reinterpret_cast<const uint4*>(b + i * b_step));
+    }
+  };
+  [[maybe_unused]] uint4 next[4];
+  const float scale = AHEAD && l >= 0 ? __ldcg(ad.scale + l) : 0.0f;
+  if (AHEAD)
+    load_b(next, brow, first);
+  else if (l >= 0 && works && first < n)   // its first rows of B towards L2 while phase 1 runs
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(brow));
   if (l >= 0) {
-    // its first rows of B towards L2 while phase 1 runs
-    if (works && first < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(brow));
     const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * k);
     const uint4* ar = reinterpret_cast<const uint4*>(ad.a + ((size_t)l * ad.rank + rank) * k);
-    const size_t row_step = (size_t)kDeltaCluster * (k / 8);
+    const size_t a_step = (size_t)kDeltaCluster * (k / 8);
     for (int i0 = 0; i0 < rows; i0 += 8) {   // 8 rows' loads in flight
       float acc[8] = {};
       for (int c = threadIdx.x; c < k / 8; c += kDeltaThreads) {   // 16-byte pieces of a row
@@ -95,7 +117,7 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
         uint4 av[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i0 + i < rows) av[i] = __ldcg(ar + (i0 + i) * row_step + c);
+          if (i0 + i < rows) av[i] = __ldcg(ar + (i0 + i) * a_step + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i0 + i < rows) acc[i] = dot8(av[i], xv, acc[i]);
@@ -117,7 +139,7 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
     if (l >= 0) {
 #pragma unroll
       for (int w = 0; w < kDeltaWarps; ++w) v += part[w][i];
-      v *= __ldcg(ad.scale + l);
+      v *= AHEAD ? scale : __ldcg(ad.scale + l);
     }
     const uint32_t dst = cluster_map((uint32_t)__cvta_generic_to_shared(&us[r]), (uint32_t)peer);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
@@ -128,12 +150,14 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
 #pragma unroll
   for (int i = 0; i < 8; ++i) uv[i] = us[8 * part_of + i];
   float* out = delta + (size_t)t * n;
-  for (int row = first; row - lane / parts < n; row += 4 * warps * per_warp, brow += 4 * b_step) {
-    uint4 q[4];   // four steps' loads in flight
+  for (int row = first; row - lane / parts < n; row += 4 * row_step, brow += 4 * b_step) {
+    uint4 q[4];
+    if (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (l >= 0 && works && row + i * warps * per_warp < n) q[i] = __ldcg(reinterpret_cast<const uint4*>(brow + i * b_step));
+      for (int i = 0; i < 4; ++i) q[i] = next[i];
+      load_b(next, brow + 4 * b_step, row + 4 * row_step);
+    } else {
+      load_b(q, brow, row);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -149,10 +173,39 @@ __global__ void __launch_bounds__(kDeltaThreads) adapter_delta_kernel(const uint
         const float v = __shfl_down_sync(0xFFFFFFFFu, acc, d);
         if (part_of + d < parts) acc += v;
       }
-      const int at = row + i * warps * per_warp;
+      const int at = row + i * row_step;
       if (works && part_of == 0 && at < n) out[at] = acc;
     }
   }
+}
+
+// How many clusters of adapter_delta_kernel<true> the current device holds at once.
+cudaError_t delta_clusters(int* count) {
+  static std::atomic<int> known[64];   // 0: not asked yet, else the number + 1
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int have = known[dev].load(std::memory_order_relaxed);
+  if (have == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kDeltaCluster);
+    cfg.blockDim = dim3(kDeltaThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kDeltaCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, adapter_delta_kernel<true>, &cfg);
+    if (e != cudaSuccess) return e;
+    have = n + 1;
+    known[dev].store(have, std::memory_order_relaxed);
+  }
+  *count = have - 1;
+  return cudaSuccess;
 }
 
 cudaError_t launch_delta(const uint16_t* x, const Adapters& ad, int m, int n, int k, float* delta, uint16_t* u,
@@ -162,6 +215,9 @@ cudaError_t launch_delta(const uint16_t* x, const Adapters& ad, int m, int n, in
   const int per_pass = kDeltaCluster * kDeltaWarps * (32 / (ad.rank / 8)) * 4, most = (n + per_pass - 1) / per_pass;
   int slices = num_sms / (kDeltaCluster * m);
   slices = slices < 1 ? 1 : slices > most ? most : slices;
+  int at_once = 0;
+  const cudaError_t e = delta_clusters(&at_once);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kDeltaCluster, (unsigned)m, (unsigned)slices);
   cfg.blockDim = dim3(kDeltaThreads);
@@ -175,7 +231,8 @@ cudaError_t launch_delta(const uint16_t* x, const Adapters& ad, int m, int n, in
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, adapter_delta_kernel, x, ad, n, k, delta, u);
+  return m * slices <= at_once ? cudaLaunchKernelEx(&cfg, adapter_delta_kernel<true>, x, ad, n, k, delta, u)
+                               : cudaLaunchKernelEx(&cfg, adapter_delta_kernel<false>, x, ad, n, k, delta, u);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
