@@ -56,7 +56,8 @@ constexpr int kGemmThreads = 192;
 constexpr int kOutWarpBytes = 32 * 64;         // an epilogue warp's 32 rows of 32 tokens, [token][row]
 constexpr int kOutBytes = 4 * kOutWarpBytes;
 constexpr int kListBytes = 4352;               // a split's own adapter stages
-constexpr int kPatchThreads = 256;             // with adapters: 8 warps more
+constexpr int kPatchThreads = 256;             // with adapters: 8 warps more,
+constexpr int kPatchGroup = 128;               // 4 for the even stages and 4 for the odd ones
 
 // BN tokens per tile (MMA N): 256, or 64 and 128 for the gradient of few tokens.
 // PAIR: two blocks share a tile of 256 rows, each with half of its tokens.
@@ -211,6 +212,8 @@ struct Extra {
   int rank0, zcol, steps;   // first rank column, column of the pairs, 16-deep steps
   bool both;                // leading and trailing part in one stage
 };
+// 16-byte pieces of z's rows that the stage's products read
+__device__ __forceinline__ int z_pieces(const Extra& ex) { return (ex.both ? 4 : 2) * ex.steps; }
 __device__ __forceinline__ int extra_stages(int r16) { return r16 <= 32 ? 1 : (r16 + 63) / 64 * 2; }   // per adapter
 __device__ __forceinline__ Extra extra_stage(int r16, int h) {
   if (r16 <= 32) return {0, 0, r16 / 16, true};
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       mbar_init(smem_addr(&ctl->listed), 1);
       for (int s = 0; s < kStages; ++s) {
         mbar_init(smem_addr(&ctl->raw[s]), 1);
-        mbar_init(smem_addr(&ctl->patched[s]), kPatchThreads / 32 + (PAIR && peer == 0));
+        mbar_init(smem_addr(&ctl->patched[s]), kPatchGroup / 32 + (PAIR && peer == 0));
       }
       for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
     }
@@ -567,7 +570,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
   } else if (LORA && warp >= 6) {
     // ---------------------------------------------------------- patching
     if constexpr (LORA) {
-      const int thread = threadIdx.x - kGemmThreads;
+      // A group's warps patch a stage while the other group's wait for or finish
+      // theirs (64 mixed adapters of rank 72, 986 tokens: the gradients 343 -> 321 us).
+      const int thread = (threadIdx.x - kGemmThreads) % kPatchGroup, odd = (threadIdx.x - kGemmThreads) / kPatchGroup;
+      static_assert(kStages % 2 == 0, "a stage has its group");
       int it = 0, tcount = 0;
       uint32_t raw_phase = 0;
       for (int u = u_first; u < units && !*abort_flag; u += u_step, ++tcount) {
@@ -580,30 +586,31 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         if (splits > 1 && !__all_sync(0xFFFFFFFFu, gemm_wait_idle(smem_addr(&ctl->listed), 0u, abort_flag, status))) break;
         const StageList list = stage_list(lora, mt, splits > 1, own);
         if (list.head.mixed) {
-          constexpr int kOwn = (kBTokens + kPatchThreads - 1) / kPatchThreads;   // this thread's token rows
+          constexpr int kOwn = (kBTokens + kPatchGroup - 1) / kPatchGroup;   // this thread's token rows
           int id[kOwn];
 #pragma unroll
           for (int i = 0; i < kOwn; ++i) {
-            const int row = thread + i * kPatchThreads, t = m0 + row;
+            const int row = thread + i * kPatchGroup, t = m0 + row;
             id[i] = row < kBTokens && t < m ? adapter_of(lora.ad, t) : -1;
           }
           bool ok = true;
-          int l_next = list.count > 0 ? list.adapter(0) : 0;
-          for (int e = 0; e < list.count; ++e) {
+          const int e_first = (it + odd) & 1;   // its stages are the even or the odd ones
+          int l_next = e_first < list.count ? list.adapter(e_first) : 0;
+          for (int e = e_first; e < list.count; e += 2) {
             const int s = (it + e) % kStages;
             const int l = l_next;
-            if (e + 1 < list.count) l_next = list.adapter(e + 1);
+            if (e + 2 < list.count) l_next = list.adapter(e + 2);
             // the first one comes at the end of the tile's main loop
             const uint32_t rb = smem_addr(&ctl->raw[s]), rp = (raw_phase >> s) & 1u;
-            ok = __all_sync(0xFFFFFFFFu, e == 0 ? gemm_wait_idle(rb, rp, abort_flag, status)
-                                                 : gemm_wait(rb, rp, abort_flag, status));
+            ok = __all_sync(0xFFFFFFFFu, e == e_first ? gemm_wait_idle(rb, rp, abort_flag, status)
+                                                      : gemm_wait(rb, rp, abort_flag, status));
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
-            if (patch_tile<TRANS, kPatchThreads>(sa(s), extra_stage(lora.r16, list.part(e)).steps, thread))
-              *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            const Extra ex = extra_stage(lora.r16, list.part(e));
+            if (patch_tile<TRANS, kPatchGroup>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
-              if (thread + i * kPatchThreads < kBTokens && id[i] != l) zero_row(sb(s), thread + i * kPatchThreads);
+              if (thread + i * kPatchGroup < kBTokens && id[i] != l) zero_row(sb(s), thread + i * kPatchGroup, z_pieces(ex));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));
@@ -912,9 +919,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             if (!mixed) continue;
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
-            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), extra_stage(lora.r16, list.part(e)).steps, thread))
-              *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
-            if (thread < BN && id != l) zero_row(sb(s), thread);
+            const Extra ex = extra_stage(lora.r16, list.part(e));
+            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (thread < BN && id != l) zero_row(sb(s), thread, z_pieces(ex));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&ctl->patched[s]));

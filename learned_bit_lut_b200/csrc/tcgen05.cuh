@@ -297,12 +297,13 @@ __device__ __forceinline__ bool patch_finite(uint32_t addr) {
   return found;
 }
 
-// Zeroes row `row` (128 bytes) of a tile at addr; neighbouring threads take
-// neighbouring rows, so the pieces go in the swizzle's order, which keeps 8
-// rows on different banks.
-__device__ __forceinline__ void zero_row(uint32_t addr, int row) {
+// Zeroes the first `pieces` 16-byte pieces of row `row` (128 bytes) of a tile
+// at addr; neighbouring threads take neighbouring rows, so the pieces go in the
+// swizzle's order, which keeps 8 rows on different banks.
+__device__ __forceinline__ void zero_row(uint32_t addr, int row, int pieces = 8) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) sts128(addr + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)), 0u, 0u, 0u, 0u);
+  for (int c = 0; c < 8; ++c)
+    if (c < pieces) sts128(addr + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)), 0u, 0u, 0u, 0u);
 }
 
 // bf16 matrix of rows x cols (row-major) as 2-D boxes of box_rows x 64
