@@ -501,3 +501,40 @@ def test_overlapping_buffers_are_refused():
     x = c.x.clone()
     dx, da, db = grads(c, kept=x, u=u, dx=x, outputs=("dx", "db"))
     assert da is None and torch.equal(dx, want[0]) and torch.equal(db, want[2])
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import learned_bit_lut_b200 as a4
+from lora_util import Case
+c = Case({m}, 528, 1024, 128, 4, 3, 16, "mixed", seed=51)
+p, args = c.packed(), (*c.shape(), c.a, c.b, c.scale, c.ids)
+u = torch.empty(c.m, c.rank, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = a4.any4_linear_lora(c.x, p, *args, u=u)
+    kept = a4.any4_act_pack(c.x, 128)
+    x = a4.any4_act_unpack(*kept, 128)
+    g = a4.any4_linear_lora_grad(c.dy, kept, u, p, *args)
+graph.replay()
+torch.cuda.synchronize()
+again = a4.any4_linear_lora(c.x, p, *args), x, *a4.any4_linear_lora_grad(c.dy, x, u, p, *args)
+assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip((y, x, *g), again))
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("m", [2, 100, 700])
+def test_first_call_of_a_process_is_captured(m):
+    """What a call asks the driver once (sizes, how many clusters fit) may be
+    asked while a graph is being captured."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests, m=m)
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
