@@ -71,7 +71,10 @@ struct GemmCfg {
 };
 constexpr int kBN = 256;
 constexpr int kMaxStages = 6;
-constexpr int kBand = 8;   // token tiles side by side, pairs of blocks
+// Token tiles side by side, pairs of blocks (B200, long runs, bands of 4, 8 and
+// 16: 8192 tokens through 14336 x 4096 812, 769, 754 us, its dx 856, 843, 855
+// us; 4096 tokens through 4096 x 14336 433, 426, 432 us).
+constexpr int kBand = 8;
 
 struct alignas(1024) GemmCtl {
   uint64_t full[kMaxStages];
