@@ -71,6 +71,12 @@ struct GemmCfg {
 };
 constexpr int kBN = 256;
 constexpr int kMaxStages = 6;
+// Tiles whose `spoilt` flags are apart. While the epilogue is at tile T, the
+// products of T + 2 wait for its accumulator, and every stage may hold a chunk
+// of T + 2 or later: with a chunk and one adapter stage or none a tile, patching
+// is as far as tile T + kMaxStages.
+constexpr int kSpoiltTiles = 8;
+static_assert(kSpoiltTiles >= kMaxStages + 2, "a tile's flag is read and cleared before another tile's patching sets it");
 // Token tiles side by side, pairs of blocks (B200, long runs, bands of 4, 8 and
 // 16: 8192 tokens through 14336 x 4096 812, 769, 754 us, its dx 856, 843, 855
 // us; 4096 tokens through 4096 x 14336 433, 426, 432 us).
@@ -87,7 +93,8 @@ struct alignas(1024) GemmCtl {
   uint32_t tmem_base;
   int abort_flag;
   int last_split;   // epilogue: this block finishes the tile's split-K sum
-  int spoilt[4];    // tile tcount & 3: an adapter's infinities or NaN were taken out
+  int spoilt[kSpoiltTiles];   // tile tcount % kSpoiltTiles: an adapter's infinities or NaN were taken out
+  int tile_spoilt[2];         // that of the tile at work, as one thread of the epilogue read it
 };
 
 static_assert(sizeof(GemmCtl) == 1024, "control block");
@@ -100,6 +107,17 @@ constexpr int kMaxExtraSplits = 8;              // the same where adapters' stag
 
 __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync %0, 128;" ::"n"(kEpilogueBar) : "memory");
+}
+
+// One thread of the epilogue, when the tile's products are done: reads its
+// `spoilt` flag and clears it for tile tcount + kSpoiltTiles. All four warps act
+// on the copy (so none takes another branch than the others), which is written
+// again two tiles and an epilogue_sync() later.
+template <typename Ctl>
+__device__ __forceinline__ void take_spoilt(Ctl* ctl, int tcount) {
+  volatile int* flag = &ctl->spoilt[tcount % kSpoiltTiles];
+  *(volatile int*)&ctl->tile_spoilt[tcount & 1] = *flag;
+  *flag = 0;
 }
 
 // 32 tokens from m0 on of an epilogue warp's 32 output rows (row0 on): v[i] is
@@ -389,7 +407,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
         mbar_init(smem_addr(&ctl->raw[s]), 1);
         mbar_init(smem_addr(&ctl->patched[s]), kPatchGroup / 32 + (PAIR && peer == 0));
       }
-      for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
+      for (int i = 0; i < kSpoiltTiles; ++i) ctl->spoilt[i] = 0;
     }
     ctl->abort_flag = 0;
     ctl->last_split = 0;
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
             if (!ok) break;   // the whole warp leaves
             raw_phase ^= 1u << s;
             const Extra ex = extra_stage(lora.r16, list.part(e));
-            if (patch_tile<TRANS, kPatchGroup>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (patch_tile<TRANS, kPatchGroup>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount % kSpoiltTiles] = 1;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
               if (thread + i * kPatchGroup < kBTokens && id[i] != l) zero_row(sb(s), thread + i * kPatchGroup, z_pieces(ex));
@@ -643,11 +661,13 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
       gemm_wait(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
+      if constexpr (LORA)
+        if (q == 0 && lane == 0) take_spoilt(ctl, tcount);
       epilogue_sync();          // all four warps leave together if any wait gave up
       if (*abort_flag) break;
       tc_fence_after();
       [[maybe_unused]] int spoilt = 0;
-      if constexpr (LORA) spoilt = *(volatile int*)&ctl->spoilt[tcount & 3];
+      if constexpr (LORA) spoilt = ctl->tile_spoilt[tcount & 1];
       const int r = 32 * q + lane, row = nt * kBM + r;
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * BN;
       float* part = partials + (size_t)u * kPartialFloats;   // [token][row] of this split
@@ -670,11 +690,6 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
           store_rows(y, v, m0, m, nt * kBM + 32 * q, n, out, wide, lane);
         }
       }
-      if constexpr (LORA)
-        if (spoilt) {   // all four warps have read it
-          epilogue_sync();
-          if (q == 0 && lane == 0) *(volatile int*)&ctl->spoilt[tcount & 3] = 0;
-        }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -749,8 +764,10 @@ struct alignas(1024) FusedCtl {
   uint32_t tmem_base;
   int abort_flag;
   int last_split;
-  int spoilt[4];
+  int spoilt[kSpoiltTiles];
+  int tile_spoilt[2];
 };
+static_assert(kFusedStages <= kMaxStages, "kSpoiltTiles");
 
 struct FusedParams {
   const uint8_t* packed;
@@ -796,7 +813,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     if (LORA) {
       mbar_init(smem_addr(&ctl->listed), 1);
       for (int s = 0; s < kFusedStages; ++s) mbar_init(smem_addr(&ctl->patched[s]), kFusedDecoders);
-      for (int i = 0; i < 4; ++i) ctl->spoilt[i] = 0;
+      for (int i = 0; i < kSpoiltTiles; ++i) ctl->spoilt[i] = 0;
     }
     ctl->abort_flag = 0;
     ctl->last_split = 0;
@@ -923,7 +940,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, gemm_wait(smem_addr(&ctl->full[s]), ph, abort_flag, status));
             if (!ok) break;
             const Extra ex = extra_stage(lora.r16, list.part(e));
-            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount & 3] = 1;
+            if (patch_tile<false, 32 * kFusedDecoders>(sa(s), ex.steps, thread)) *(volatile int*)&ctl->spoilt[tcount % kSpoiltTiles] = 1;
             if (thread < BN && id != l) zero_row(sb(s), thread, z_pieces(ex));
             fence_proxy_async_smem();
             __syncwarp();
@@ -1040,11 +1057,13 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
       gemm_wait_idle(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
+      if constexpr (LORA)
+        if (q == 0 && lane == 0) take_spoilt(ctl, tcount);
       epilogue_sync();
       if (*abort_flag) break;
       tc_fence_after();
       [[maybe_unused]] int spoilt = 0;
-      if constexpr (LORA) spoilt = *(volatile int*)&ctl->spoilt[tcount & 3];
+      if constexpr (LORA) spoilt = ctl->tile_spoilt[tcount & 1];
       const int r = 32 * q + lane, row = nt * kBM + r;
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * BN;
       float* part = partials + (size_t)u * kPartialFloats;
@@ -1067,11 +1086,6 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
           store_rows(y, v, m0, m, nt * kBM + 32 * q, n, out, wide, lane);
         }
       }
-      if constexpr (LORA)
-        if (spoilt) {   // all four warps have read it
-          epilogue_sync();
-          if (q == 0 && lane == 0) *(volatile int*)&ctl->spoilt[tcount & 3] = 0;
-        }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_one(smem_addr(&ctl->acc_empty[b]));
