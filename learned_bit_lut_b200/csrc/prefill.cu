@@ -94,7 +94,8 @@ struct alignas(1024) GemmCtl {
   int abort_flag;
   int last_split;   // epilogue: this block finishes the tile's split-K sum
   int spoilt[kSpoiltTiles];   // tile tcount % kSpoiltTiles: an adapter's infinities or NaN were taken out
-  int tile_spoilt[2];         // that of the tile at work, as one thread of the epilogue read it
+  int tile_spoilt[2];         // that of the tile at work, and whether its wait gave up, as one thread of the
+  int tile_leave[2];          // epilogue saw them
 };
 
 static_assert(sizeof(GemmCtl) == 1024, "control block");
@@ -109,15 +110,21 @@ __device__ __forceinline__ void epilogue_sync() {
   asm volatile("bar.sync %0, 128;" ::"n"(kEpilogueBar) : "memory");
 }
 
-// One thread of the epilogue, when the tile's products are done: reads its
-// `spoilt` flag and clears it for tile tcount + kSpoiltTiles. All four warps act
-// on the copy (so none takes another branch than the others), which is written
-// again two tiles and an epilogue_sync() later.
-template <typename Ctl>
-__device__ __forceinline__ void take_spoilt(Ctl* ctl, int tcount) {
-  volatile int* flag = &ctl->spoilt[tcount % kSpoiltTiles];
-  *(volatile int*)&ctl->tile_spoilt[tcount & 1] = *flag;
-  *flag = 0;
+// One thread of the epilogue, once its wait for the tile's products is over:
+// what all four warps act on, so that none takes another branch (and another
+// number of barriers) than the others. A warp that reads the abort flag for
+// itself may leave alone, and the others wait for it without end. If this
+// thread saw the products done, the others' waits see it too. Reads the tile's
+// `spoilt` flag and clears it for tile tcount + kSpoiltTiles. The copies are
+// written again two tiles and an epilogue_sync() later.
+template <bool LORA, typename Ctl>
+__device__ __forceinline__ void take_tile(Ctl* ctl, int tcount, bool leave) {
+  *(volatile int*)&ctl->tile_leave[tcount & 1] = leave;
+  if (LORA) {
+    volatile int* flag = &ctl->spoilt[tcount % kSpoiltTiles];
+    *(volatile int*)&ctl->tile_spoilt[tcount & 1] = *flag;
+    *flag = 0;
+  }
 }
 
 // 32 tokens from m0 on of an epilogue warp's 32 output rows (row0 on): v[i] is
@@ -660,11 +667,10 @@ __global__ void __launch_bounds__(kGemmThreads + (std::is_same<X, LoraArgs>::val
       nt = nt * kPeers + peer;
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
-      gemm_wait(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
-      if constexpr (LORA)
-        if (q == 0 && lane == 0) take_spoilt(ctl, tcount);
-      epilogue_sync();          // all four warps leave together if any wait gave up
-      if (*abort_flag) break;
+      const bool done = gemm_wait(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
+      if (q == 0 && lane == 0) take_tile<LORA>(ctl, tcount, !done || *abort_flag);
+      epilogue_sync();
+      if (ctl->tile_leave[tcount & 1]) break;   // all four warps
       tc_fence_after();
       [[maybe_unused]] int spoilt = 0;
       if constexpr (LORA) spoilt = ctl->tile_spoilt[tcount & 1];
@@ -765,7 +771,7 @@ struct alignas(1024) FusedCtl {
   int abort_flag;
   int last_split;
   int spoilt[kSpoiltTiles];
-  int tile_spoilt[2];
+  int tile_spoilt[2], tile_leave[2];
 };
 static_assert(kFusedStages <= kMaxStages, "kSpoiltTiles");
 
@@ -1056,11 +1062,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       const int nt = tile / m_tiles, mt = tile % m_tiles;
       const int b = tcount & 1;
       const uint32_t ph = (uint32_t)(tcount >> 1) & 1u;
-      gemm_wait_idle(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
-      if constexpr (LORA)
-        if (q == 0 && lane == 0) take_spoilt(ctl, tcount);
+      const bool done = gemm_wait_idle(smem_addr(&ctl->acc_full[b]), ph, abort_flag, status);
+      if (q == 0 && lane == 0) take_tile<LORA>(ctl, tcount, !done || *abort_flag);
       epilogue_sync();
-      if (*abort_flag) break;
+      if (ctl->tile_leave[tcount & 1]) break;   // all four warps
       tc_fence_after();
       [[maybe_unused]] int spoilt = 0;
       if constexpr (LORA) spoilt = ctl->tile_spoilt[tcount & 1];
