@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kDeltaThreads, AHEAD ? 1 : 0) adapter_delta_ke
   __shared__ __align__(16) float us[kMaxRank];
   const int rank = blockIdx.x, t = blockIdx.y, slice = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the peers' shared memory may be written once they have all started
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int l = adapter_of(ad, t);
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kDeltaThreads, AHEAD ? 1 : 0) adapter_delta_ke
     }
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // they have
   // thread (peer, i): the block's sum i into peer's us[8 i + rank]
   if (threadIdx.x < kDeltaCluster * rows) {
     const int peer = threadIdx.x / rows, i = threadIdx.x % rows, r = kDeltaCluster * i + rank;

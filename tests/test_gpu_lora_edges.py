@@ -75,3 +75,16 @@ def test_short_tiles_of_the_forward_with_spoilt_adapters(m, n):
         y = forward(c, workspace=ws)
         assert status(ws) == 0
         check(y, *c.y_ref(), "y")
+
+
+# ---- decoding tokens without an adapter: their clusters have nothing to sum, so
+# their blocks exchange at once, while others of the cluster may not have started
+
+@pytest.mark.parametrize("order", ["nobody", "holes"])
+def test_decode_tokens_without_an_adapter_in_a_row(order):
+    c = Case(16, 4096, 1024, 128, 4, 3, 128, order, seed=63)
+    packed = c.packed()
+    ref = c.y_ref()
+    outs = [a4.any4_linear_lora(c.x, packed, *c.shape(), c.a, c.b, c.scale, c.ids) for _ in range(200)]
+    check(outs[0], *ref, "y")
+    assert all(torch.equal(y, outs[0]) for y in outs)

@@ -20,3 +20,18 @@ def test_warps_that_share_a_barrier_leave_together(path):
     """Behind a barrier of some warps, none decides by a flag that other warps
     may set meanwhile: a warp that leaves alone keeps the next barrier waiting."""
     assert not re.search(r"_sync\(\);\s*if \(\*abort(_flag)?\)", code(path))
+
+
+@pytest.mark.parametrize("path", [p for p in SOURCES if p.endswith(".cu")], ids=os.path.basename)
+def test_blocks_of_a_cluster_have_started_before_they_are_written_to(path):
+    """Shared memory of another block is there once that block has started, which
+    only a cluster barrier tells: each kernel has one before its first store
+    into another block or arrival at one."""
+    text = code(path)
+    cuts = [m.start() for m in re.finditer(r"__global__", text)] + [len(text)]
+    for kernel in (text[a:b] for a, b in zip(cuts, cuts[1:])):
+        remote = re.search(r"st\.shared::cluster|st_async_v4\(|mbar_arrive_leader\(", kernel)
+        if remote is None:
+            continue
+        started = r"block_sync\(\);" if "block_sync = " in kernel else r"barrier\.cluster\.wait|cluster_sync(_init)?\(\);"
+        assert re.search(started, kernel[:remote.start()]), kernel[:80]
