@@ -267,13 +267,14 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const uint8
   const uint4* lsec = reinterpret_cast<const uint4*>(packed + L.lut_off) + (size_t)P * kPanelRows * 2;
   const uint4* asec = reinterpret_cast<const uint4*>(packed + L.ab_off) + (size_t)P * L.groups * 8 + g;
   const int gshift = __ffs(L.g) - 1;   // G is a power of two
+  // The weight is there (any kernel may have written it last), w is free, and a
+  // dependent may launch, from here on. A launch beside the one before it has
+  // all that already, and its last block ends after that one.
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Planes T[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) T[r] = to_planes(ld_nc_v4(lsec + (g + 8 * r) * 2), ld_nc_v4(lsec + (g + 8 * r) * 2 + 1));
-  // the packed weight is immutable; w is free, and a dependent may launch, from
-  // here on. Beside the kernel launched before it, the last block ends after it.
-  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 2
   for (int c = c0; c < min(c0 + chunks, L.kchunks); ++c) {
     const uint8_t* chunk = packed + L.w_off + ((size_t)P * L.kchunks + c) * L.chunk_bytes;

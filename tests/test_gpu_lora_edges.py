@@ -88,3 +88,21 @@ def test_decode_tokens_without_an_adapter_in_a_row(order):
     outs = [a4.any4_linear_lora(c.x, packed, *c.shape(), c.a, c.b, c.scale, c.ids) for _ in range(200)]
     check(outs[0], *ref, "y")
     assert all(torch.equal(y, outs[0]) for y in outs)
+
+
+# ---- the dequantized weight right behind whatever wrote the packed one
+
+@pytest.mark.parametrize("bits", [4, 3, 2])
+def test_dequantization_follows_a_copy_of_the_weight(bits):
+    one, two = (Case(8, 1024, 1024, 128, bits, 1, 8, "null", seed=s).packed() for s in (64, 65))
+    wants = [a4.any4_dequant_bits(bits, p, 1024, 1024, 128) for p in (one, two)]
+    x = torch.randn(600, 1024, device="cuda").to(torch.bfloat16)
+    ys = [a4.any4_linear_bits(bits, x, p, 1024, 1024, 128) for p in (one, two)]
+    torch.cuda.synchronize()
+    packed, outs = one.clone(), []
+    for i in range(60):
+        packed.copy_((one, two)[i % 2])
+        outs.append((a4.any4_dequant_bits(bits, packed, 1024, 1024, 128) if i % 4 < 2 else
+                     a4.any4_linear_bits(bits, x, packed, 1024, 1024, 128)))
+    for i, out in enumerate(outs):
+        assert torch.equal(out, (wants if i % 4 < 2 else ys)[i % 2])

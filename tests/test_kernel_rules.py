@@ -35,3 +35,11 @@ def test_blocks_of_a_cluster_have_started_before_they_are_written_to(path):
             continue
         started = r"block_sync\(\);" if "block_sync = " in kernel else r"barrier\.cluster\.wait|cluster_sync(_init)?\(\);"
         assert re.search(started, kernel[:remote.start()]), kernel[:80]
+
+
+def test_dequantization_reads_the_weight_behind_its_wait():
+    """It starts before the kernel ahead of it has ended, and that one may be
+    whatever wrote the weight."""
+    text = code(os.path.join(CSRC, "pack_dequant.cu"))
+    body = text[text.index("dequant_rows_kernel("):]
+    assert body.index("griddepcontrol.wait") < re.search(r"ld_\w+\(|__ldg\(", body).start()
