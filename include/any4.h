@@ -175,6 +175,9 @@ ANY4_API int any4_linear_kernel(int bits, int m, int n, int k, int group);
  *              partial-sum area behind them needs no initialization). After a
  *              failed launch, zero-fill it again. Calls that may overlap on
  *              the device need separate workspaces.
+ *              A call is one kernel for M <= 16 and may be several beyond, which
+ *              hand each other results in it: host threads that share a stream
+ *              and a workspace make these calls one at a time.
  *
  * Each weight is dequantized as w_hat = fma(alpha, LUT[idx], beta) in bf16
  * (fma.rn.bf16x2: the exact value rounded once to bf16) and contracted on the
@@ -343,7 +346,9 @@ ANY4_API int any4_pack_format(int format, const uint8_t* idx_nib, const uint16_t
  *   workspace  >= any4_lora_workspace_bytes(...) bytes, 16-byte aligned, with
  *              any4_linear's contract: its first any4_lora_header_bytes()
  *              bytes zero before the first use, left zero by every call that
- *              completes; calls that may overlap need separate ones. It may be
+ *              completes; calls that may overlap need separate ones, and so do
+ *              host threads that call at the same time, on one stream too (the
+ *              call's kernels hand each other results in it). It may be
  *              the workspace of any call of this header, if large enough. The
  *              32-bit status word is any4_linear's (byte offset 65536*4).
  *

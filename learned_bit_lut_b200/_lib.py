@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -138,6 +139,30 @@ def _stream_of(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+_DECODE_TOKENS = 16   # up to here any4_linear is one kernel
+
+
+class _Kept:
+    """What the binding keeps for a stream. The lock is held from taking the
+    workspace to the end of a library call that launches kernels which hand each
+    other results through it: ctypes opens the interpreter lock meanwhile, and
+    another thread's launches on the stream (every thread starts on the same
+    one) may not come between. Reentrant, since a finalizer may make a call of
+    its own."""
+    __slots__ = ("lock", "workspace")
+
+    def __init__(self):
+        self.lock, self.workspace = threading.RLock(), None
+
+
+_KEPT: dict = {}
+
+
+def _kept(device: int, stream: int) -> _Kept:
+    kept = _KEPT.get((device, stream))
+    return kept if kept is not None else _KEPT.setdefault((device, stream), _Kept())
+
+
 def any4_packed_bytes(n: int, k: int, group: int) -> int:
     return lib.any4_packed_bytes(n, k, group)
 
@@ -218,6 +243,8 @@ def any4_dequant_bits(bits: int, packed: torch.Tensor, n: int, k: int, group: in
 def any4_linear_bits(bits: int, x: torch.Tensor, packed: torch.Tensor, n: int, k: int, group: int,
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     m = x.shape[0]
+    if m > _DECODE_TOKENS:
+        return _prefill(bits, x, packed, n, k, group, out, workspace)
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
@@ -225,6 +252,20 @@ def any4_linear_bits(bits: int, x: torch.Tensor, packed: torch.Tensor, n: int, k
     _check(lib.any4_linear_bits(bits, _dev(x, "x", 2, (m, k)), _dev(packed, "packed", 1), m, n, k, group,
                                 _dev(out, "out", 2, (m, n)), _dev(workspace, "workspace", 1),
                                 workspace.numel(), _stream(x.device)))
+    return out
+
+
+def _prefill(bits, x, packed, n, k, group, out, workspace):
+    """any4_linear_bits beyond 16 tokens, which may be several kernels."""
+    m, x_p = x.shape[0], _dev(x, "x", 2, (x.shape[0], k))
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+    out_p, packed_p, stream = _dev(out, "out", 2, (m, n)), _dev(packed, "packed", 1), _stream(x.device)
+    with _kept(x.get_device(), stream).lock:
+        if workspace is None:
+            workspace = workspace_for(m, n, k, group, x.device, bits)
+        _check(lib.any4_linear_bits(bits, x_p, packed_p, m, n, k, group, out_p, _dev(workspace, "workspace", 1),
+                                    workspace.numel(), stream))
     return out
 
 
@@ -260,8 +301,11 @@ def any4_linear(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, group: in
                 out: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x . W_hat^T for bf16 x (M x K) -> y (M x N, bf16). M <= 16 runs the
-    fused decode kernel, M > 16 the dequantize-then-GEMM prefill path."""
+    fused decode kernel, M > 16 the dequantize-then-GEMM prefill path. Any
+    number of threads may call it, on one stream or several."""
     m = x.shape[0]
+    if m > _DECODE_TOKENS:
+        return _prefill(4, x, packed, n, k, group, out, workspace)
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
@@ -415,20 +459,18 @@ def _grad_need(device: int, *shape: int) -> int:
 
 
 _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_bytes_bits(*shape))
-_LORA_WORKSPACES: dict = {}
 
 
-def _adapter_workspace(need: int, device: torch.device, stream: int) -> torch.Tensor:
-    """A workspace with a zeroed header: kept per stream and grown on demand,
-    or, while a CUDA graph is captured, one of the graph's own."""
+def _adapter_workspace(need: int, device: torch.device, kept: _Kept) -> torch.Tensor:
+    """A workspace with a zeroed header: the stream's, grown on demand, or, while
+    a CUDA graph is captured, one of the graph's own. Called with kept.lock held."""
     if need == 0:
         raise Any4Error(ANY4_ESHAPE)
+    ws = kept.workspace
     if not _capturing():
-        key = (device.index, stream)
-        ws = _LORA_WORKSPACES.get(key)
         if ws is not None and ws.numel() >= need:
             return ws
-        ws = _LORA_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = kept.workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     ws[:_HEADER_BYTES].zero_()
@@ -475,7 +517,8 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
     and l = ids[t]: the any4 linear layer with one of L low-rank adapters per
     token (a: L x R x K, b: L x N x R bf16, scale: L fp32, ids: M int32; ids
     outside [0, L) have no adapter, None is adapter 0 for every token).
-    ``u`` (M x R bf16) is written where given, for any4_linear_lora_grad."""
+    ``u`` (M x R bf16) is written where given, for any4_linear_lora_grad. Any
+    number of threads may make these calls, on one stream or several."""
     m, dev = x.shape[0], x.device
     ad = _adapters(a, b, scale, ids, m, n, k, dev)
     if out is None:
@@ -483,13 +526,16 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
         out_p = out.data_ptr()
     else:
         out_p = _typed(out, "out", _BF16, dev, (m, n))
+    x_p, w_p = _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev)
+    u_p = None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5]))
     stream = _stream(dev)
-    if workspace is None:
-        workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev, stream)
-    st = lib.any4_linear_lora(
-        bits, _typed(x, "x", _BF16, dev, (m, k)), _weight(packed, n, k, group, bits, dev), m, n, k, group, *ad, out_p,
-        None if u is None else _typed(u, "u", _BF16, dev, (m, ad[5])),
-        _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), stream)
+    kept = _kept(dev.index, stream)
+    with kept.lock:
+        if workspace is None:
+            workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev, kept)
+        st = lib.any4_linear_lora(bits, x_p, w_p, m, n, k, group, *ad, out_p, u_p,
+                                  _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
+                                  stream)
     if st != ANY4_OK:
         raise Any4Error(st)
     return out
@@ -541,13 +587,15 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
             x_p = _typed(x, "x", _BF16, dev, (m, k))
     u_p = _typed(u, "u", _BF16, dev, (m, rank)) if db is not None else None
     w_p = _weight(packed, n, k, group, bits, dev) if dx is not None else None
+    dy_p = _typed(dy, "dy", _BF16, dev, (m, n))
     stream = _stream(dev)
-    if workspace is None:
-        workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev, stream)
-    _check(lib.any4_linear_lora_grad(
-        bits, _typed(dy, "dy", _BF16, dev, (m, n)), x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad,
-        dx_p, da_p, db_p, _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
-        stream))
+    kept = _kept(dev.index, stream)
+    with kept.lock:
+        if workspace is None:
+            workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev, kept)
+        _check(lib.any4_linear_lora_grad(
+            bits, dy_p, x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad, dx_p, da_p, db_p,
+            _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), stream))
     return dx, da, db
 
 

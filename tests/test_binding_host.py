@@ -1,0 +1,135 @@
+"""What the binding does on the host around a call: workspaces, locks, sizes and
+errors (CPU only: host tensors that say they are on a GPU, and stand-ins for
+the library's calls)."""
+import threading
+import time
+
+import pytest
+import torch
+
+from learned_bit_lut_b200 import _lib
+
+N, K, G, RANK = 64, 128, 64, 16
+HEADER = _lib.lib.any4_lora_header_bytes()
+
+
+class OnGpu(torch.Tensor):
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+class Host:
+    """The state the stand-ins look at."""
+
+    def __init__(self):
+        self.stream = threading.local()
+        self.capturing = False
+        self.need = HEADER + 4096
+        self.calls = []
+        self.during = lambda name, args: None   # what happens inside a library call
+
+    def library_call(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            self.during(name, args)
+            return 0
+        return call
+
+
+@pytest.fixture
+def host(monkeypatch):
+    h = Host()
+    plain = torch.empty
+
+    def empty(*shape, dtype=None, device=None):
+        t = plain(*shape, dtype=dtype)
+        t.view(torch.uint8).fill_(0xA5)   # not zero by chance
+        return t.as_subclass(OnGpu)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *s, dtype=None, device=None: zeros(*s, dtype=dtype).as_subclass(OnGpu))
+    monkeypatch.setattr(_lib, "_stream", lambda device: getattr(h.stream, "at", 7))
+    monkeypatch.setattr(_lib, "_stream_of", lambda t: getattr(h.stream, "at", 7))
+    monkeypatch.setattr(_lib, "_capturing", lambda: h.capturing)
+    monkeypatch.setattr(_lib, "_current_device", lambda: 0)
+    for name in ("any4_lora_workspace_bytes", "any4_lora_grad_workspace_bytes", "any4_linear_workspace_bytes_bits"):
+        monkeypatch.setattr(_lib.lib, name, lambda *a: h.need)
+    for name in ("any4_linear_lora", "any4_linear_lora_grad", "any4_linear", "any4_linear_bits"):
+        monkeypatch.setattr(_lib.lib, name, h.library_call(name))
+    for cache in ("_WORKSPACES", "_KEPT"):
+        if hasattr(_lib, cache):
+            monkeypatch.setattr(_lib, cache, {})
+    for size in (_lib._lora_need, _lib._grad_need):
+        size.cache_clear()
+    yield h
+    for size in (_lib._lora_need, _lib._grad_need):
+        size.cache_clear()
+
+
+PACKED_BYTES = _lib.lib.any4_packed_bytes(N, K, G)
+
+
+def call(name, m=40, workspace=None):
+    x, packed = on_gpu(m, K), on_gpu(PACKED_BYTES, dtype=torch.uint8)
+    if name == "linear":
+        return _lib.any4_linear(x, packed, N, K, G, workspace=workspace)
+    if name == "linear_bits":
+        return _lib.any4_linear_bits(4, x, packed, N, K, G, workspace=workspace)
+    a, b, scale = on_gpu(2, RANK, K), on_gpu(2, N, RANK), on_gpu(2, dtype=torch.float32)
+    if name == "lora":
+        return _lib.any4_linear_lora(x, packed, N, K, G, a, b, scale, workspace=workspace)
+    return _lib.any4_linear_lora_grad(on_gpu(m, N), x, on_gpu(m, RANK), packed, N, K, G, a, b, scale, workspace=workspace)
+
+
+def run_threads(*jobs):
+    errors = []
+
+    def guard(job):
+        try:
+            job()
+        except BaseException as e:   # noqa: BLE001  (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=guard, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(30)
+    assert not any(t.is_alive() for t in threads) and not errors, errors
+
+
+@pytest.mark.parametrize("pair", [("lora", "lora"), ("lora", "grad"), ("grad", "linear"), ("linear", "linear_bits")], ids=str)
+def test_calls_of_two_threads_on_one_stream_do_not_mix_their_launches(host, pair):
+    """A call's kernels hand each other results in its workspace, and the
+    interpreter lock is open while the library launches them."""
+    inside, most = [], []
+
+    def during(name, args):
+        inside.append(name)
+        most.append(len(inside))
+        time.sleep(0.002)
+        inside.remove(name)
+
+    host.during = during
+    run_threads(*[lambda name=name: [call(name) for _ in range(10)] for name in pair])
+    assert len(host.calls) == 20 and max(most) == 1
+
+
+def test_threads_on_their_own_streams_do_not_wait_for_each_other(host):
+    both = threading.Barrier(2)
+    host.during = lambda name, args: both.wait(10)   # each call is inside while the other is
+
+    def job(stream):
+        host.stream.at = stream
+        for _ in range(5):
+            call("lora")
+
+    run_threads(lambda: job(1), lambda: job(2))

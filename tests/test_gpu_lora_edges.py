@@ -106,3 +106,37 @@ def test_dequantization_follows_a_copy_of_the_weight(bits):
                      a4.any4_linear_bits(bits, x, packed, 1024, 1024, 128)))
     for i, out in enumerate(outs):
         assert torch.equal(out, (wants if i % 4 < 2 else ys)[i % 2])
+
+
+# ---- host threads
+
+def test_two_threads_on_one_stream():
+    """Threads share the default stream, and each gets its own results."""
+    import threading
+    cases = [Case(40, 272, 512, 128, 4, 3, 16, "mixed", seed=66), Case(700, 528, 1088, 64, 3, 6, 40, "holes", seed=67),
+             Case(9, 528, 1024, 128, 4, 2, 24, "mixed", seed=68)]
+    packed, us = [c.packed() for c in cases], [inner(c) for c in cases]
+
+    def step(i):
+        c = cases[i]
+        args = (packed[i], *c.shape(), c.a, c.b, c.scale, c.ids)
+        return (a4.any4_linear_lora(c.x, *args, bits=c.bits), a4.any4_linear_bits(c.bits, c.x, packed[i], *c.shape()),
+                *a4.any4_linear_lora_grad(c.dy, c.x, us[i], *args, bits=c.bits))
+
+    wants = [step(i) for i in range(len(cases))]
+    torch.cuda.synchronize()
+    outs = [[] for _ in cases]
+
+    def job(i):
+        torch.cuda.set_device(0)
+        outs[i] = [step(i) for _ in range(40)]
+
+    threads = [threading.Thread(target=job, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    for got, want in zip(outs, wants):
+        assert len(got) == 40
+        assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for one in got for p, q in zip(one, want))
