@@ -66,7 +66,8 @@ cudaError_t launch_slot_lists(const Adapters& ad, int m, void* space, cudaStream
 // M_l = A_l^T (forward: in = x, u) or B_l (backward: in = dy, v), zeros
 // without an adapter, as a bf16 pair: row t of `pairs` is [leading part, R16
 // values][trailing part, R16 values], R16 = R rounded up to 16, whose sum is z
-// to 2^-16; `rounded` (or null) gets z in bf16, R values a row.
+// to 2^-16 and whose parts have z's sign and are zero only with it; `rounded`
+// (or null) gets z rounded to bf16, R values a row.
 inline int rank16(int rank) { return (rank + 15) / 16 * 16; }
 inline size_t pairs_bytes(int m, int rank) { return (size_t)m * rank16(rank) * 4; }
 //

@@ -165,12 +165,30 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two values as bf16 pairs: the leading parts, and in lo the trailing ones. An
-// infinity or NaN goes into both: the sum of their products is that of the one.
+// Two values as bf16 pairs (lora.cuh): the leading parts, and in lo the trailing
+// ones. The leading part is the largest bf16 number below |v|, with v's sign:
+// bits - 1 without its lower half. So the trailing part has that sign too and is
+// not zero, and the sum of both parts' products with an infinity is that of the
+// one value, where parts of two signs (as rounding to nearest gives) or a zero
+// would make it NaN. An infinity's trailing part is the infinity, a NaN's a NaN.
+// A trailing part may round to zero below 2^-110 (tiny_pair).
+constexpr uint32_t kTinyPair = 0x08800000u;
+__device__ __noinline__ uint32_t tiny_pair(float v, uint32_t hi_lo) {   // leading part, trailing part << 16
+  const uint32_t mag = __float_as_uint(v) & 0x7FFFFFFFu, sign = __float_as_uint(v) >> 16 & 0x8000u;
+  if (mag - 1u >= kTinyPair) return hi_lo;
+  if (mag <= 0x10000u) return (sign | 1u) * 0x10001u;   // to 2^-133: twice the smallest bf16 number
+  return hi_lo & 0x7FFF0000u ? hi_lo : hi_lo | (sign | 1u) << 16;
+}
 __device__ __forceinline__ uint32_t split_pair(float a, float b, uint32_t& lo) {
-  const uint32_t hi = bf16x2_of(a, b);
-  const float h0 = bf16_bits_to_float(hi & 0xFFFFu), h1 = __uint_as_float(hi & 0xFFFF0000u);
-  lo = bf16x2_of(isfinite(h0) ? a - h0 : h0, isfinite(h1) ? b - h1 : h1);
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b), mx = x & 0x7FFFFFFFu, my = y & 0x7FFFFFFFu;
+  const uint32_t hx = (x - (mx != 0u)) & 0xFFFF0000u, hy = (y - (my != 0u)) & 0xFFFF0000u;
+  uint32_t hi = __byte_perm(hx, hy, 0x7632);
+  lo = bf16x2_of(a - __uint_as_float(hx), b - __uint_as_float(hy));   // exact before the rounding
+  if (mx - 1u < kTinyPair || my - 1u < kTinyPair) {
+    const uint32_t p = tiny_pair(a, __byte_perm(hi, lo, 0x5410)), q = tiny_pair(b, __byte_perm(hi, lo, 0x7632));
+    hi = __byte_perm(p, q, 0x5410);
+    lo = __byte_perm(p, q, 0x7632);
+  }
   return hi;
 }
 
@@ -187,8 +205,11 @@ __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, 
   row[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
   if (p.rounded != nullptr) {
     uint4* out = reinterpret_cast<uint4*>(p.rounded + (size_t)t * p.ad.rank + r0);
-    out[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (r0 + 8 < p.ad.rank) out[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16x2_of(z[2 * i], z[2 * i + 1]);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (r0 + 8 < p.ad.rank) out[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -421,13 +442,15 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
       if (l[h] == kNotOwn) continue;
       const int i = i0 + h * kDownTcThreads, tr = i / quads, r0 = (i - tr * quads) * 4, tt = tile * kTileTokens + tr;
       const float sc = scales[tr];
+      const float4 v = make_float4(z[h].x * sc, z[h].y * sc, z[h].z * sc, z[h].w * sc);
       uint32_t lo0, lo1;
-      const uint32_t hi0 = split_pair(z[h].x * sc, z[h].y * sc, lo0), hi1 = split_pair(z[h].z * sc, z[h].w * sc, lo1);
+      const uint32_t hi0 = split_pair(v.x, v.y, lo0), hi1 = split_pair(v.z, v.w, lo1);
       uint16_t* row = p.pairs + (size_t)tt * 2 * r16 + r0;
       *reinterpret_cast<uint2*>(row) = make_uint2(hi0, hi1);
       *reinterpret_cast<uint2*>(row + r16) = make_uint2(lo0, lo1);
       if (p.rounded != nullptr && r0 < p.ad.rank)
-        *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) = make_uint2(hi0, hi1);
+        *reinterpret_cast<uint2*>(p.rounded + (size_t)tt * p.ad.rank + r0) =
+            make_uint2(bf16x2_of(v.x, v.y), bf16x2_of(v.z, v.w));
     }
   }
   if (threadIdx.x == 0) p.counters[tg] = 0u;   // ready for the next call

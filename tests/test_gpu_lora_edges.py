@@ -140,3 +140,89 @@ def test_two_threads_on_one_stream():
     for got, want in zip(outs, wants):
         assert len(got) == 40
         assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for one in got for p, q in zip(one, want))
+
+
+# ---- infinities and NaN where one adapter fills a tile, where several share it,
+# and in every order of the tokens: the formulas' values
+
+def same(p, q):
+    return torch.equal(p.nan_to_num(7.0, 8.0, 9.0), q.nan_to_num(7.0, 8.0, 9.0)) and torch.equal(p.isnan(), q.isnan())
+
+
+def non_finite(t):
+    """One of each kind, far apart, in the first and the last adapter."""
+    for l in {0, t.shape[0] - 1}:
+        rows, cols = t[l].shape
+        t[l, 0, cols // 3], t[l, rows - 1, cols // 2], t[l, rows // 2, 1] = INF, -INF, NAN
+
+
+ORDERS = ["null", "runs", "last", "holes"]
+# fused and dequantized prefill, splits, pairs of blocks; ranks inside, at and over a stage's halves
+SPOILT = [(40, 272, 320, 64, 4, 8), (150, 528, 1024, 128, 4, 16), (300, 272, 320, 64, 3, 24), (600, 272, 576, 64, 4, 72),
+          (2600, 2320, 2112, 64, 4, 40), (1100, 1040, 4096, 128, 4, 16)]
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("m,n,k,g,bits,rank", SPOILT, ids=["m%d_r%d" % (s[0], s[5]) for s in SPOILT])
+def test_infinite_adapters(m, n, k, g, bits, rank, order):
+    """B in y, A in dx: their products with u and v are +-infinity, not NaN."""
+    c = Case(m, n, k, g, bits, 1 if order == "null" else 3, rank, order, seed=71)
+    non_finite(c.b)
+    y = forward(c)
+    check(y, *c.y_ref(), "y")
+    assert bool(y.isinf().any())
+    if c.ids is not None:   # and the same next to other tokens
+        perm = torch.randperm(m, device="cuda")
+        other = a4.any4_linear_lora(c.x[perm].contiguous(), c.packed(), *c.shape(), c.a, c.b, c.scale,
+                                    c.ids[perm].contiguous(), bits=bits)
+        assert same(other, y[perm])
+    c = Case(m, n, k, g, bits, c.adapters, rank, order, seed=72)
+    non_finite(c.a)
+    u = torch.zeros(m, rank, dtype=torch.bfloat16, device="cuda")
+    dx = grads(c, u=u, outputs=("dx",))[0]
+    check(dx, *c.grad_ref(c.x, u)[0], "dx")
+    assert bool(dx.isinf().any())
+    if c.ids is not None:
+        other = a4.any4_linear_lora_grad(c.dy[perm].contiguous(), None, None, c.packed(), *c.shape(), c.a, c.b, c.scale,
+                                         c.ids[perm].contiguous(), bits=bits, outputs=("dx",))[0]
+        assert same(other, dx[perm])
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("m,n,k,g,bits,rank", SPOILT, ids=["m%d_r%d" % (s[0], s[5]) for s in SPOILT])
+def test_infinite_inputs_of_the_adapters_gradients(m, n, k, g, bits, rank, order):
+    """An infinite x[t][k] makes column k of its adapter's dA infinite with the
+    signs of v[t], or NaN where two tokens' signs differ; u the same in dB."""
+    c = Case(m, n, k, g, bits, 1 if order == "null" else 3, rank, order, seed=73)
+    u = inner(c)
+    for i, v in enumerate((INF, -INF, INF, NAN)):
+        for t in (min(i, m - 1), m - 1 - i):
+            c.x[t, 5 + 7 * i] = v
+    c.x[m // 2, k - 1] = INF
+    u[m // 2, rank - 1], u[m // 3, 0] = -INF, NAN
+    got = grads(c, u=u)
+    refs = c.grad_ref(c.x, u)
+    for name, g_, ref in zip(("dx", "da", "db"), got, refs):
+        check(g_, *ref, name)
+
+
+def test_pairs_of_any_size_meet_an_infinity():
+    """u from 2^-140 to 2^120, powers of two (whose bf16 form is exact) among
+    them, times an infinite B, in tiles of one adapter and of several."""
+    for order in ("null", "holes"):
+        c = Case(64, 16, 64, 64, 4, 1, 8, order, seed=74)
+        c.x.zero_(), c.a.zero_(), c.b.zero_()
+        size = torch.linspace(-132, 120, 64, device="cuda").round()
+        c.x[:, 0] = torch.exp2(size.double()).to(torch.bfloat16)
+        c.x[1::2, 0] *= -1.0
+        c.x[2::4, 0] *= 1.5
+        c.a[0, 0, 0], c.a[0, 1, 0] = 1.0, 2.0 ** -8
+        c.scale.fill_(1.0)
+        c.b[0, 3, 0], c.b[0, 4, 0], c.b[0, 5, 1] = INF, -INF, INF
+        y = forward(c)
+        x, t = c.x.double(), c.tokens[0]
+        assert bool((x[t, 0] != 0).all())
+        assert torch.equal(y[t, 3].double(), torch.copysign(torch.full_like(x[t, 0], INF), x[t, 0]))
+        assert torch.equal(y[t, 4].double(), torch.copysign(torch.full_like(x[t, 0], INF), -x[t, 0]))
+        big = t[x[t, 0].abs() > 2.0 ** -118]   # u = 2^-8 x is a normal number
+        assert torch.equal(y[big, 5].double(), torch.copysign(torch.full_like(x[big, 0], INF), x[big, 0]))
