@@ -195,8 +195,12 @@ __device__ __forceinline__ uint32_t split_pair(float a, float b, uint32_t& lo) {
 // z (16 values from r0 on) of token t: the bf16 pair, and z rounded to bf16.
 __device__ __forceinline__ void store_inner(const DownParams& p, int t, int r0, const float (&z)[16]) {
   uint32_t hi[8], lo[8];
+  // the ranks past R: zeros, not 0 * an infinity or NaN of `in`
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hi[i] = split_pair(z[2 * i], z[2 * i + 1], lo[i]);
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = split_pair(z[2 * i], z[2 * i + 1], lo[i]);
+    if (i >= 4 && r0 + 8 >= p.ad.rank) hi[i] = lo[i] = 0u;
+  }
   uint4* row = reinterpret_cast<uint4*>(p.pairs + (size_t)t * 2 * p.r16 + r0);
   row[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   row[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -442,7 +446,8 @@ __global__ void __launch_bounds__(kDownTcThreads, 2)
       if (l[h] == kNotOwn) continue;
       const int i = i0 + h * kDownTcThreads, tr = i / quads, r0 = (i - tr * quads) * 4, tt = tile * kTileTokens + tr;
       const float sc = scales[tr];
-      const float4 v = make_float4(z[h].x * sc, z[h].y * sc, z[h].z * sc, z[h].w * sc);
+      float4 v = make_float4(z[h].x * sc, z[h].y * sc, z[h].z * sc, z[h].w * sc);
+      if (r0 >= p.ad.rank) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // as store_inner
       uint32_t lo0, lo1;
       const uint32_t hi0 = split_pair(v.x, v.y, lo0), hi1 = split_pair(v.z, v.w, lo1);
       uint16_t* row = p.pairs + (size_t)tt * 2 * r16 + r0;

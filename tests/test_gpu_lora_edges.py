@@ -226,3 +226,27 @@ def test_pairs_of_any_size_meet_an_infinity():
         assert torch.equal(y[t, 4].double(), torch.copysign(torch.full_like(x[t, 0], INF), -x[t, 0]))
         big = t[x[t, 0].abs() > 2.0 ** -118]   # u = 2^-8 x is a normal number
         assert torch.equal(y[big, 5].double(), torch.copysign(torch.full_like(x[big, 0], INF), x[big, 0]))
+
+
+# ranks that end inside 16 columns: an infinite input meets A's and B's missing ranks
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("m,n,k,g,bits,rank", [(40, 272, 320, 64, 4, 8), (40, 272, 320, 64, 4, 16), (300, 272, 320, 64, 3, 24),
+                                               (600, 272, 4096, 64, 4, 72), (2600, 2320, 2112, 64, 4, 40)], ids=str)
+def test_infinite_inputs_of_the_layer(m, n, k, g, bits, rank, order):
+    """x in y and u, dy in dx and (over v) dA: signs by the formulas. A and B
+    are made positive, so that u and v of such a token are +-infinity."""
+    c = Case(m, n, k, g, bits, 1 if order == "null" else 3, rank, order, seed=75)
+    c.a, c.b = c.a.abs() + 2.0 ** -9, c.b.abs() + 2.0 ** -9
+    c.a, c.b = c.a.to(torch.bfloat16), c.b.to(torch.bfloat16)
+    c.x[0, 3], c.x[m // 2, k - 1], c.x[m - 1, 64], c.x[m - 2, 1] = INF, -INF, INF, NAN
+    u = torch.empty(m, rank, dtype=torch.bfloat16, device="cuda")
+    y = forward(c, u=u)
+    check(u, *c.u_ref(), "u")
+    check(y, *c.y_ref(), "y")
+    c = Case(m, n, k, g, bits, c.adapters, rank, order, seed=76)
+    c.a, c.b = (c.a.abs() + 2.0 ** -9).to(torch.bfloat16), (c.b.abs() + 2.0 ** -9).to(torch.bfloat16)
+    c.dy[0, 3], c.dy[m // 2, n - 1], c.dy[m - 1, 15], c.dy[m - 2, 1] = INF, -INF, INF, NAN
+    u = inner(c)
+    for name, g_, ref in zip(("dx", "da", "db"), grads(c, u=u), c.grad_ref(c.x, u)):
+        check(g_, *ref, name)
