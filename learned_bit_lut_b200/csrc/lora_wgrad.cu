@@ -431,7 +431,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         a_phase ^= 1u << s;
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kABytes / 16 / kWorkThreads; ++i) bad |= patch_finite(abase + (uint32_t)(thread + i * kWorkThreads) * 16u);
+        for (int i = 0; i < kABytes / 16 / kWorkThreads; ++i) bad |= patch_finite<false>(abase + (uint32_t)(thread + i * kWorkThreads) * 16u);
         if (bad) *(volatile int*)&ctl->spoilt = 1;
         fence_proxy_async_smem();
         __syncwarp();

@@ -222,8 +222,9 @@ __device__ __forceinline__ void finish_splits(const float* __restrict__ parts, i
 // its adapters, with z zeroed in the rows of the other tokens. So that an
 // infinity or NaN in an adapter reaches none of those (0 times it is NaN), it
 // is taken out of M's tile as well, and the epilogue, told by `spoilt`, adds
-// its products for the adapter's own tokens in fp32 (where z is not finite
-// either, the result is NaN). This patching runs on
+// its products for the adapter's own tokens in fp32. A one of its sign stays in
+// its place: what that adds to those tokens is lost in an infinity or NaN, and
+// an infinite z times a zero would be NaN. This patching runs on
 // warps that idle otherwise; tiles of one adapter go straight from TMA to the
 // tensor core.
 struct NoLora {};
@@ -303,16 +304,16 @@ __device__ __forceinline__ bool patch_tile(uint32_t tile, int steps, int thread)
     if (e >= 256 * steps) break;
     if (TRANS) {
       const int per_half = 128 * steps;
-      found |= patch_finite(tile + (uint32_t)(e < per_half ? e * 16 : kAStageBytes / 2 + (e - per_half) * 16));
+      found |= patch_finite<true>(tile + (uint32_t)(e < per_half ? e * 16 : kAStageBytes / 2 + (e - per_half) * 16));
     } else {
       const int row = e & 127, c = e >> 7;
-      found |= patch_finite(tile + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
+      found |= patch_finite<true>(tile + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
     }
   }
   return found;
 }
 
-// What patch_finite took out of the products of token t and output row: the
+// What patch_tile took out of the products of token t and output row: the
 // non-finite entries of its adapter's row times z.
 template <bool TRANS>
 __device__ __noinline__ float spoilt_term(const LoraArgs& la, int t, int row, int rows) {

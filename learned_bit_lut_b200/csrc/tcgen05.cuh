@@ -288,12 +288,15 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in eac
   return ~((bad >> 15) * 0xFFFFu);
 }
 
-// Takes the infinities and NaN out of the 16 bytes at addr; true if there were any.
+// Takes the infinities and NaN out of the 16 bytes at addr, which become zeros
+// or, with ONES, ones of their sign; true if there were any.
+template <bool ONES>
 __device__ __forceinline__ bool patch_finite(uint32_t addr) {
   const uint4 v = lds128(addr);
   const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
   const bool found = (a & b & c & d) != 0xFFFFFFFFu;
-  if (found) sts128(addr, v.x & a, v.y & b, v.z & c, v.w & d);
+  auto patched = [](uint32_t w, uint32_t m) { return ONES ? (w & (m | 0x80008000u)) | (~m & 0x3F803F80u) : w & m; };
+  if (found) sts128(addr, patched(v.x, a), patched(v.y, b), patched(v.z, c), patched(v.w, d));
   return found;
 }
 

@@ -250,3 +250,27 @@ def test_infinite_inputs_of_the_layer(m, n, k, g, bits, rank, order):
     u = inner(c)
     for name, g_, ref in zip(("dx", "da", "db"), grads(c, u=u), c.grad_ref(c.x, u)):
         check(g_, *ref, name)
+
+
+@pytest.mark.parametrize("m", [13, 40, 300, 600, 2600])
+@pytest.mark.parametrize("order", ["null", "holes", "runs"])
+def test_infinite_input_and_infinite_adapter_meet(m, order):
+    """u (v) and B (A) infinite at the same rank: their product is an infinity
+    of their signs, whoever else shares the tile."""
+    shape = (2320, 2112, 64) if m == 2600 else (272, 320, 64)
+    c = Case(m, *shape, 4, 1 if order == "null" else 3, 24, order, seed=77)
+    c.a, c.b = (c.a.abs() + 2.0 ** -9).to(torch.bfloat16), (c.b.abs() + 2.0 ** -9).to(torch.bfloat16)
+    c.x[0, 3], c.x[m // 2, 7], c.x[m - 1, 64] = INF, -INF, INF
+    c.b[:, 5, 2], c.b[:, 6, 20], c.b[:, 7, 9] = INF, -INF, NAN
+    y = forward(c)
+    check(y, *c.y_ref(), "y")
+    if c.ids is not None:
+        perm = torch.randperm(m, device="cuda")
+        assert same(a4.any4_linear_lora(c.x[perm].contiguous(), c.packed(), *c.shape(), c.a, c.b, c.scale,
+                                        c.ids[perm].contiguous()), y[perm])
+    c = Case(m, *shape, 4, c.adapters, 24, order, seed=78)
+    c.a, c.b = (c.a.abs() + 2.0 ** -9).to(torch.bfloat16), (c.b.abs() + 2.0 ** -9).to(torch.bfloat16)
+    c.dy[0, 3], c.dy[m // 2, 7], c.dy[m - 1, 64] = INF, -INF, INF
+    c.a[:, 2, 5], c.a[:, 20, 6], c.a[:, 9, 7] = INF, -INF, NAN
+    u = torch.zeros(m, 24, dtype=torch.bfloat16, device="cuda")
+    check(grads(c, u=u, outputs=("dx",))[0], *c.grad_ref(c.x, u)[0], "dx")
