@@ -404,7 +404,8 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
  *   code = x / step rounded half to even, -127 .. 127
  *   value = code * step, rounded once to bf16
  *
- * |value - x| <= step / 2 before that rounding. A group of zeros has step 0
+ * |value - x| <= step / 2 before that rounding, which takes values within half
+ * a step of the largest bf16 number to infinity. A group of zeros has step 0
  * and zero codes; a group with an infinity or a NaN has step NaN and zero
  * codes, and reads back as NaN.
  *

@@ -15,6 +15,10 @@ inline bool act_shape_ok(int m, int k, int group) {
   return m >= 1 && m <= kMaxTokens && k <= (1 << 20) && shape_ok(kTileRows, k, group);
 }
 
+// 2^121: from this step on a code's value may round to an infinity (-128 times
+// any smaller step is a bf16 number yet).
+constexpr uint32_t kHugeStep = 0x7C00u;
+
 // Four codes (a 32-bit word) times a step (in both halves of step2): two bf16
 // pairs. Byte c = 128 s + m (s its sign bit) stands for m - 128 s; as bf16
 // bits, 0x4300 | m is 128 + m and 0x4300 | 128 s is 128 + 128 s, both exact,

@@ -399,13 +399,16 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
           if (!ok) break;
         }
         rc.next(src_stages);
-        bool bad = false;
+        bool bad = false, huge = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t st = half ? step2nd : step;
-          if (mixed && (st & 0x7F80u) == 0x7F80u) {   // a group that reads back as NaN
-            st = 0;
-            bad = true;
+          if (mixed && (st & 0x7FFFu) >= kHugeStep) {
+            huge = true;
+            if ((st & 0x7F80u) == 0x7F80u) {   // a group that reads back as NaN
+              st = 0;
+              bad = true;
+            }
           }
           const uint32_t step2 = st | (st << 16);
           const uint4 q = lds128(rbase + (uint32_t)(rs * kRawBytes + token * 128 + (((run + 4 * half) ^ (token & 7)) << 4)));
@@ -418,6 +421,10 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
           sts128(row + (uint32_t)(((2 * run) ^ (token & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
           sts128(row + (uint32_t)(((2 * run + 1) ^ (token & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
         }
+        if (huge)
+          for (int i = 0; i < 4; ++i)   // this thread's four runs of 8 values
+            bad |= patch_finite<false>(abase + (uint32_t)((i >> 1) * (kABytes / 2) + token * 128 +
+                                                          (((2 * run + (i & 1)) ^ (token & 7)) << 4)));
         if (bad) *(volatile int*)&ctl->spoilt = 1;
         fence_proxy_async_smem();
         __syncwarp();

@@ -274,3 +274,34 @@ def test_infinite_input_and_infinite_adapter_meet(m, order):
     c.a[:, 2, 5], c.a[:, 20, 6], c.a[:, 9, 7] = INF, -INF, NAN
     u = torch.zeros(m, 24, dtype=torch.bfloat16, device="cuda")
     check(grads(c, u=u, outputs=("dx",))[0], *c.grad_ref(c.x, u)[0], "dx")
+
+
+# ---- checkpoints whose finite steps stand for values that round to infinity
+
+@pytest.mark.parametrize("order", ["mixed", "runs", "null"])
+@pytest.mark.parametrize("m", [13, 150, 600])
+def test_values_beyond_bf16_of_one_request_reach_no_other(m, order):
+    c = Case(m, 272, 320, 64, 4, 1 if order == "null" else 3, 24, order, seed=79)
+    top = torch.finfo(torch.bfloat16).max
+    spoilt = c.tokens[c.adapters - 1][:2]
+    c.x[spoilt[0], 64:70] = torch.tensor([top, -top, top / 2, 1e38, -1e30, 1.0], device="cuda")
+    c.x[spoilt[1], 200] = -top
+    kept = a4.any4_act_pack(c.x, 64)
+    x = a4.any4_act_unpack(*kept, 64)
+    assert bool(torch.isfinite(kept[1].float()).all()) and int(x.isinf().sum()) == 3
+    u = inner(c)
+    got = grads(c, kept, u)
+    for name, g, ref in zip(("dx", "da", "db"), got, c.grad_ref(x, u)):
+        check(g, *ref, name)
+    assert bool(torch.isfinite(got[1][:-1].float()).all())
+    # the same from the values, and with every code as the host may hand them over
+    plain = grads(c, x, u)
+    assert all(same(p, q) for p, q in zip(got, plain))
+    codes, steps = kept[0].clone(), kept[1].clone()
+    codes[spoilt[0], :64] = torch.arange(-128, -64, dtype=torch.int8, device="cuda")
+    steps[spoilt[0], 0] = 2.0 ** 121
+    steps[spoilt[1], 1] = -2.0 ** 123
+    x = a4.any4_act_unpack(codes, steps, 64)
+    assert bool(x.isinf().any())
+    got = grads(c, (codes, steps), u, outputs=("da",))
+    check(got[1], *c.grad_ref(x, u)[1], "da")
