@@ -279,15 +279,20 @@ def any4_dequant(packed: torch.Tensor, n: int, k: int, group: int,
     return out
 
 
+def _refused(bits: int, m: int, n: int, k: int, group: int) -> int:
+    """Raises what made a workspace's size 0: the device could not be asked, or
+    the call does not take the shape (or its adapters')."""
+    code = lib.any4_linear_kernel(bits, m, n, k, group)
+    raise Any4Error(code if code == ANY4_ECUDA else ANY4_ESHAPE)
+
+
 _WORKSPACES: dict = {}
 
 
 def workspace_for(m: int, n: int, k: int, group: int, device: torch.device, bits: int = 4) -> torch.Tensor:
     """A zero-initialised workspace for this stream, grown on demand and reused
     by later calls on the same stream (calls on one stream never overlap)."""
-    need = lib.any4_linear_workspace_bytes_bits(bits, m, n, k, group)
-    if need == 0:
-        raise Any4Error(ANY4_ESHAPE)
+    need = lib.any4_linear_workspace_bytes_bits(bits, m, n, k, group) or _refused(bits, m, n, k, group)
     key = (device.index if device.index is not None else torch.cuda.current_device(),
            _stream(device))
     ws = _WORKSPACES.get(key)
@@ -447,15 +452,15 @@ def _on_device(name: str):
     return wrap
 
 
-@functools.lru_cache(maxsize=1024)
+@functools.lru_cache(maxsize=1024)   # a refusal is not kept: it may be a CUDA error that passes
 def _lora_need(device: int, *shape: int) -> int:
     """any4_lora_workspace_bytes of a shape (it depends on the device's SM count)."""
-    return lib.any4_lora_workspace_bytes(*shape)
+    return lib.any4_lora_workspace_bytes(*shape) or _refused(*shape[:5])
 
 
 @functools.lru_cache(maxsize=1024)
 def _grad_need(device: int, *shape: int) -> int:
-    return lib.any4_lora_grad_workspace_bytes(*shape)
+    return lib.any4_lora_grad_workspace_bytes(*shape) or _refused(*shape[:5])
 
 
 _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_bytes_bits(*shape))
@@ -464,8 +469,6 @@ _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_
 def _adapter_workspace(need: int, device: torch.device, kept: _Kept) -> torch.Tensor:
     """A workspace with a zeroed header: the stream's, grown on demand, or, while
     a CUDA graph is captured, one of the graph's own. Called with kept.lock held."""
-    if need == 0:
-        raise Any4Error(ANY4_ESHAPE)
     ws = kept.workspace
     if not _capturing():
         if ws is not None and ws.numel() >= need:

@@ -74,6 +74,24 @@ def host(monkeypatch):
         size.cache_clear()
 
 
+@pytest.mark.parametrize("name", ["lora", "grad", "linear", "decode"])
+def test_a_device_that_cannot_be_asked_is_not_a_shape(host, monkeypatch, name):
+    """A size of 0 is told apart, and asked for again by the next call."""
+    ask = lambda: call("linear", m=1) if name == "decode" else call(name)   # noqa: E731
+    host.need = 0
+    monkeypatch.setattr(_lib.lib, "any4_linear_kernel", lambda *a: _lib.ANY4_ECUDA)
+    with pytest.raises(_lib.Any4Error) as e:
+        ask()
+    assert e.value.status == _lib.ANY4_ECUDA
+    monkeypatch.setattr(_lib.lib, "any4_linear_kernel", lambda *a: _lib.ANY4_ESHAPE)
+    with pytest.raises(_lib.Any4Error) as e:
+        ask()
+    assert e.value.status == _lib.ANY4_ESHAPE
+    host.need = HEADER + 4096
+    ask()
+    assert len(host.calls) == 1
+
+
 PACKED_BYTES = _lib.lib.any4_packed_bytes(N, K, G)
 
 
