@@ -418,6 +418,16 @@ ANY4_API int any4_act_pack(const uint16_t* x, int m, int k, int group, int8_t* c
 ANY4_API int any4_act_unpack(const int8_t* codes, const uint16_t* steps, int m, int k, int group, uint16_t* x,
                              any4_stream_t stream);
 
+/*
+ * any4_stream_capture_id - which CUDA graph capture `stream` takes part in: a
+ * number of its own for every capture of the process, or 0 for none. For callers
+ * that keep workspaces: a captured call's workspace belongs to its graph, which
+ * may be replayed beside other calls, at any time while it lives. Host only.
+ * Returns ANY4_OK, ANY4_EINVAL for a NULL id, ANY4_ECUDA if the stream cannot be
+ * queried.
+ */
+ANY4_API int any4_stream_capture_id(any4_stream_t stream, uint64_t* id);
+
 /* Static description of a status code (never NULL). */
 ANY4_API const char* any4_strerror(int status);
 

@@ -77,6 +77,8 @@ lib.any4_act_pack.argtypes = [_p, _c_int, _c_int, _c_int, _p, _p, _p]
 lib.any4_act_pack.restype = _c_int
 lib.any4_act_unpack.argtypes = [_p, _p, _c_int, _c_int, _c_int, _p, _p]
 lib.any4_act_unpack.restype = _c_int
+lib.any4_stream_capture_id.argtypes = [_p, ctypes.POINTER(ctypes.c_uint64)]
+lib.any4_stream_capture_id.restype = _c_int
 lib.any4_strerror.argtypes = [_c_int]
 lib.any4_strerror.restype = ctypes.c_char_p
 lib.any4_last_cuda_error.argtypes = []
@@ -88,7 +90,7 @@ EXPORTED = ("any4_packed_bytes", "any4_pack", "any4_dequant", "any4_linear_works
             "any4_pack_format", "any4_packed_bytes_bits", "any4_pack_bits", "any4_dequant_bits",
             "any4_linear_bits", "any4_lora_header_bytes", "any4_lora_workspace_bytes", "any4_linear_lora",
             "any4_lora_grad_workspace_bytes", "any4_linear_lora_grad", "any4_act_pack", "any4_act_unpack",
-            "any4_strerror", "any4_last_cuda_error")
+            "any4_stream_capture_id", "any4_strerror", "any4_last_cuda_error")
 
 ANY4_FORMAT_INT4, ANY4_FORMAT_NF4, ANY4_FORMAT_FP4 = 1, 2, 3
 FORMATS = {"int4": ANY4_FORMAT_INT4, "nf4": ANY4_FORMAT_NF4, "fp4": ANY4_FORMAT_FP4}
@@ -286,15 +288,59 @@ def _refused(bits: int, m: int, n: int, k: int, group: int) -> int:
     raise Any4Error(code if code == ANY4_ECUDA else ANY4_ESHAPE)
 
 
+@functools.lru_cache(maxsize=1024)   # a refusal is not kept: it may be a CUDA error that passes
+def _linear_need(device: int, *shape: int) -> int:
+    """any4_linear_workspace_bytes_bits of a shape (it depends on the device's SM count)."""
+    return lib.any4_linear_workspace_bytes_bits(*shape) or _refused(*shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_need(device: int, *shape: int) -> int:
+    return lib.any4_lora_workspace_bytes(*shape) or _refused(*shape[:5])
+
+
+@functools.lru_cache(maxsize=1024)
+def _grad_need(device: int, *shape: int) -> int:
+    return lib.any4_lora_grad_workspace_bytes(*shape) or _refused(*shape[:5])
+
+
+_HEADER_BYTES = lib.any4_lora_header_bytes()
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 _WORKSPACES: dict = {}
+_GRAPH_WORKSPACES: dict = {}
+
+
+def _zeroed(need: int, device: torch.device) -> torch.Tensor:
+    """A workspace with the zero header a first call asks for."""
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:_HEADER_BYTES].zero_()
+    return ws
+
+
+def _graph_workspace(need: int, device: torch.device, key: tuple) -> torch.Tensor:
+    """While stream key = (device, stream) is captured: a workspace of the graph's
+    own, whose header each replay clears once. Eager calls and other graphs may
+    run beside a replay, so it is shared with none of them; the reference kept
+    here serves the later calls of the same capture."""
+    capture = ctypes.c_uint64(0)
+    _check(lib.any4_stream_capture_id(key[1], ctypes.byref(capture)))
+    have = _GRAPH_WORKSPACES.get(key)
+    if have is None or have[0] != capture.value or have[1].numel() < need:
+        have = _GRAPH_WORKSPACES[key] = (capture.value, _zeroed(need, device))
+    return have[1]
 
 
 def workspace_for(m: int, n: int, k: int, group: int, device: torch.device, bits: int = 4) -> torch.Tensor:
     """A zero-initialised workspace for this stream, grown on demand and reused
-    by later calls on the same stream (calls on one stream never overlap)."""
-    need = lib.any4_linear_workspace_bytes_bits(bits, m, n, k, group) or _refused(bits, m, n, k, group)
+    by later calls on the same stream (calls on one stream never overlap), or,
+    while the stream is captured, by the later calls of that capture."""
     key = (device.index if device.index is not None else torch.cuda.current_device(),
            _stream(device))
+    need = _linear_need(key[0], bits, m, n, k, group)
+    if _capturing():
+        return _graph_workspace(need, device, key)
+    if _GRAPH_WORKSPACES:
+        _GRAPH_WORKSPACES.clear()   # a capture still under way makes itself another
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
         ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
@@ -428,10 +474,6 @@ def _typed(t: torch.Tensor, name: str, dtypes, device: torch.device, shape) -> i
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values, or their bit patterns
 _BYTES = (torch.uint8,)
 _INT8, _INT32, _FP32 = (torch.int8,), (torch.int32,), (torch.float32,)
-_HEADER_BYTES = lib.any4_lora_header_bytes()
-_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
-
-
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
@@ -452,31 +494,19 @@ def _on_device(name: str):
     return wrap
 
 
-@functools.lru_cache(maxsize=1024)   # a refusal is not kept: it may be a CUDA error that passes
-def _lora_need(device: int, *shape: int) -> int:
-    """any4_lora_workspace_bytes of a shape (it depends on the device's SM count)."""
-    return lib.any4_lora_workspace_bytes(*shape) or _refused(*shape[:5])
-
-
-@functools.lru_cache(maxsize=1024)
-def _grad_need(device: int, *shape: int) -> int:
-    return lib.any4_lora_grad_workspace_bytes(*shape) or _refused(*shape[:5])
-
-
 _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_bytes_bits(*shape))
 
 
-def _adapter_workspace(need: int, device: torch.device, kept: _Kept) -> torch.Tensor:
-    """A workspace with a zeroed header: the stream's, grown on demand, or, while
-    a CUDA graph is captured, one of the graph's own. Called with kept.lock held."""
+def _adapter_workspace(need: int, device: torch.device, stream: int, kept: _Kept) -> torch.Tensor:
+    """A workspace with a zeroed header: the stream's, grown on demand, or the
+    graph's that is captured. Called with kept.lock held."""
+    if _capturing():
+        return _graph_workspace(need, device, (device.index, stream))
+    if _GRAPH_WORKSPACES:
+        _GRAPH_WORKSPACES.clear()
     ws = kept.workspace
-    if not _capturing():
-        if ws is not None and ws.numel() >= need:
-            return ws
-        ws = kept.workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    ws[:_HEADER_BYTES].zero_()
+    if ws is None or ws.numel() < need:
+        ws = kept.workspace = _zeroed(need, device)
     return ws
 
 
@@ -535,7 +565,8 @@ def any4_linear_lora(x: torch.Tensor, packed: torch.Tensor, n: int, k: int, grou
     kept = _kept(dev.index, stream)
     with kept.lock:
         if workspace is None:
-            workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev, kept)
+            workspace = _adapter_workspace(_lora_need(dev.index, bits, m, n, k, group, ad[4], ad[5]), dev, stream,
+                                           kept)
         st = lib.any4_linear_lora(bits, x_p, w_p, m, n, k, group, *ad, out_p, u_p,
                                   _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(),
                                   stream)
@@ -595,7 +626,8 @@ def any4_linear_lora_grad(dy: torch.Tensor, x, u: torch.Tensor | None, packed: t
     kept = _kept(dev.index, stream)
     with kept.lock:
         if workspace is None:
-            workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev, kept)
+            workspace = _adapter_workspace(_grad_need(dev.index, bits, m, n, k, group, count, rank), dev, stream,
+                                           kept)
         _check(lib.any4_linear_lora_grad(
             bits, dy_p, x_p, codes_p, steps_p, x_group, u_p, w_p, m, n, k, group, *ad, dx_p, da_p, db_p,
             _typed(workspace, "workspace", _BYTES, dev, workspace.shape), workspace.numel(), stream))

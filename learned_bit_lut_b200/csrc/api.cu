@@ -196,6 +196,16 @@ int any4_linear_bits(int bits, const uint16_t* x, const void* packed, int m, int
   return e == cudaSuccess ? ANY4_OK : fail_cuda(e);
 }
 
+int any4_stream_capture_id(any4_stream_t stream, uint64_t* id) {
+  if (!id) return ANY4_EINVAL;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, &capture);
+  if (e != cudaSuccess) return fail_cuda(e);
+  *id = status == cudaStreamCaptureStatusNone ? 0 : (uint64_t)capture;
+  return ANY4_OK;
+}
+
 const char* any4_strerror(int status) {
   switch (status) {
     case ANY4_OK: return "ANY4_OK: success";

@@ -30,7 +30,7 @@ class Host:
 
     def __init__(self):
         self.stream = threading.local()
-        self.capturing = False
+        self.capturing, self.capture = False, 0
         self.need = HEADER + 4096
         self.calls = []
         self.during = lambda name, args: None   # what happens inside a library call
@@ -64,13 +64,18 @@ def host(monkeypatch):
         monkeypatch.setattr(_lib.lib, name, lambda *a: h.need)
     for name in ("any4_linear_lora", "any4_linear_lora_grad", "any4_linear", "any4_linear_bits"):
         monkeypatch.setattr(_lib.lib, name, h.library_call(name))
-    for cache in ("_WORKSPACES", "_KEPT"):
+    def capture_id(stream, out):
+        out._obj.value = h.capture if h.capturing else 0
+        return 0
+
+    monkeypatch.setattr(_lib.lib, "any4_stream_capture_id", capture_id)
+    for cache in ("_WORKSPACES", "_KEPT", "_GRAPH_WORKSPACES"):
         if hasattr(_lib, cache):
             monkeypatch.setattr(_lib, cache, {})
-    for size in (_lib._lora_need, _lib._grad_need):
+    for size in (_lib._linear_need, _lib._lora_need, _lib._grad_need):
         size.cache_clear()
     yield h
-    for size in (_lib._lora_need, _lib._grad_need):
+    for size in (_lib._linear_need, _lib._lora_need, _lib._grad_need):
         size.cache_clear()
 
 
@@ -151,3 +156,65 @@ def test_threads_on_their_own_streams_do_not_wait_for_each_other(host):
             call("lora")
 
     run_threads(lambda: job(1), lambda: job(2))
+
+
+# ---- workspaces of captured calls
+
+def test_capture_id_needs_a_place_for_it():
+    assert _lib.lib.any4_stream_capture_id(None, None) == _lib.ANY4_EINVAL
+
+WORKSPACE_AT = {"any4_linear_lora": -3, "any4_linear_lora_grad": -3, "any4_linear": -3, "any4_linear_bits": -3}
+
+
+def used(host):
+    """Addresses of the workspaces of the calls so far."""
+    return [args[WORKSPACE_AT[name]] for name, args in host.calls]
+
+
+KINDS = ["lora", "grad", "linear", "linear_bits", "decode"]
+
+
+def make(name):
+    return call("linear", m=4) if name == "decode" else call(name)
+
+
+@pytest.mark.parametrize("warm", [False, True])
+@pytest.mark.parametrize("name", KINDS)
+def test_a_graph_has_a_workspace_of_its_own(host, monkeypatch, name, warm):
+    """Not the stream's, which eager calls use beside a replay and which is freed
+    when it grows, nor another graph's; and it is not left to eager calls,
+    for which nothing has cleared it."""
+    held = []   # no address is used twice by chance
+    zeroed = _lib._zeroed
+    monkeypatch.setattr(_lib, "_zeroed", lambda *a: held.append(zeroed(*a)) or held[-1])
+    if warm:
+        make(name)
+    host.capturing, host.capture = True, 11
+    make(name), make(name)
+    host.capture = 12
+    make(name)
+    host.capturing = False
+    make(name), make(name)
+    at = used(host)[1:] if warm else used(host)
+    first, again, other, eager, later = at
+    assert first == again and eager == later and len({first, other, eager}) == 3
+    assert not warm or used(host)[0] == eager
+    assert not _lib._GRAPH_WORKSPACES   # graphs keep their memory themselves
+
+
+@pytest.mark.parametrize("name", KINDS)
+def test_a_graph_clears_its_workspace_before_the_first_call(host, name):
+    seen = []
+
+    def during(call_name, args):
+        at = args[WORKSPACE_AT[call_name]]
+        ws = next(w for _, w in _lib._GRAPH_WORKSPACES.values() if w.data_ptr() == at)
+        seen.append(int(ws[:HEADER].max()))
+
+    host.during, host.capturing, host.capture = during, True, 5
+    make(name)
+    host.need += 8192   # a larger call of the same graph
+    for size in (_lib._linear_need, _lib._lora_need, _lib._grad_need):
+        size.cache_clear()
+    make(name)
+    assert seen == [0, 0] and len(set(used(host))) == 2

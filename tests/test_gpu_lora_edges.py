@@ -305,3 +305,65 @@ def test_values_beyond_bf16_of_one_request_reach_no_other(m, order):
     assert bool(x.isinf().any())
     got = grads(c, (codes, steps), u, outputs=("da",))
     check(got[1], *c.grad_ref(x, u)[1], "da")
+
+
+# ---- graphs
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (4, 4096, 2048), (16, 4096, 4096), (40, 1024, 4096), (700, 1024, 4096)])
+def test_graphs_of_the_plain_layer_share_no_workspace(m, n, k):
+    """Captured without a call before, replayed in another order than captured,
+    at the same time, and beside eager calls on the stream of the capture."""
+    cases = [Case(m, n, k, 128, 4, 1, 8, "null", seed=s) for s in (81, 82)]
+    packed = [c.packed() for c in cases]
+    side, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in cases]
+    graphs, outs = [], []
+    for c, p in zip(cases, packed):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append([a4.any4_linear(c.x, p, *c.shape()) for _ in range(4)])
+        graphs.append(g)
+    graphs[1].replay()   # the second one first
+    torch.cuda.synchronize()
+    wants = [a4.any4_linear(c.x, p, *c.shape()) for c, p in zip(cases, packed)]
+    assert all(torch.equal(y, wants[1]) for y in outs[1])
+    for _ in range(10):
+        for ys in outs:
+            for y in ys:
+                y.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, others):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(side):
+            eager = [a4.any4_linear(cases[0].x, packed[0], *cases[0].shape()) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for ys, w in zip(outs, wants) for y in ys)
+        assert all(torch.equal(y, wants[0]) for y in eager)
+
+
+def test_one_graph_of_many_calls_clears_one_workspace():
+    """Calls of all kinds in one graph, the workspace growing on the way."""
+    cases = [Case(3, 528, 1024, 128, 4, 2, 24, "mixed", seed=83), Case(40, 272, 512, 128, 4, 3, 16, "mixed", seed=84),
+             Case(700, 1040, 1088, 64, 3, 6, 40, "holes", seed=85), Case(2, 528, 1024, 128, 4, 2, 24, "mixed", seed=86)]
+    packed, us = [c.packed() for c in cases], [inner(c) for c in cases]
+
+    def step(i):
+        c = cases[i]
+        args = (packed[i], *c.shape(), c.a, c.b, c.scale, c.ids)
+        return (a4.any4_linear_lora(c.x, *args, bits=c.bits), a4.any4_linear_bits(c.bits, c.x, packed[i], *c.shape()),
+                *a4.any4_linear_lora_grad(c.dy, c.x, us[i], *args, bits=c.bits))
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [step(i) for i in (0, 1, 2, 3, 1, 0)]
+    wants = [step(i) for i in (0, 1, 2, 3, 1, 0)]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, wants):
+            assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(got, want))
