@@ -306,8 +306,8 @@ def _grad_need(device: int, *shape: int) -> int:
 
 _HEADER_BYTES = lib.any4_lora_header_bytes()
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
-_WORKSPACES: dict = {}
-_GRAPH_WORKSPACES: dict = {}
+_WORKSPACES: dict = {}         # of decode calls, a few hundred KB, taken without a lock
+_GRAPH_WORKSPACES: dict = {}   # (device, stream): (capture, workspace) of captures under way
 
 
 def _zeroed(need: int, device: torch.device) -> torch.Tensor:
@@ -330,6 +330,16 @@ def _graph_workspace(need: int, device: torch.device, key: tuple) -> torch.Tenso
     return have[1]
 
 
+def _kept_workspace(need: int, device: torch.device, kept: _Kept) -> torch.Tensor:
+    """The stream's one workspace for calls of several kernels, which may hold a
+    whole dequantized weight; grown on demand. Called with kept.lock held."""
+    ws = kept.workspace
+    if ws is None or ws.numel() < need:
+        ws = kept.workspace = None   # free before the larger one is made
+        ws = kept.workspace = _zeroed(need, device)
+    return ws
+
+
 def workspace_for(m: int, n: int, k: int, group: int, device: torch.device, bits: int = 4) -> torch.Tensor:
     """A zero-initialised workspace for this stream, grown on demand and reused
     by later calls on the same stream (calls on one stream never overlap), or,
@@ -341,6 +351,10 @@ def workspace_for(m: int, n: int, k: int, group: int, device: torch.device, bits
         return _graph_workspace(need, device, key)
     if _GRAPH_WORKSPACES:
         _GRAPH_WORKSPACES.clear()   # a capture still under way makes itself another
+    if m > _DECODE_TOKENS:
+        kept = _kept(*key)
+        with kept.lock:
+            return _kept_workspace(need, device, kept)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
         ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
@@ -498,16 +512,13 @@ _packed_need = functools.lru_cache(maxsize=1024)(lambda *shape: lib.any4_packed_
 
 
 def _adapter_workspace(need: int, device: torch.device, stream: int, kept: _Kept) -> torch.Tensor:
-    """A workspace with a zeroed header: the stream's, grown on demand, or the
-    graph's that is captured. Called with kept.lock held."""
+    """The stream's workspace, or the graph's that is captured. Called with
+    kept.lock held."""
     if _capturing():
         return _graph_workspace(need, device, (device.index, stream))
     if _GRAPH_WORKSPACES:
         _GRAPH_WORKSPACES.clear()
-    ws = kept.workspace
-    if ws is None or ws.numel() < need:
-        ws = kept.workspace = _zeroed(need, device)
-    return ws
+    return _kept_workspace(need, device, kept)
 
 
 def _adapters(a, b, scale, ids, m: int, n: int, k: int, device: torch.device):

@@ -218,3 +218,15 @@ def test_a_graph_clears_its_workspace_before_the_first_call(host, name):
         size.cache_clear()
     make(name)
     assert seen == [0, 0] and len(set(used(host))) == 2
+
+
+def test_calls_of_several_kernels_share_the_stream_s_workspace(host):
+    """It may hold a whole dequantized weight, once; decode calls, which take no
+    lock, have a small one of their own."""
+    for name in ("linear", "lora", "grad", "linear_bits", "decode", "lora"):
+        make(name)
+    at = used(host)
+    assert len({at[i] for i in (0, 1, 2, 3, 5)}) == 1 and at[4] != at[0]
+    host.stream.at = 8
+    make("linear")
+    assert used(host)[-1] not in at
