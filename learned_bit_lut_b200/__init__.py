@@ -18,7 +18,8 @@ from ._lib import (ANY4_EALIGN, ANY4_ECUDA, ANY4_EINVAL, ANY4_ESHAPE, ANY4_EWORK
                    any4_packed_bytes, any4_quantize, any4_strerror, lib, workspace_for,
                    any4_packed_bytes_bits, any4_pack_bits, any4_dequant_bits, any4_linear_bits,
                    any4_linear_lora, any4_linear_lora_grad, any4_lora_workspace_bytes,
-                   any4_lora_grad_workspace_bytes, any4_act_pack, any4_act_unpack)
+                   any4_lora_grad_workspace_bytes, any4_act_pack, any4_act_unpack, workspace_status,
+                   reset_workspaces)
 
 __all__ = ["any4_quantize", "any4_pack", "any4_pack_bits", "any4_dequant_bits", "any4_linear_bits",
            "any4_packed_bytes_bits", "any4_pack_format", "any4_format_lut", "FORMATS", "ANY4_FORMAT_INT4",
@@ -26,4 +27,5 @@ __all__ = ["any4_quantize", "any4_pack", "any4_pack_bits", "any4_dequant_bits", 
            "any4_linear_workspace_bytes", "any4_linear_grid", "any4_linear_kernel", "KERNELS", "any4_strerror", "Any4Error", "workspace_for", "lib",
            "LIB_PATH", "EXPORTED", "ANY4_OK", "ANY4_EINVAL", "ANY4_EALIGN", "ANY4_ESHAPE",
            "ANY4_EWORKSPACE", "ANY4_ECUDA", "any4_linear_lora", "any4_linear_lora_grad",
-           "any4_lora_workspace_bytes", "any4_lora_grad_workspace_bytes", "any4_act_pack", "any4_act_unpack"]
+           "any4_lora_workspace_bytes", "any4_lora_grad_workspace_bytes", "any4_act_pack", "any4_act_unpack",
+           "workspace_status", "reset_workspaces"]

@@ -305,6 +305,7 @@ def _grad_need(device: int, *shape: int) -> int:
 
 
 _HEADER_BYTES = lib.any4_lora_header_bytes()
+_STATUS_AT = 65536 * 4   # the status word, behind the counters
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 _WORKSPACES: dict = {}         # of decode calls, a few hundred KB, taken without a lock
 _GRAPH_WORKSPACES: dict = {}   # (device, stream): (capture, workspace) of captures under way
@@ -416,6 +417,42 @@ def noalloc_status(device: torch.device | None = None) -> int:
         torch.cuda.synchronize(dev)
         word = torch.as_tensor(_DeviceWord(ptr.value), device=dev)
         return int(word.view(torch.int32).item()) & 0xFFFFFFFF
+
+
+def _workspaces_of(device: torch.device) -> list:
+    """The workspaces kept for a device's streams."""
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    found = [ws for key, ws in list(_WORKSPACES.items()) if key[0] == index]
+    for key, kept in list(_KEPT.items()):
+        if key[0] == index:
+            with kept.lock:
+                found += [] if kept.workspace is None else [kept.workspace]
+    return found
+
+
+def workspace_status(device: torch.device | None = None) -> int:
+    """The status of the calls that were given no workspace, on any stream of
+    ``device``: 0 if all completed; bit 0 is set once a bounded wait in a kernel
+    gave up, which leaves that call's outputs incomplete and the workspace unfit
+    for another call until reset_workspaces. Synchronizes the device. Graphs
+    that were captured without a workspace keep their status to themselves."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    torch.cuda.synchronize(dev)
+    status = 0
+    for ws in _workspaces_of(dev):
+        status |= int(ws[_STATUS_AT:_STATUS_AT + 4].view(torch.int32).item()) & 0xFFFFFFFF
+    return status
+
+
+def reset_workspaces(device: torch.device | None = None) -> None:
+    """Clears the counters and the status of the workspaces kept for ``device``,
+    as before their first use. Synchronizes the device, before and after: no call
+    may be made on it meanwhile."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    torch.cuda.synchronize(dev)
+    for ws in _workspaces_of(dev):
+        ws[:_HEADER_BYTES].zero_()
+    torch.cuda.synchronize(dev)
 
 
 def any4_quantize(w: torch.Tensor, ex: torch.Tensor, group: int, bits: int = 4,

@@ -230,3 +230,30 @@ def test_calls_of_several_kernels_share_the_stream_s_workspace(host):
     host.stream.at = 8
     make("linear")
     assert used(host)[-1] not in at
+
+
+# ---- after a wait that gave up
+
+@pytest.mark.parametrize("name", KINDS)
+def test_a_call_that_gave_up_is_seen_and_mended(host, monkeypatch, name):
+    """The kernels leave the status word set and counters behind, in a workspace
+    that the caller cannot see."""
+    import learned_bit_lut_b200 as a4
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    dev = torch.device("cuda", 0)
+    assert a4.workspace_status(dev) == 0
+    make(name)
+    host.stream.at = 9
+    make("lora")
+    assert a4.workspace_status(dev) == 0
+    broken = used(host)[0]
+    ws = next(w for w in _lib._workspaces_of(dev) if w.data_ptr() == broken)
+    ws[65536 * 4], ws[12] = 1, 3
+    assert a4.workspace_status(dev) == 1 and a4.workspace_status(torch.device("cuda", 1)) == 0
+    a4.reset_workspaces(torch.device("cuda", 1))
+    assert a4.workspace_status(dev) == 1
+    a4.reset_workspaces(dev)
+    assert a4.workspace_status(dev) == 0 and not bool(ws[:HEADER].any())
+    host.stream.at = 7
+    make(name)
+    assert used(host)[-1] == broken

@@ -367,3 +367,12 @@ def test_one_graph_of_many_calls_clears_one_workspace():
         torch.cuda.synchronize()
         for got, want in zip(outs, wants):
             assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(got, want))
+
+
+def test_status_of_the_kept_workspaces():
+    c = Case(700, 528, 1088, 64, 3, 6, 40, "holes", seed=87)
+    want = forward(c)
+    a4.any4_linear(c.x[:4].contiguous(), Case(4, 528, 1088, 64, 4, 1, 8, "null").packed(), *c.shape())
+    assert a4.workspace_status() == 0
+    a4.reset_workspaces()
+    assert torch.equal(forward(c), want) and a4.workspace_status(torch.device("cuda")) == 0
