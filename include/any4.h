@@ -382,7 +382,8 @@ ANY4_API int any4_linear_lora(int bits, const uint16_t* x, const void* packed, i
  *              checkpoint of any4_act_pack with groups of x_group columns.
  *              With a checkpoint, da is that of its any4_act_unpack values.
  *   u          [M][R] bf16 as any4_linear_lora wrote it (needed for db).
- *   packed, a  needed for dx; b for dx and da.
+ *   packed, a  needed for dx; b and scale for dx and da. What the asked outputs
+ *              do not need may be NULL.
  *   workspace  >= any4_lora_grad_workspace_bytes(...), as for any4_linear_lora.
  *              It holds W_hat in bf16 (N*K*2 bytes) while dx is computed.
  * Sums are fp32 in a fixed order: repeated calls give the same bits.

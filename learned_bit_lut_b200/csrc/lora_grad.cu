@@ -86,8 +86,10 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
                                    const int32_t* ids, int adapters, int rank, uint16_t* dx, uint16_t* da,
                                    uint16_t* db, void* workspace, size_t workspace_bytes, any4_stream_t stream) {
   using namespace any4;
-  if (!dy || !b || !scale || !workspace || (!dx && !da && !db)) return ANY4_EINVAL;
+  if (!dy || !workspace || (!dx && !da && !db)) return ANY4_EINVAL;
   if (dx && (!packed || !a)) return ANY4_EINVAL;
+  const bool need_v = dx || da;
+  if (need_v && (!b || !scale)) return ANY4_EINVAL;
   if (db && !u) return ANY4_EINVAL;
   const bool kept8 = x_codes != nullptr || x_steps != nullptr;
   if (da && (kept8 ? x != nullptr || !x_codes || !x_steps : x == nullptr)) return ANY4_EINVAL;   // one form of x
@@ -117,8 +119,8 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
                           {db ? u : nullptr, (size_t)m * rank * 2},
                           {dx ? packed : nullptr, L.total},
                           {dx ? a : nullptr, ab * k},
-                          {b, ab * n},
-                          {scale, adapters * sizeof(float)},
+                          {need_v ? b : nullptr, ab * n},
+                          {need_v ? scale : nullptr, adapters * sizeof(float)},
                           {ids, m * sizeof(int32_t)}};
   if (!disjoint(ranges, 4, sizeof(ranges) / sizeof(ranges[0]))) return ANY4_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -135,7 +137,7 @@ ANY4_API int any4_linear_lora_grad(int bits, const uint16_t* dy, const uint16_t*
     for (int i = 0; i < 3; ++i) term.lists[i] = slot_lists(ws + space.lists, m, 64 << i);
     e = launch_slot_lists(ad, m, ws + space.lists, st);
   }
-  if (e == cudaSuccess && (dx || da))
+  if (e == cudaSuccess && need_v)
     e = launch_down(true, dy, ad, m, n, k, pairs, nullptr, partials, counters, status, sms, ids != nullptr, st);
   if (e == cudaSuccess && dx) e = launch_dequant(static_cast<const uint8_t*>(packed), L, what, st, true);
   if (e == cudaSuccess && dx) e = launch_dx(dy, what, L, m, dx, partials, counters, status, sms, term, st);

@@ -376,3 +376,17 @@ def test_status_of_the_kept_workspaces():
     assert a4.workspace_status() == 0
     a4.reset_workspaces()
     assert torch.equal(forward(c), want) and a4.workspace_status(torch.device("cuda")) == 0
+
+
+def test_db_alone_needs_neither_b_nor_scale():
+    c = Case(150, 272, 320, 64, 4, 3, 24, "holes", seed=88)
+    u = inner(c)
+    want = grads(c, u=u, outputs=("db",))[2]
+    db, ws = torch.empty_like(want), torch.zeros(
+        a4.any4_lora_grad_workspace_bytes(c.m, *c.shape(), c.adapters, c.rank), dtype=torch.uint8, device="cuda")
+    assert a4.lib.any4_linear_lora_grad(4, c.dy.data_ptr(), None, None, None, 0, u.data_ptr(), None, c.m, *c.shape(), None,
+                                        None, None, c.ids.data_ptr(), c.adapters, c.rank, None, None, db.data_ptr(),
+                                        ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == a4.ANY4_OK
+    assert torch.equal(db, want)
+    # b is not read, so it may be what is written
+    assert torch.equal(grads(c, u=u, outputs=("db",), db=c.b)[2], want)
