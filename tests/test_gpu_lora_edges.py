@@ -390,3 +390,77 @@ def test_db_alone_needs_neither_b_nor_scale():
     assert torch.equal(db, want)
     # b is not read, so it may be what is written
     assert torch.equal(grads(c, u=u, outputs=("db",), db=c.b)[2], want)
+
+
+# ---- the trailing parts of u and v: with W_hat = 0 and factors that cancel the
+# leading parts, y, dx and dA are made of what rounding u and v to bf16 loses
+
+def nothing_of_the_weight(c: Case):
+    c.q.alpha[:], c.q.beta[:] = 0, 0
+    c._w = None
+    return c
+
+
+def limit_of(ref, bound):
+    return bound + 2.0 ** -8 * (ref.abs() + bound) + 1e-37
+
+
+def without_trailing_part(ref, bound, planted):
+    """The planted mistake (u or v rounded to bf16) is well outside the bound."""
+    assert float(((planted - ref).abs() > limit_of(ref, bound)).double().mean()) > 0.5
+
+
+@pytest.mark.parametrize("order", ["null", "mixed"])
+@pytest.mark.parametrize("m,rank", [(40, 16), (40, 72), (300, 8), (600, 40)])
+def test_trailing_parts_in_y(m, rank, order):
+    c = nothing_of_the_weight(Case(m, 272, 64, 64, 4, 1 if order == "null" else 3, rank, order, seed=91))
+    c.scale.fill_(1.0)
+    c.a[:, 1::2] = c.a[:, 0::2]
+    c.a[:, 1::2, 3] += 2.0 ** -6
+    c.b[:, :, 1::2] = -c.b[:, :, 0::2]
+    ref, bound = c.y_ref()
+    u, planted = c.u_ref()[0].to(torch.bfloat16).double(), torch.zeros_like(ref)
+    for l, t in enumerate(c.tokens):
+        planted[t] = u[t] @ c.b[l].double().T
+    without_trailing_part(ref, bound, planted)
+    check(forward(c), ref, bound, "y")
+
+
+@pytest.mark.parametrize("order", ["null", "mixed"])
+@pytest.mark.parametrize("m,rank", [(40, 16), (40, 72), (300, 8), (600, 40)])
+def test_trailing_parts_in_dx(m, rank, order):
+    c = nothing_of_the_weight(Case(m, 64, 320, 64, 4, 1 if order == "null" else 3, rank, order, seed=92))
+    c.scale.fill_(1.0)
+    c.b[:, :, 1::2] = c.b[:, :, 0::2]
+    c.b[:, 3, 1::2] += 2.0 ** -8
+    c.a[:, 1::2] = -c.a[:, 0::2]
+    u = torch.zeros(m, rank, dtype=torch.bfloat16, device="cuda")
+    ref, bound = c.grad_ref(c.x, u)[0]
+    v, planted = c.v_ref()[0].to(torch.bfloat16).double(), torch.zeros_like(ref)
+    for l, t in enumerate(c.tokens):
+        planted[t] = v[t] @ c.a[l].double()
+    without_trailing_part(ref, bound, planted)
+    check(grads(c, u=u, outputs=("dx",))[0], ref, bound, "dx")
+
+
+@pytest.mark.parametrize("kept", ["bf16", "8bit"])
+@pytest.mark.parametrize("m,adapters,rank", [(8, 1, 16), (40, 10, 16), (600, 150, 8), (130, 33, 72)])
+def test_trailing_parts_in_da(m, adapters, rank, kept):
+    c = Case(m, 64, 320, 64, 4, adapters, rank, "mixed", seed=93)
+    c.scale.fill_(1.0)
+    c.ids = torch.arange(m, device="cuda", dtype=torch.int32) // 4 % adapters   # two such pairs of tokens an adapter
+    c.tokens = [torch.nonzero(c.ids == l).flatten() for l in range(adapters)]
+    c.dy[1::2] = c.dy[0::2]
+    c.dy[1::2, 3] += 2.0 ** -9
+    c.x[1::2] = -c.x[0::2]
+    stored, x = c.x, c.x
+    if kept == "8bit":
+        stored = a4.any4_act_pack(c.x, 64)
+        x = a4.any4_act_unpack(*stored, 64)
+    u = torch.zeros(m, rank, dtype=torch.bfloat16, device="cuda")
+    ref, bound = c.grad_ref(x, u)[1]
+    v, planted = c.v_ref()[0].to(torch.bfloat16).double(), torch.zeros_like(ref)
+    for l, t in enumerate(c.tokens):
+        planted[l] = v[t].T @ x[t].double()
+    without_trailing_part(ref, bound, planted)
+    check(grads(c, stored, u, outputs=("da",))[1], ref, bound, "da")
