@@ -450,8 +450,9 @@ def reset_workspaces(device: torch.device | None = None) -> None:
     may be made on it meanwhile."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     torch.cuda.synchronize(dev)
-    for ws in _workspaces_of(dev):
-        ws[:_HEADER_BYTES].zero_()
+    with torch.inference_mode():   # a workspace may have been made in that mode
+        for ws in _workspaces_of(dev):
+            ws[:_HEADER_BYTES].zero_()
     torch.cuda.synchronize(dev)
 
 

@@ -257,3 +257,17 @@ def test_a_call_that_gave_up_is_seen_and_mended(host, monkeypatch, name):
     host.stream.at = 7
     make(name)
     assert used(host)[-1] == broken
+
+
+def test_workspaces_made_in_inference_mode_are_reset_outside_it(host, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    dev = torch.device("cuda", 0)
+    with torch.inference_mode():
+        for name in KINDS:
+            make(name)
+        for ws in _lib._workspaces_of(dev):
+            ws[65536 * 4] = 1
+    _lib.reset_workspaces(dev)
+    assert _lib.workspace_status(dev) == 0
+    for name in KINDS:
+        make(name)
