@@ -81,6 +81,10 @@ ANY4_API size_t any4_packed_bytes(int n, int k, int group);
  *   packed   output, packed_bytes >= any4_packed_bytes(n, k, group); 16-byte
  *            aligned. The layout is opaque and immutable once written; it may
  *            be read by any number of calls and streams.
+ *            any4_linear starts to read it while the kernel ahead of it on the
+ *            stream ends. Behind a pack that is in order. Whoever writes the
+ *            buffer with a kernel of their own (a copy between two tensors,
+ *            say) lets another kernel, a copy or an event come between.
  * Inputs need no particular alignment. Returns ANY4_OK or an error status.
  */
 ANY4_API int any4_pack(const uint8_t* idx_nib, const uint16_t* lut, const uint16_t* alpha,

@@ -146,6 +146,9 @@ __global__ void pack_scales_kernel(const uint16_t* __restrict__ alpha,
     if (r1 < (size_t)L.n) v |= (uint32_t)src[r1 * L.groups + grp] << 16;
     out[e] = v;
   }
+  // the pack's last kernel: the linear kernels read a packed weight before their
+  // wait for the kernel ahead, so these stores are out before the block ends
+  __threadfence();
 }
 
 // One thread per packed 32-bit word: 8 weights (two columns of four rows).

@@ -464,3 +464,16 @@ def test_trailing_parts_in_da(m, adapters, rank, kept):
         planted[l] = v[t].T @ x[t].double()
     without_trailing_part(ref, bound, planted)
     check(grads(c, stored, u, outputs=("da",))[1], ref, bound, "da")
+
+
+@pytest.mark.parametrize("m", [1, 8, 16, 40])
+def test_the_layer_right_behind_its_pack(m):
+    from gpu_util import to_dev
+    cases = [Case(m, 1024, 2048, 64, 4, 1, 8, "null", seed=s) for s in (94, 95)]
+    raw = [tuple(to_dev(t) for t in (c.q.idx_nib, c.q.lut, c.q.alpha, c.q.beta)) for c in cases]
+    wants = [a4.any4_linear(cases[0].x, c.packed(), *c.shape()) for c in cases]
+    packed, outs = torch.empty_like(cases[0].packed()), []
+    for i in range(60):
+        a4.any4_pack(*raw[i % 2], 64, packed)
+        outs.append(a4.any4_linear(cases[0].x, packed, *cases[0].shape()))
+    assert all(torch.equal(y, wants[i % 2]) for i, y in enumerate(outs))
