@@ -477,3 +477,73 @@ def test_the_layer_right_behind_its_pack(m):
         a4.any4_pack(*raw[i % 2], 64, packed)
         outs.append(a4.any4_linear(cases[0].x, packed, *cases[0].shape()))
     assert all(torch.equal(y, wants[i % 2]) for i, y in enumerate(outs))
+
+
+# ---- addresses and sizes at the borders of what is accepted
+
+def at_offset(t, count):
+    """A copy of t that starts `count` elements into a buffer."""
+    buf = torch.empty(t.numel() + count + 64, dtype=t.dtype, device=t.device)
+    view = buf[count:count + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("m,n,k,bits,rank", [(1, 1024, 2048, 4, 16), (7, 272, 1024, 4, 24), (16, 4096, 1024, 4, 8),
+                                             (40, 272, 1024, 4, 16), (300, 1040, 512, 4, 72), (600, 272, 320, 3, 8),
+                                             (2600, 2320, 2112, 4, 40)])
+def test_least_alignment(m, n, k, bits, rank):
+    """y on 4 bytes, scales and ids on 4, everything else on 16."""
+    c = Case(m, n, k, 64, bits, 3, rank, "holes", seed=96)
+    u0 = inner(c)
+    want, wants = forward(c), grads(c, u=u0)
+    packed = at_offset(c.packed(), 16)
+    y = at_offset(torch.zeros_like(want), 2)
+    assert y.data_ptr() % 16 == 4
+    x, dy, a, b, u = (at_offset(t, 8) for t in (c.x, c.dy, c.a, c.b, u0))
+    scale, ids = at_offset(c.scale, 1), at_offset(c.ids, 3)
+    size = max(f(m, n, k, 64, 3, rank, bits=bits) for f in (a4.any4_lora_workspace_bytes, a4.any4_lora_grad_workspace_bytes))
+    ws = at_offset(torch.zeros(size, dtype=torch.uint8, device="cuda"), 16)
+    assert {t.data_ptr() % 32 for t in (x, dy, a, b, u, packed, ws)} == {16}
+    got_u = at_offset(torch.zeros_like(u0), 8)
+    a4.any4_linear_lora(x, packed, n, k, 64, a, b, scale, ids, bits=bits, out=y, u=got_u, workspace=ws)
+    assert torch.equal(y, want)
+    outs = {"dx": at_offset(wants[0], 8), "da": at_offset(wants[1], 8), "db": at_offset(wants[2], 8)}
+    for t in outs.values():
+        t.zero_()
+    got = a4.any4_linear_lora_grad(dy, x, u, packed, n, k, 64, a, b, scale, ids, bits=bits, workspace=ws, **outs)
+    assert all(torch.equal(p, q) for p, q in zip(got, wants))
+    assert status(ws) == 0
+
+
+def test_as_many_tokens_as_are_accepted():
+    m = 1 << 20
+    c = Case(m, 16, 64, 64, 4, 5, 8, "holes", seed=97)
+    u = torch.empty(m, 8, dtype=torch.bfloat16, device="cuda")
+    check(forward(c, u=u), *c.y_ref(), "y")
+    check(u, *c.u_ref(), "u")
+    for kept in (c.x, a4.any4_act_pack(c.x, 64)):
+        x = c.x if kept is c.x else a4.any4_act_unpack(*kept, 64)
+        for name, g, ref in zip(("dx", "da", "db"), grads(c, kept, u), c.grad_ref(x, u)):
+            check(g, *ref, name)
+
+
+@pytest.mark.parametrize("m", [5, 300, 1100])
+def test_as_many_adapters_as_are_accepted(m):
+    """65536 adapters, of which a few have tokens, the first and the last among them."""
+    few = Case(m, 48, 64, 64, 4, 4, 8, "mixed", seed=98)
+    places = torch.tensor([0, 257, 32768, 65535], device="cuda")
+    many = {t: torch.randn(65536, *s, device="cuda").to(d) for t, s, d in (
+        ("a", (8, 64), torch.bfloat16), ("b", (48, 8), torch.bfloat16), ("scale", (), torch.float32))}
+    for name, t in many.items():
+        t[places] = getattr(few, name)
+    ids = places[few.ids.long()].to(torch.int32)
+    packed, u = few.packed(), inner(few)
+    y = a4.any4_linear_lora(few.x, packed, *few.shape(), many["a"], many["b"], many["scale"], ids)
+    check(y, *few.y_ref(), "y")
+    dx, da, db = a4.any4_linear_lora_grad(few.dy, few.x, u, packed, *few.shape(), many["a"], many["b"], many["scale"], ids)
+    for name, g, ref in zip(("dx", "da", "db"), (dx, da[places], db[places]), few.grad_ref(few.x, u)):
+        check(g, *ref, name)
+    others = torch.ones(65536, dtype=torch.bool, device="cuda")
+    others[places] = False
+    assert not bool(da[others].any()) and not bool(db[others].any())
