@@ -11,12 +11,11 @@
 // cluster of 8 thread blocks takes a token and a slice of its output rows, its
 // blocks share the R rows of A_l, exchange the sums through distributed
 // shared memory and share the output rows. The decode kernel is its
-// programmatic dependent, but one of its blocks fills an SM, so it follows
-// rather than overlaps (waiting for the term only before its stores measured
-// the same). B200: 1024 x 4096, one token, rank 16: both kernels 6.7 us back to
-// back (the layer alone 3.0); 4096 x 4096, 16 tokens, rank 16: 14.6 us (the
-// term 6.6); 14336 x 4096, 7 tokens, rank 64: 28 us (the term 9, 9.5 MB of A
-// and B).
+// programmatic dependent: it brings its first weights in beside it and waits for
+// its end before it reads x. B200: 1024 x 4096, one token, rank 16: both kernels
+// 6.5 us back to back (the layer alone 2.8); 4096 x 4096, 16 tokens, rank 16:
+// 14.4 us (the term 6.6); 14336 x 4096, 7 tokens, rank 64: 28 us (the term 9,
+// 9.5 MB of A and B).
 //
 // M > 16: the lists of the adapters in each token tile and u = s x . A^T on
 // the tensor cores (lora_down.cu), then the prefill GEMM with u . B^T as R

@@ -230,13 +230,15 @@ __global__ void dequant_bits_kernel(const uint8_t* __restrict__ packed, Layout L
 // one 32-byte run: the 4 lanes of a row write a 128-byte line. Codes of 3 and
 // 2 bits are first spread to the 4-bit words of the same steps. Same fp32 fma
 // and nearest-even rounding as dequant_kernel, so the same bits.
-// B200, 14336 x 4096: 34.9 us any4, 37 us any3, 36 us any2, about the rate at
+// B200, 14336 x 4096: 35.6 us any4, 37.8 us any3, 31.1 us any2, about the rate at
 // which 117 MB can be written (3.4 TB/s); by look-ups in shared memory any4 took 38.8
 // us, in global memory any3 took 4096 x 4096 in 93 us.
 constexpr int kDqWarps = 8;
 constexpr int kDqChunks = 4;   // chunks of a warp in a row: the tables are loaded once
-// With fewer blocks than this a warp takes one chunk (B200, any4: 1024 x 4096
-// 2.8 us, with four 5.6; 2048 x 4096 5.3 and 5.8; 4096 x 4096 is beyond it, 8.8).
+// With fewer blocks than this a warp takes one chunk (B200, any4, tables read
+// before the wait as the form beside another kernel does: 1024 x 4096 2.8 us, with
+// four 5.6; 2048 x 4096 5.3 and 5.8; 4096 x 4096 is beyond it, 8.8. With the
+// wait first 3.2, 5.9 and 9.6).
 constexpr int kDqFewBlocks = 256;
 
 // The 4-bit word of step s (a row-pair code per byte) from the lane's packed bits.
