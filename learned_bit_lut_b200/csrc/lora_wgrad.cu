@@ -23,9 +23,13 @@
 // For a chunk whose tokens do not all have one adapter the same warps build
 // z's tile: each token's values in the columns of its own adapter, zeros in
 // the others', so that one product serves all adapters of the block. They also
-// take infinities and NaN out of src, where 0 times them would be NaN; for the
-// columns and adapters they belong to the epilogue then sums anew in fp32. So
+// take infinities and NaN out of src, where 0 times them would be NaN (a one of
+// their sign stays: an infinite z times 0 would be NaN too), and mark the chunk;
+// the epilogue adds their products to the sums of their own token's adapter. So
 // a padding token's or another request's values reach no sum but their own.
+// Only marked chunks are gone through again, once for all of a block's sums
+// (B200, dA of 2^20 x 128, 2048 adapters of rank 64, one column of NaN: summing
+// that column's tokens anew per adapter took 34 s).
 //
 // Blocks: 128 columns of src x a share of the chunks x as many adapters as
 // one instruction holds (256 columns). Shares of the chunks are added by the
@@ -68,6 +72,8 @@ constexpr int kWgradSmem = 200 * 1024;
 static_assert(kMaxTokens / kTokens * 4 + 2 * (kABytes + 4 * 8192) + 2 * kRawBytes + kWgradFixed <= kWgradSmem, "stages");
 
 constexpr unsigned kMixed = 1u << 31;
+constexpr unsigned kSpoilt = 1u << 30;
+constexpr unsigned kAdapterBits = (1u << kMaxPass) - 1u;
 
 struct alignas(1024) WgradCtl {
   uint64_t a_full[kMaxAStages], a_empty[kMaxAStages];
@@ -123,23 +129,40 @@ __device__ __forceinline__ float src_value(const WgradParams& p, int t, int col)
   return __bfloat162float(__float2bfloat16_rn((float)(int8_t)__ldcg(p.codes + at) * step));
 }
 
-// Column col of adapter l, ranks r0 .. r0 + 15, where infinities or NaN of the
-// adapter's own tokens were taken out of src: the sum over its tokens anew.
+// The products that were taken out of the sums of the pass's adapters: those of
+// their own tokens' infinities and NaN, in the chunks where any were found. A
+// warp goes through them for its 32 columns (col is this lane's) and adds to the
+// sums in tensor memory; lanes whose value is finite leave theirs as they are.
 template <bool PAIRS>
-__device__ __noinline__ void spoilt_sums(const WgradParams& p, int c0, int c1, int l, int col, int r0, float (&sum)[16]) {
-  const int t0 = c0 * kTokens, t1 = min(p.m, c1 * kTokens);
-  bool own = false;
-  for (int t = t0; t < t1 && !own; ++t) own = adapter_of(p.ad, t) == l && !isfinite(src_value(p, t, col));
-  if (!own) return;
-  for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-  for (int t = t0; t < t1; ++t) {
-    if (adapter_of(p.ad, t) != l) continue;
-    const float s = src_value(p, t, col);
-    const uint16_t* z = p.z + (size_t)t * p.z_stride + r0;
-    for (int i = 0; i < 16 && r0 + i < p.ad.rank; ++i) {
-      float v = bf16_bits_to_float(__ldcg(z + i));
-      if (PAIRS) v += bf16_bits_to_float(__ldcg(z + p.r16 + i));
-      sum[i] += v * s;
+__device__ __noinline__ void add_spoilt(const WgradParams& p, const unsigned* info, int c0, int c1, int l_lo, int l_hi,
+                                        int col, uint32_t tlane) {
+  const int lane = threadIdx.x & 31;
+  for (int c = c0; c < c1; ++c) {
+    if (!(info[c - c0] & kSpoilt)) continue;
+    for (int t0 = c * kTokens; t0 < (c + 1) * kTokens; t0 += 32) {
+      const int l = t0 + lane < p.m ? adapter_of(p.ad, t0 + lane) : -1;
+      for (unsigned own = __ballot_sync(0xFFFFFFFFu, l >= l_lo && l < l_hi); own != 0; own &= own - 1) {
+        const int i = __ffs(own) - 1, t = t0 + i, g = __shfl_sync(0xFFFFFFFFu, l, i) - l_lo;
+        const float s = col < p.cols ? src_value(p, t, col) : 0.0f;
+        if (!__any_sync(0xFFFFFFFFu, !isfinite(s))) continue;
+        for (int r0 = 0; r0 < p.r16; r0 += 16) {
+          const uint32_t at = tlane + (uint32_t)(g * p.group_cols + r0);
+          uint32_t sum[16];
+          tc_ld_x16(at, sum);
+          tc_wait_ld();
+          const uint16_t* z = p.z + (size_t)t * p.z_stride + r0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (isfinite(s) || r0 + j >= p.ad.rank) continue;
+            float v = bf16_bits_to_float(__ldcg(z + j));
+            if (PAIRS) v += bf16_bits_to_float(__ldcg(z + p.r16 + j));
+            sum[j] = __float_as_uint(__uint_as_float(sum[j]) + v * s);
+          }
+          __syncwarp();
+          tc_st_x16(at, sum);
+          tc_wait_st();
+        }
+      }
     }
   }
 }
@@ -182,7 +205,8 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
   const int a_stages = p.a_stages, raw_stages = p.raw_stages;
   const uint32_t rbase = sbase + (uint32_t)(a_stages * kABytes), zbase = rbase + (uint32_t)(raw_stages * kRawBytes);
   WgradCtl* ctl = reinterpret_cast<WgradCtl*>(smem_raw + (zbase - raw) + (size_t)p.z_stages * p.z_stage);
-  // chunk c0 + i: bit g is adapter l_lo + g, kMixed: its tokens do not all have one adapter
+  // chunk c0 + i: bit g is adapter l_lo + g, kMixed: its tokens do not all have one adapter; the workers add
+  // kSpoilt where they take infinities or NaN out of src
   unsigned* info = reinterpret_cast<unsigned*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort_flag;
   // unit: column tile, then pass, then share of the chunks
@@ -328,7 +352,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         for (int kk = 0; kk < kTokens / 16; ++kk) tc_mma(d, ad + 128u * (uint64_t)kk, bd + 128u * (uint64_t)kk, id, 1u);
         tc_commit(smem_addr(&ctl->z_empty[zs]));
         tc_commit(smem_addr(&ctl->a_empty[s]));
-        touched |= in & ~kMixed;
+        touched |= in & kAdapterBits;
       }
       *(volatile unsigned*)&ctl->touched = touched;
       mbar_arrive_one(smem_addr(&ctl->acc_full));
@@ -361,6 +385,10 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
       return c < c1 && (info[c - c0] & kMixed) && t < p.m ? __ldcg(p.ad.ids + t) : -1;
     };
     int id_next = id_at(c0);
+    auto found_spoilt = [&](int c) {
+      atomicOr(&info[c - c0], kSpoilt);
+      *(volatile int*)&ctl->spoilt = 1;
+    };
     for (int c = c0; c < c1 && ok; ++c) {
       const unsigned in = info[c - c0];
       const bool mixed = in & kMixed;
@@ -404,14 +432,8 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         bool bad = false, huge = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t st = half ? step2nd : step;
-          if (mixed && (st & 0x7FFFu) >= kHugeStep) {
-            huge = true;
-            if ((st & 0x7F80u) == 0x7F80u) {   // a group that reads back as NaN
-              st = 0;
-              bad = true;
-            }
-          }
+          const uint32_t st = half ? step2nd : step;
+          huge |= mixed && (st & 0x7FFFu) >= kHugeStep;   // values may be infinite, or NaN as the step
           const uint32_t step2 = st | (st << 16);
           const uint4 q = lds128(rbase + (uint32_t)(rs * kRawBytes + token * 128 + (((run + 4 * half) ^ (token & 7)) << 4)));
           uint4 lo, hi;
@@ -425,9 +447,9 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         }
         if (huge)
           for (int i = 0; i < 4; ++i)   // this thread's four runs of 8 values
-            bad |= patch_finite<false>(abase + (uint32_t)((i >> 1) * (kABytes / 2) + token * 128 +
-                                                          (((2 * run + (i & 1)) ^ (token & 7)) << 4)));
-        if (bad) *(volatile int*)&ctl->spoilt = 1;
+            bad |= patch_finite(abase + (uint32_t)((i >> 1) * (kABytes / 2) + token * 128 +
+                                                   (((2 * run + (i & 1)) ^ (token & 7)) << 4)));
+        if (bad) found_spoilt(c);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -440,8 +462,8 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
         a_phase ^= 1u << s;
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kABytes / 16 / kWorkThreads; ++i) bad |= patch_finite<false>(abase + (uint32_t)(thread + i * kWorkThreads) * 16u);
-        if (bad) *(volatile int*)&ctl->spoilt = 1;
+        for (int i = 0; i < kABytes / 16 / kWorkThreads; ++i) bad |= patch_finite(abase + (uint32_t)(thread + i * kWorkThreads) * 16u);
+        if (bad) found_spoilt(c);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_one(smem_addr(&ctl->a_ready[s]));
@@ -464,7 +486,7 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
     if (!ctl->leave) {
       tc_fence_after();
       const unsigned touched = *(volatile unsigned*)&ctl->touched;
-      const int spoilt = *(volatile int*)&ctl->spoilt;
+      if (*(volatile int*)&ctl->spoilt) add_spoilt<PAIRS>(p, info, c0, c1, l_lo, l_hi, col, tlane);
       const size_t unit_floats = (size_t)p.per_pass * p.r16 * kCols;
       // PAIRS [adapter][rank][column], else [adapter][column][rank]: as the output's
       float* part = p.partials + (size_t)unit * unit_floats + (PAIRS ? row : row * p.r16);
@@ -487,14 +509,6 @@ __device__ __forceinline__ void wgrad_block(const CUtensorMap& smap, const CUten
               tc_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
-            }
-            if (spoilt && col < p.cols) {
-              float w[16];   // a copy: the call's argument lives in memory, v in registers
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = v[i];
-              spoilt_sums<PAIRS>(p, c0, c1, l, col, r0, w);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = w[i];
             }
             __syncwarp();
           }

@@ -304,10 +304,10 @@ __device__ __forceinline__ bool patch_tile(uint32_t tile, int steps, int thread)
     if (e >= 256 * steps) break;
     if (TRANS) {
       const int per_half = 128 * steps;
-      found |= patch_finite<true>(tile + (uint32_t)(e < per_half ? e * 16 : kAStageBytes / 2 + (e - per_half) * 16));
+      found |= patch_finite(tile + (uint32_t)(e < per_half ? e * 16 : kAStageBytes / 2 + (e - per_half) * 16));
     } else {
       const int row = e & 127, c = e >> 7;
-      found |= patch_finite<true>(tile + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
+      found |= patch_finite(tile + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
     }
   }
   return found;

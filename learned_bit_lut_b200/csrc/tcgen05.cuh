@@ -231,6 +231,14 @@ __device__ __forceinline__ void tc_zero_x32(uint32_t taddr) {
       "r"(0u)
       : "memory");
 }
+__device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -288,14 +296,13 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {   // 0xFFFF in eac
   return ~((bad >> 15) * 0xFFFFu);
 }
 
-// Takes the infinities and NaN out of the 16 bytes at addr, which become zeros
-// or, with ONES, ones of their sign; true if there were any.
-template <bool ONES>
+// Takes the infinities and NaN out of the 16 bytes at addr, which become ones of
+// their sign; true if there were any.
 __device__ __forceinline__ bool patch_finite(uint32_t addr) {
   const uint4 v = lds128(addr);
   const uint32_t a = finite_mask(v.x), b = finite_mask(v.y), c = finite_mask(v.z), d = finite_mask(v.w);
   const bool found = (a & b & c & d) != 0xFFFFFFFFu;
-  auto patched = [](uint32_t w, uint32_t m) { return ONES ? (w & (m | 0x80008000u)) | (~m & 0x3F803F80u) : w & m; };
+  auto patched = [](uint32_t w, uint32_t m) { return (w & (m | 0x80008000u)) | (~m & 0x3F803F80u); };
   if (found) sts128(addr, patched(v.x, a), patched(v.y, b), patched(v.z, c), patched(v.w, d));
   return found;
 }

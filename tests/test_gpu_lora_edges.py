@@ -547,3 +547,58 @@ def test_as_many_adapters_as_are_accepted(m):
     others = torch.ones(65536, dtype=torch.bool, device="cuda")
     others[places] = False
     assert not bool(da[others].any()) and not bool(db[others].any())
+
+
+# ---- infinities and NaN cost their own sums a little, and no other
+
+@pytest.mark.parametrize("kept", ["bf16", "8bit"])
+def test_a_column_of_nan_takes_no_longer_than_its_tokens(kept):
+    """2^20 tokens of 2048 mixed adapters: going through all tokens again for
+    each adapter and column took half a minute."""
+    tokens, adapters, rank, cols, n = 1 << 20, 2048, 64, 128, 16
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(tokens, cols, device="cuda", generator=gen).to(torch.bfloat16)
+    x[:, 5] = NAN
+    x[7, 9], x[9, 9], x[adapters + 9, 9] = INF, INF, -INF
+    dy = torch.randn(tokens, n, device="cuda", generator=gen).to(torch.bfloat16)
+    a = torch.zeros(adapters, rank, cols, dtype=torch.bfloat16, device="cuda")
+    b = torch.randn(adapters, n, rank, device="cuda", generator=gen).to(torch.bfloat16)
+    scale, ids = torch.ones(adapters, device="cuda"), torch.arange(tokens, device="cuda", dtype=torch.int32) % adapters
+    u = torch.zeros(tokens, rank, dtype=torch.bfloat16, device="cuda")
+    group = 64
+    stored = a4.any4_act_pack(x, group) if kept == "8bit" else x
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+    def call():
+        return a4.any4_linear_lora_grad(dy, stored, u, None, n, cols, group, a, b, scale, ids, outputs=("da",))[1]
+
+    call()
+    start.record()
+    da = call()
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 1000.0 and a4.workspace_status() == 0
+    xs = (a4.any4_act_unpack(*stored, group) if kept == "8bit" else x).double()
+    for l in (0, 7, 9, 1000, adapters - 1):
+        t = torch.arange(l, tokens, adapters, device="cuda")
+        v = dy[t].double() @ b[l].double()
+        ref = v.T @ xs[t]
+        bound = (n + 2) * 2.0 ** -23 * (dy[t].double().abs() @ b[l].double().abs()) + 2.0 ** -16 * v.abs()
+        bound = bound.T @ xs[t].abs() + (2 * len(t) + 8) * 2.0 ** -23 * (v.abs().T @ xs[t].abs())
+        check(da[l], ref, bound, f"da of {l}")
+
+
+@pytest.mark.parametrize("m,adapters,rank", [(40, 3, 24), (600, 3, 72), (1100, 40, 16), (3000, 5, 8)])
+@pytest.mark.parametrize("order", ["mixed", "holes"])
+def test_everything_not_finite(m, adapters, rank, order):
+    """All of x and dy NaN or infinite for two adapters and for tokens of none."""
+    c = Case(m, 272, 320, 64, 4, adapters, rank, order, seed=101)
+    for l, v in ((0, NAN), (adapters - 1, INF)):
+        c.x[c.tokens[l]], c.dy[c.tokens[l]] = v, v
+    others = torch.nonzero((c.ids < 0) | (c.ids >= adapters)).flatten()
+    c.x[others], c.dy[others] = NAN, -INF
+    u = inner(c)
+    for stored in (c.x, a4.any4_act_pack(c.x, 64)):
+        x = c.x if stored is c.x else a4.any4_act_unpack(*stored, 64)
+        for name, g, ref in zip(("dx", "da", "db"), grads(c, stored, u), c.grad_ref(x, u)):
+            check(g, *ref, name)
