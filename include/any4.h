@@ -194,7 +194,8 @@ ANY4_API int any4_linear_kernel(int bits, int m, int n, int k, int group);
  * shared memory) and adds them in a fixed order, so the result is
  * deterministic (every kernel adds in a fixed order; two calls of the same
  * shape on the same device give the same bits).
- * Every wait in the kernels is bounded (~2-4 s); if one gives up, the kernel
+ * Every wait in the kernels is bounded (~2-4 s, not counting the kernel ahead
+ * on the stream); if one gives up, the kernel
  * completes without hanging and the first 32-bit word of the workspace's
  * reserved area (byte offset 65536*4) is set non-zero. It is zero after
  * every normal call.

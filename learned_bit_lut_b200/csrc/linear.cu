@@ -427,6 +427,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1) linear_kernel(const Pa
       const int slot = issued % NS;
       const int n = min(kPieceChunks, cur.cend - cur.c);
       const uint32_t wbytes = (uint32_t)n * kCB;
+      if (issued == NS)   // slots are released once the consumers read x: the kernel before does not count as waiting
+        asm volatile("griddepcontrol.wait;" ::: "memory");
       if (issued >= NS)   // the consumer's release of the slot's previous use
         wait_bar(empty_bar(lane, slot), (uint32_t)(issued / NS - 1) & 1u, abort);
       if (*abort) break;

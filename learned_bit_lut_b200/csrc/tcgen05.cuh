@@ -46,18 +46,31 @@ __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// A wait's time is up. Its kernel may have started while the one ahead was still
+// running, and what it waits for may come when that one has ended, however long
+// that takes: the first time, a wait goes on from that end.
+static __device__ __noinline__ long long clock_after_kernel_ahead() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  return clock64();
+}
+
 // Bounded wait; false when the block is aborting or the wait timed out. The
 // waiting loop is a call, so that the path of a barrier that is ready stays
 // short: the issuing threads run from the instruction cache or not at all.
 static __device__ __noinline__ bool gemm_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  const long long t0 = clock64();
+  long long t0 = clock64();
+  bool again = false;
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kTcWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
+      if (again) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusWaitTimeout);
+        return false;
+      }
+      again = true;
+      t0 = clock_after_kernel_ahead();
     }
   }
 }
@@ -68,20 +81,28 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatil
 
 // gemm_wait for warps that wait long (a whole tile) and must not take issue
 // slots from the warps doing the work meanwhile: sleeps between polls.
-__device__ __forceinline__ bool gemm_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                               unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
+static __device__ __noinline__ bool gemm_wait_idle_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                        unsigned* status) {
+  long long t0 = clock64();
+  bool again = false;
   while (true) {
     __nanosleep(200);
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kTcWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
+      if (again) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusWaitTimeout);
+        return false;
+      }
+      again = true;
+      t0 = clock_after_kernel_ahead();
     }
   }
+}
+__device__ __forceinline__ bool gemm_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               unsigned* status) {
+  return mbar_try_wait(bar, parity) || gemm_wait_idle_loop(bar, parity, abort_flag, status);
 }
 
 __device__ __forceinline__ void tc_fence_before() {
@@ -138,6 +159,7 @@ __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
 // gemm_wait for arrivals from both blocks
 __device__ __forceinline__ bool gemm_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
   long long t0 = 0;
+  bool again = false;
   while (true) {
     uint32_t ok;
     asm volatile(
@@ -151,9 +173,13 @@ __device__ __forceinline__ bool gemm_wait_cluster(uint32_t bar, uint32_t parity,
     if (*abort_flag) return false;
     if (t0 == 0) t0 = clock64();
     if (clock64() - t0 > kTcWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
+      if (again) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusWaitTimeout);
+        return false;
+      }
+      again = true;
+      t0 = clock_after_kernel_ahead();
     }
   }
 }

@@ -43,3 +43,15 @@ def test_dequantization_reads_the_weight_behind_its_wait():
     text = code(os.path.join(CSRC, "pack_dequant.cu"))
     body = text[text.index("dequant_rows_kernel("):]
     assert body.index("griddepcontrol.wait") < re.search(r"ld_\w+\(|__ldg\(", body).start()
+
+
+def test_bounded_waits_do_not_count_the_kernel_before():
+    """A wait that begins while the kernel ahead still runs ends when that one
+    has; only then may its bound start."""
+    waits = code(os.path.join(CSRC, "tcgen05.cuh"))
+    assert waits.count("> kTcWaitCycles") == waits.count("t0 = clock_after_kernel_ahead()") == 3
+    restart = waits[waits.index("clock_after_kernel_ahead() {"):]
+    assert restart.index("griddepcontrol.wait") < restart.index("clock64()")
+    decode = code(os.path.join(CSRC, "linear.cu"))
+    producer = decode.index("if (warp == NW) {")
+    assert decode.index("griddepcontrol.wait", producer) < decode.index("wait_bar(", producer)
